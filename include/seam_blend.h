@@ -19,6 +19,11 @@
  *      model support", the PatchGroupNorm commits and the Patchify commit
  *      (first patches one band longer).
  *
+ *
+ * Beside them, operators of the transformer over latent tokens that makes the
+ * latents those tiles are decoded from: layer norm (forward and backward),
+ * rotary position embedding, and the gradient norm with clipping.
+ *
  * Conventions shared by every entry point
  *  - Pointers named "device" are HIP device pointers (any device memory the
  *    current device can read/write); everything else is host memory read
@@ -32,7 +37,8 @@
  *    available from seamblend_last_error().  Argument and geometry errors are
  *    detected on the host before anything is enqueued.  Faults during
  *    execution surface asynchronously on the stream, as for any HIP kernel.
- *  - Tensors are dense, contiguous, row-major (last index fastest).
+ *  - Tensors are dense, contiguous, row-major (last index fastest), except
+ *    where an entry point takes strides.
  */
 #ifndef SEAM_BLEND_H
 #define SEAM_BLEND_H
@@ -247,6 +253,107 @@ typedef enum {
 
 int vae_tile_layout(int64_t L, int rule, const int64_t params[4], int64_t max_tiles,
                     int64_t *origins, int64_t *extents, int64_t *n_tiles);
+
+/*
+ * Layer norm of rows of D elements (the transformer over latent tokens):
+ *   m = sum x / D, v = sum (x - m)^2 / D, r = 1 / sqrt(v + eps),
+ *   out = (x - m) r gamma + beta.
+ *   shape        {outer, inner, D}: outer * inner rows (< 2^31), D in 1..2^28.
+ *   *_stride     {outer, inner} strides in elements, 0..2^40; the D elements of a
+ *                row are contiguous.  Views of a packed projection need no copy.
+ *   gamma, beta  device pointers to [D] of weight_dtype, or NULL (1 and 0).
+ *   dtype        of x and out; weight_dtype: dtype, or SB_F32.
+ *   out          each element held once; x itself (same pointer and strides), or
+ *                sharing no element with it (checked; SB_EARG).
+ * Any element alignment is taken; 16-byte aligned rows are fastest.  Statistics
+ * are fp32 and corrected two-pass (sums about a first mean, then its rounding
+ * error taken out), so a mean that is large against the spread costs no
+ * accuracy; one rounding to dtype.  Deterministic.  No rows: no-op.
+ */
+int layer_norm_forward(const void *x, const int64_t x_stride[2], const int64_t shape[3], float eps,
+                       const void *gamma, const void *beta, int dtype, int weight_dtype, void *out,
+                       const int64_t out_stride[2], void *stream);
+
+/* Device workspace (bytes) layer_norm_backward needs; 0 with an error message
+ * for invalid arguments. */
+size_t layer_norm_backward_workspace_bytes(const int64_t shape[3], int dtype);
+
+/*
+ * Gradient of layer_norm_forward: with h = (x - m) r and g = dy gamma,
+ *   dx = r (g - mean(g) - h mean(g h)),
+ *   dgamma = sum over rows of dy h,  dbeta = sum over rows of dy.
+ * The statistics are formed again from x: nothing is kept from the forward
+ * pass.  dy, x, dx: rows as above; dx may be dy or x themselves, else it
+ * shares no element with them.  gamma: NULL for 1.  dgamma, dbeta: device
+ * pointers to [D] of weight_dtype, or NULL where not wanted; they are written,
+ * not added to (zeros without rows).  workspace: caller-owned device scratch,
+ * 16-byte aligned, contents need not be initialised.  Sums over rows are fp32
+ * in a fixed order.
+ */
+int layer_norm_backward(const void *dy, const int64_t dy_stride[2], const void *x, const int64_t x_stride[2],
+                        const int64_t shape[3], float eps, const void *gamma, int dtype, int weight_dtype,
+                        void *dx, const int64_t dx_stride[2], void *dgamma, void *dbeta, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* which elements of a head's rotated part make pair i of n */
+#define SB_ROTARY_HALF 0        /* i and i + n */
+#define SB_ROTARY_INTERLEAVED 1 /* 2i and 2i + 1 */
+
+/*
+ * Rotary position embedding of query heads and, in the same launch, key heads:
+ * pair i of every head of token t turns by a = position * freqs[i],
+ *   (u, v) -> scale (u cos a - v sin a, u sin a + v cos a),
+ * and the head's elements from rot_dim on are copied.  transpose != 0 turns by
+ * -a: the gradient of the forward call.
+ *   q, k         device tensors [B, T, heads, D]; q_heads or k_heads may be 0
+ *                (then its pointers and strides are not read).
+ *   shape        {B, T, D}: B * T < 2^31, D <= 2^16, at most 2^12 heads each.
+ *   *_stride     {B, T, head} strides in elements, 0..2^40; D is contiguous.
+ *   *_out        each element held once; q_out is q itself or shares no element
+ *                with q (k alike), and no output one with the other tensor's
+ *                input or output (SB_EARG).  Views of one packed projection are
+ *                told apart exactly; tensors of unlike strides whose memory
+ *                interleaves are refused.
+ *   freqs        device pointer to rot_dim / 2 doubles: radians per position.
+ *   positions    device pointer to 4- or 8-byte signed integers, strides
+ *                {axis, B, T} in elements (0 broadcasts).
+ *   sections     n_sections (1..4) pair counts that add up to rot_dim / 2:
+ *                consecutive pairs turn by the positions of axis 0, 1, ...
+ * The angle is formed and reduced in 64 bits, cosine and sine in fp32, one
+ * rounding to dtype.  No tokens or no heads: no-op.
+ */
+int rotary_apply(const void *q, const int64_t q_stride[3], void *q_out, const int64_t q_out_stride[3],
+                 int64_t q_heads, const void *k, const int64_t k_stride[3], void *k_out,
+                 const int64_t k_out_stride[3], int64_t k_heads, const int64_t shape[3], int dtype,
+                 const double *freqs, int64_t rot_dim, int layout, const void *positions, int position_bytes,
+                 const int64_t position_stride[3], const int64_t *sections, int n_sections, float scale,
+                 int transpose, void *stream);
+
+/* Device workspace (bytes) of grad_norm and grad_norm_clip for n tensors of
+ * these element counts; 0 with an error message for invalid arguments. */
+size_t grad_norm_workspace_bytes(const int64_t *numels, int64_t n);
+
+/*
+ * norm = sqrt(sum of g^2 over every element of n tensors), written to a device
+ * float.  grads: host array of device pointers, each to numels[k] contiguous
+ * elements of dtypes[k] (not read where numels[k] == 0); at most 2^20 tensors
+ * and 2^44 elements.  Squares are formed and summed in 64 bits, in a fixed
+ * order.  workspace: device scratch, 16-byte aligned.
+ */
+int grad_norm(const void *const *grads, const int64_t *numels, const int *dtypes, int64_t n, float *norm,
+              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * grad_norm, and every gradient times c = min(1, max_norm / (norm + eps)): in
+ * place where outs is NULL, else into outs[k] of out_dtypes[k] (dtypes[k], or
+ * SB_F32), which is the gradient itself or shares no memory with any gradient
+ * (checked against its own).  In place nothing is written when c is 1.  A norm
+ * that is NaN or infinite scales by NaN or 0, as the formula says; the host is
+ * not told (no synchronisation).  max_norm >= 0.
+ */
+int grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *numels, const int *dtypes,
+                   const int *out_dtypes, int64_t n, float max_norm, float eps, float *norm, void *workspace,
+                   size_t workspace_bytes, void *stream);
 
 /* Thread-local message describing the last non-zero return on this thread. */
 const char *seamblend_last_error(void);

@@ -1,10 +1,12 @@
 """MI355X (gfx950) tiled-VAE decode assembly: blend + crop + stitch of
-overlapping decoded tiles, and patch-split GroupNorm.
+overlapping decoded tiles, and patch-split GroupNorm; and operators of the
+transformer over latent tokens: layer norm, rotary position embedding, gradient
+norm and clipping.
 
 This module is the thin Python binding of ``libseamblend.so`` (C ABI in
 ``include/seam_blend.h``): it turns torch tensors into pointers, sizes and the
 current HIP stream and calls the library.  PyTorch is used for device memory
-and streams only; every step of both operations runs in the library's HIP
+and streams only; every step of every operation runs in the library's HIP
 kernels.  There is no CPU fallback: importing this package fails if the
 library has not been built, and every call requires GPU tensors.
 """
@@ -19,6 +21,9 @@ import torch
 __all__ = ["vae_tile_layout", "LAYOUT_RULES", "vae_tile_ramp_blend", "RampBlend", "vae_tile_blend_stitch", "vae_tile_blend_stitch_output_extents", "BlendStitch",
            "patch_groupnorm", "patch_groupnorm_workspace_bytes", "PatchGroupNorm",
            "patch_groupnorm_noalloc", "GN_STATIC_SCRATCH_BYTES",
+           "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes", "LayerNorm",
+           "LayerNormBackward", "rotary", "rotary_backward", "rotary_frequencies", "Rotary",
+           "grad_norm", "grad_norm_clip", "GradNormClip",
            "SeamBlendError", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libseamblend.so")
@@ -396,3 +401,10 @@ def patch_groupnorm_noalloc(x: torch.Tensor, groups: int, split_axis: int, n_pat
     if rc != 0:
         raise SeamBlendError(rc, "patch_groupnorm_noalloc")
     return out
+
+
+# the transformer's operators (each module declares its own entry points on _lib)
+from ._layer_norm import (LayerNorm, LayerNormBackward, layer_norm, layer_norm_backward,  # noqa: E402
+                        layer_norm_backward_workspace_bytes)
+from ._rotary import Rotary, rotary, rotary_backward, rotary_frequencies  # noqa: E402
+from ._grad_clip import GradNormClip, grad_norm, grad_norm_clip  # noqa: E402

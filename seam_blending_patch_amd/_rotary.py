@@ -1,0 +1,169 @@
+"""Rotary position embedding (``rotary_apply`` of ``include/seam_blend.h``) and
+the frequencies it turns by."""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Sequence, Tuple, Union
+
+import torch
+
+from . import _DTYPE, _check, _lib, _stream_ptr
+
+_i64 = ctypes.c_int64
+_i64p = ctypes.POINTER(_i64)
+_ptr = ctypes.c_void_p
+_lib.rotary_apply.argtypes = [_ptr, _i64p, _ptr, _i64p, _i64, _ptr, _i64p, _ptr, _i64p, _i64, _i64p, ctypes.c_int,
+                              _ptr, _i64, ctypes.c_int, _ptr, ctypes.c_int, _i64p, _i64p, ctypes.c_int,
+                              ctypes.c_float, ctypes.c_int, _ptr]
+_lib.rotary_apply.restype = ctypes.c_int
+_3 = _i64 * 3
+_NONE = _3(0, 0, 0)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       original_length: int = 0, low_turns: float = 1.0, high_turns: float = 32.0,
+                       sections: Optional[Sequence[int]] = None, device="cuda") -> Tuple[torch.Tensor, float]:
+    """Radians per position of the rot_dim / 2 pairs (float64 tensor on
+    ``device``), and the factor for ``scale``.
+
+    Pair i of n turns by ``base ** (-i / n)``; with ``sections`` (pair counts, one
+    for each position axis) every section has a ladder of its own.  ``scaling``
+    for contexts ``factor`` times longer:
+      "linear"    f / factor (positions interpolated);
+      "base"      base * factor ** (n / (n - 1)): the last pair is slowed by
+                  factor, the first not at all;
+      "by_parts"  pairs that turn more than high_turns times over
+                  original_length are kept, those below low_turns slowed by
+                  factor, those between mixed linearly in their turns; the
+                  factor for ``scale`` is 0.1 ln(factor) + 1.
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    parts = (rot_dim // 2,) if sections is None else tuple(int(n) for n in sections)
+    if any(n < 0 for n in parts) or sum(parts) != rot_dim // 2:
+        raise ValueError("sections must add up to rot_dim / 2 pairs")
+    if scaling == "base" and any(n == 1 for n in parts):
+        raise ValueError("base scaling needs at least two pairs in a section")
+    if scaling == "by_parts" and not (original_length > 0 and high_turns > low_turns):
+        raise ValueError("by_parts scaling needs original_length > 0 and high_turns > low_turns")
+    ladders = []
+    for n in parts:
+        b = base * factor ** (n / (n - 1)) if scaling == "base" and n else base
+        ladders.append(b ** (-torch.arange(n, dtype=torch.float64) / max(n, 1)))
+    f = torch.cat(ladders)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        turns = original_length * f / (2 * math.pi)
+        keep = ((turns - low_turns) / (high_turns - low_turns)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return f.to(device), scale
+
+
+def _heads(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU (HIP) tensor")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [B, T, heads, D] or [T, heads, D]")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device or t.dim() != like.dim()
+                             or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]):
+        raise ValueError(f"{name} must match q in all but its heads")
+
+
+def _strides(t: torch.Tensor):
+    s = t.stride()
+    return _3(*s[:3]) if len(s) == 4 else _3(0, s[0], s[1])
+
+
+class Rotary:
+    """A prepared rotation over fixed tensors (arguments validated and outputs
+    allocated once).  See rotary for the arguments; ``transpose`` turns by the
+    negative angles."""
+
+    def __init__(self, q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+                 k: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 sections: Optional[Sequence[int]] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, transpose: bool = False):
+        _heads(q, "q")
+        dev, dim = q.device, q.dim()
+        batch, length = (q.shape[0], q.shape[1]) if dim == 4 else (1, q.shape[0])
+        if not isinstance(freqs, torch.Tensor) or freqs.device != dev or freqs.dtype != torch.float64 \
+                or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise ValueError("freqs must be a contiguous 1-D float64 tensor on q's device")
+        if not isinstance(positions, torch.Tensor) or positions.device != dev \
+                or positions.dtype not in (torch.int64, torch.int32):
+            raise ValueError("positions must be an int64 or int32 tensor on q's device")
+        parts = (freqs.numel(),) if sections is None else tuple(int(n) for n in sections)
+        p = positions if sections is not None else positions.unsqueeze(0)
+        if p.dim() not in (2, 3) or p.shape[0] != len(parts) or p.shape[-1] != length \
+                or (p.dim() == 3 and p.shape[1] not in (1, batch)):
+            raise ValueError("positions must be [T] or [B, T], with a leading axis for sections")
+        ps = p.stride()
+        pos_strides = _3(ps[0], ps[1] if p.dim() == 3 and p.shape[1] > 1 else 0, ps[-1])
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _heads(out, "out", q)
+            if out.shape != q.shape:
+                raise ValueError("out must match q")
+        k_args = (None, _NONE, None, _NONE, 0)
+        if k is not None:
+            _heads(k, "k", q)
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            else:
+                _heads(k_out, "k_out", k)
+                if k_out.shape != k.shape:
+                    raise ValueError("k_out must match k")
+            k_args = (k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out), k.shape[-2])
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        self.out, self.device = (out if k is None else (out, k_out)), dev
+        self._keep = (q, k, positions, freqs)
+        self._args = (q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), q.shape[-2], *k_args,
+                      _3(batch, length, q.shape[-1]), _DTYPE[q.dtype], freqs.data_ptr(), 2 * freqs.numel(),
+                      int(bool(interleaved)), p.data_ptr(), p.element_size(), pos_strides,
+                      (_i64 * len(parts))(*parts), len(parts), scale, int(bool(transpose)))
+
+    def __call__(self) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
+        _check(_lib.rotary_apply(*self._args, _stream_ptr(self.device)), "rotary_apply")
+        return self.out
+
+
+def rotary(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, k: Optional[torch.Tensor] = None,
+           interleaved: bool = False, sections: Optional[Sequence[int]] = None, scale: float = 1.0,
+           out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Rotary position embedding of the heads of q, and of k in the same launch:
+    [B, T, heads, D] or [T, heads, D] GPU tensors of one dtype, the last axis
+    contiguous, the others strided as they come.  The first 2 * len(freqs)
+    elements of every head turn in pairs (neighbours where ``interleaved``, else
+    the two halves) by position * freqs (float64, see rotary_frequencies), times
+    ``scale``; the rest is copied.  positions: int64 or int32 [T] or [B, T];
+    with ``sections`` (pair counts) a leading axis holds the positions each
+    section turns by.  ``out`` / ``k_out`` may be ``q`` / ``k``.  Returns the
+    turned q, or (q, k)."""
+    plan = Rotary(q, positions, freqs, k, interleaved, sections, scale, out, k_out)
+    with torch.cuda.device(plan.device):
+        return plan()
+
+
+def rotary_backward(dq: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+                    k: Optional[torch.Tensor] = None, interleaved: bool = False,
+                    sections: Optional[Sequence[int]] = None, scale: float = 1.0,
+                    out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Gradient of rotary: the gradients of its outputs (dq, and k's as ``k``)
+    turned back.  Arguments as rotary's."""
+    plan = Rotary(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, transpose=True)
+    with torch.cuda.device(plan.device):
+        return plan()

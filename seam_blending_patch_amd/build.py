@@ -9,6 +9,7 @@ Every source is compiled for gfx950 only, with:
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -17,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libseamblend.so")
-SOURCES = ["abi.cpp", "layout.cpp", "ramp.cpp", "blend_stitch.hip", "groupnorm.hip", "ramp_blend.hip"]
+SOURCES = ["abi.cpp", "layout.cpp", "ramp.cpp", "blend_stitch.hip", "groupnorm.hip", "ramp_blend.hip",
+           "layer_norm.cpp", "layer_norm.hip", "rotary.cpp", "rotary.hip", "grad_clip.cpp", "grad_clip.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=off",
@@ -29,9 +31,9 @@ def build(verbose: bool = False) -> str:
     """Compile every source and link the shared library (always rebuilds)."""
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
+
+    def compile_one(src: str) -> str:
+        obj = os.path.join(objdir, src + ".o")
         cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -39,7 +41,10 @@ def build(verbose: bool = False) -> str:
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError(f"hipcc failed on {src}")
-        objs.append(obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,144 @@
+// grad_clip.cpp -- host side of grad_norm and grad_norm_clip: argument checks,
+// the split of the tensors into chunks, and launches of at most kClipTensors
+// tensors whose table travels as a kernel argument (no copy to the device, so
+// the calls can be captured in a graph).  No device memory is allocated and the
+// stream is never synchronised.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "sb_host.h"
+#include "sb_transformer.h"
+
+using sb::failf;
+
+namespace {
+
+constexpr int64_t kMaxTensors = 1 << 20;
+constexpr int64_t kMaxElements = (int64_t)1 << 44; // over all tensors
+
+struct ClipPlan {
+  int64_t chunk, chunks;
+};
+
+int plan_clip(const int64_t *numels, int64_t n, ClipPlan &p) {
+  if (n < 0 || n > kMaxTensors) return failf(SB_EGEOM, "0..2^20 tensors (got %lld)", (long long)n);
+  if (n > 0 && !numels) return failf(SB_EARG, "null element counts");
+  int64_t total = 0;
+  for (int64_t k = 0; k < n; ++k) {
+    if (numels[k] < 0) return failf(SB_EARG, "tensor %lld: negative element count", (long long)k);
+    if (numels[k] > kMaxElements - total) return failf(SB_EGEOM, "more than 2^44 elements");
+    total += numels[k];
+  }
+  // chunks of 16384 elements, longer where that would be more than 4096 of them
+  constexpr int64_t step = sb::kClipThreads * 8;
+  p.chunk = std::max<int64_t>(16384, (total / 4096 + step - 1) / step * step);
+  p.chunks = 0;
+  for (int64_t k = 0; k < n; ++k) p.chunks += (numels[k] + p.chunk - 1) / p.chunk;
+  return SB_OK;
+}
+
+int clip_call(const void *const *grads, void *const *outs, const int64_t *numels, const int *dtypes,
+              const int *out_dtypes, int64_t n, bool scale, float max_norm, float eps, float *norm, void *workspace,
+              size_t workspace_bytes, void *stream) {
+  ClipPlan p;
+  int rc = plan_clip(numels, n, p);
+  if (rc) return rc;
+  if (!norm || !sb::aligned(norm, 4)) return failf(SB_EARG, "norm must be a 4-byte aligned device pointer");
+  if (scale && !(max_norm >= 0.0f)) return failf(SB_EARG, "max_norm must be >= 0");
+  if (scale && (!(eps >= 0.0f) || eps == __builtin_inff())) return failf(SB_EARG, "eps must be finite and >= 0");
+  if (n > 0 && (!grads || !dtypes || (outs && !out_dtypes))) return failf(SB_EARG, "null tensor table");
+  for (int64_t k = 0; k < n; ++k) {
+    if (!sb::known_dtype(dtypes[k])) return failf(SB_EARG, "tensor %lld: unknown dtype %d", (long long)k, dtypes[k]);
+    if (outs && out_dtypes[k] != dtypes[k] && out_dtypes[k] != SB_F32)
+      return failf(SB_EARG, "tensor %lld: the output must be of the gradient's dtype or fp32", (long long)k);
+    if (numels[k] == 0) continue;
+    if (!grads[k] || !sb::aligned(grads[k], sb::elem_bytes(dtypes[k])))
+      return failf(SB_EARG, "gradient %lld is null or not aligned to its element size", (long long)k);
+    if (!outs) continue;
+    if (!outs[k] || !sb::aligned(outs[k], sb::elem_bytes(out_dtypes[k])))
+      return failf(SB_EARG, "output %lld is null or not aligned to its element size", (long long)k);
+    const uintptr_t g = (uintptr_t)grads[k], o = (uintptr_t)outs[k];
+    const uintptr_t gn = (uintptr_t)(numels[k] * sb::elem_bytes(dtypes[k]));
+    const uintptr_t on = (uintptr_t)(numels[k] * sb::elem_bytes(out_dtypes[k]));
+    if (!(g == o && dtypes[k] == out_dtypes[k]) && g < o + on && o < g + gn)
+      return failf(SB_EARG, "output %lld overlaps its gradient without being it", (long long)k);
+  }
+  if (!workspace || !sb::aligned(workspace, 16)) return failf(SB_EARG, "workspace must be 16-byte aligned device memory");
+  const size_t need = (size_t)std::max<int64_t>(p.chunks, 2) * sizeof(double);
+  if (workspace_bytes < need)
+    return failf(SB_EWORKSPACE, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+
+  sb::ClipArgs a;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t done = 0, k = 0;
+    bool first = true;
+    while (k < n) {
+      std::memset(&a, 0, sizeof a);
+      a.chunk = p.chunk;
+      a.max_norm = max_norm;
+      a.eps = eps;
+      uint32_t c = 0;
+      while (k < n && a.tensors < sb::kClipTensors) {
+        if (numels[k] > 0) {
+          const int t = a.tensors++;
+          a.in[t] = grads[k];
+          a.out[t] = outs ? outs[k] : const_cast<void *>(grads[k]);
+          a.n[t] = numels[k];
+          a.begin[t] = c;
+          a.types[t] = (uint8_t)(dtypes[k] | (outs ? out_dtypes[k] : dtypes[k]) << 2);
+          c += (uint32_t)((numels[k] + p.chunk - 1) / p.chunk);
+        }
+        ++k;
+      }
+      if (a.tensors == 0) break;
+      a.begin[a.tensors] = c;
+      hipError_t e;
+      if (pass == 0) {
+        a.partials = (double *)workspace + done;
+        e = sb_launch_square_sums(a, c, (hipStream_t)stream);
+      } else {
+        a.partials = (double *)workspace;
+        a.npartials = (int32_t)p.chunks;
+        a.norm = first ? norm : nullptr;
+        e = sb_launch_clip(a, c, (hipStream_t)stream);
+      }
+      if (e != hipSuccess) return failf(SB_ELAUNCH, "gradient norm launch failed: %s", hipGetErrorString(e));
+      done += c;
+      first = false;
+    }
+    if (pass == 0 && (!scale || p.chunks == 0)) { // the norm alone
+      std::memset(&a, 0, sizeof a);
+      a.partials = (double *)workspace;
+      a.npartials = (int32_t)p.chunks;
+      a.norm = norm;
+      const hipError_t e = sb_launch_clip(a, 1, (hipStream_t)stream);
+      if (e != hipSuccess) return failf(SB_ELAUNCH, "gradient norm launch failed: %s", hipGetErrorString(e));
+      break;
+    }
+  }
+  return SB_OK;
+}
+
+} // namespace
+
+extern "C" size_t grad_norm_workspace_bytes(const int64_t *numels, int64_t n) {
+  ClipPlan p;
+  if (plan_clip(numels, n, p)) return 0;
+  return (size_t)std::max<int64_t>(p.chunks, 2) * sizeof(double);
+}
+
+extern "C" int grad_norm(const void *const *grads, const int64_t *numels, const int *dtypes, int64_t n, float *norm,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+  return clip_call(grads, nullptr, numels, dtypes, nullptr, n, false, 0.0f, 0.0f, norm, workspace, workspace_bytes,
+                   stream);
+}
+
+extern "C" int grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *numels, const int *dtypes,
+                              const int *out_dtypes, int64_t n, float max_norm, float eps, float *norm,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+  return clip_call(grads, outs, numels, dtypes, out_dtypes, n, true, max_norm, eps, norm, workspace, workspace_bytes,
+                   stream);
+}

@@ -1,0 +1,233 @@
+// layer_norm.hip -- layer norm, forward and backward, gfx950.
+//
+// Rows of D elements: m = sum x / D, v = sum (x - m)^2 / D,
+// r = 1 / sqrt(v + eps), h = (x - m) r, y = h gamma + beta.  With
+// g = dy gamma the gradient is
+//   dx = r (g - mean(g) - h mean(g h)),
+//   dgamma = sum over rows of dy h,  dbeta = sum over rows of dy.
+//
+// Statistics are fp32 and corrected two-pass: m0 = sum x / D rounded, then
+// over d = x - m0 both e = sum d / D and sum d^2, so that v = sum d^2 / D - e^2
+// and x - m = d - e.  e is of the size of m0's rounding error, so nothing
+// cancels, and a mean that is large against the spread costs no accuracy.
+// The backward pass forms the statistics again from the rows it reads anyway:
+// nothing has to be kept from the forward pass.
+
+#include "sb_row.h"
+#include "sb_transformer.h"
+
+#include <algorithm>
+
+namespace sb {
+
+__device__ __forceinline__ int64_t row_offset(uint32_t row, const FastDiv &inner, const RowStride &s) {
+  const uint32_t o = fdiv(row, inner);
+  return (int64_t)o * s.o + (int64_t)(row - o * inner.d) * s.i;
+}
+
+// ---------------------------------------------------------------------------
+// Rows of any length: one block a row, looping over it (three times forward,
+// the second and third from cache).
+// ---------------------------------------------------------------------------
+constexpr int kLoopWaves = kLNThreads / 64;
+
+// m0 of the row, then whatever `f` adds up over d = x - m0
+template <int DT, int K, int N, class F>
+__device__ __forceinline__ float row_loop(const void *x, int64_t xo, int D, float inv_d, float (&lds)[2][N],
+                                          int &turn, float (&sums)[K], F f) {
+  constexpr int V = kVec<DT>;
+  float s[1] = {0.f};
+  for (int e = threadIdx.x * V; e < D; e += kLNThreads * V) {
+    float v[V];
+    load_floats<DT, V>(x, xo + e, D - e, v);
+#pragma unroll
+    for (int k = 0; k < V; ++k) s[0] += v[k];
+  }
+  block_sum<1, kLoopWaves>(s, lds, turn);
+  const float m0 = s[0] * inv_d;
+#pragma unroll
+  for (int k = 0; k < K; ++k) sums[k] = 0.f;
+  for (int e = threadIdx.x * V; e < D; e += kLNThreads * V) {
+    float v[V];
+    load_floats<DT, V>(x, xo + e, D - e, v);
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = e + k < D ? v[k] - m0 : 0.f;
+    f(e, v);
+  }
+  block_sum<K, kLoopWaves>(sums, lds, turn);
+  return m0;
+}
+
+template <int DT, int WDT>
+__global__ __launch_bounds__(kLNThreads) void ln_loop_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>;
+  __shared__ float lds[2][2 * kLoopWaves];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const int64_t xo = row_offset((uint32_t)row, A.inner, A.sx), yo = row_offset((uint32_t)row, A.inner, A.sout);
+    float s[2];
+    const float m0 = row_loop<DT>(A.x, xo, A.D, A.inv_d, lds, turn, s, [&](int, const float (&d)[V]) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        s[0] += d[k];
+        s[1] = fmaf(d[k], d[k], s[1]);
+      }
+    });
+    const float e = s[0] * A.inv_d;
+    const float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
+    for (int c = threadIdx.x * V; c < A.D; c += kLNThreads * V) {
+      float v[V], w[V], b[V];
+      load_floats<DT, V>(A.x, xo + c, A.D - c, v);
+      if (A.gamma) load_floats<WDT, V>(A.gamma, c, A.D - c, w);
+      if (A.beta) load_floats<WDT, V>(A.beta, c, A.D - c, b);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float h = ((v[k] - m0) - e) * r;
+        v[k] = fmaf(h, A.gamma ? w[k] : 1.f, A.beta ? b[k] : 0.f);
+      }
+      store_part<DT>(A.out, yo + c, A.D - c, pack<DT, 16>(v));
+    }
+  }
+}
+
+// per-row (m, r, mean g, mean g h): the sums over d = x - m0 of d, d^2, g and
+// g d give all of them
+template <int DT, int WDT>
+__global__ __launch_bounds__(kLNThreads) void ln_loop_rowstat_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>;
+  __shared__ float lds[2][4 * kLoopWaves];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const int64_t xo = row_offset((uint32_t)row, A.inner, A.sx), go = row_offset((uint32_t)row, A.inner, A.sdy);
+    float s[4];
+    const float m0 = row_loop<DT>(A.x, xo, A.D, A.inv_d, lds, turn, s, [&](int c, const float (&d)[V]) {
+      float g[V], w[V];
+      load_floats<DT, V>(A.dy, go + c, A.D - c, g);
+      if (A.gamma) load_floats<WDT, V>(A.gamma, c, A.D - c, w);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (A.gamma) g[k] *= w[k];
+        s[0] += d[k];
+        s[1] = fmaf(d[k], d[k], s[1]);
+        s[2] += g[k];
+        s[3] = fmaf(g[k], d[k], s[3]);
+      }
+    });
+    if (threadIdx.x == 0) {
+      const float e = s[0] * A.inv_d, mg = s[2] * A.inv_d;
+      const float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
+      // m0 and e apart: their sum would round e away when m0 is large
+      reinterpret_cast<float4 *>(A.rowstat)[2 * row] = make_float4(m0, e, r, mg);
+      A.rowstat[8 * row + 4] = r * fmaf(s[3], A.inv_d, -e * mg);
+    }
+  }
+}
+
+// dx and the column sums: a block has 256 vectors of columns (blockIdx.x) and
+// every gridDim.y-th row
+template <int DT, int WDT>
+__global__ __launch_bounds__(kLNThreads) void ln_columns_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>;
+  const int c = (blockIdx.x * kLNThreads + threadIdx.x) * V;
+  float w[V], dg[V], db[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) w[k] = 1.f, dg[k] = db[k] = 0.f;
+  if (A.gamma) load_floats<WDT, V>(A.gamma, c, A.D - c, w);
+  for (int64_t row = blockIdx.y; row < A.rows; row += gridDim.y) {
+    const float4 st = reinterpret_cast<const float4 *>(A.rowstat)[2 * row];
+    const float mgh = A.rowstat[8 * row + 4];
+    float x[V], g[V];
+    load_floats<DT, V>(A.x, row_offset((uint32_t)row, A.inner, A.sx) + c, A.D - c, x);
+    load_floats<DT, V>(A.dy, row_offset((uint32_t)row, A.inner, A.sdy) + c, A.D - c, g);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float h = ((x[k] - st.x) - st.y) * st.z;
+      dg[k] = fmaf(g[k], h, dg[k]);
+      db[k] += g[k];
+      x[k] = st.z * (fmaf(-h, mgh, g[k] * w[k]) - st.w);
+    }
+    store_part<DT>(A.out, row_offset((uint32_t)row, A.inner, A.sout) + c, A.D - c, pack<DT, 16>(x));
+  }
+  if (A.part) {
+    // floats of a block of partials: columns in the order [u][k][thread], so
+    // that stores of a wave are contiguous
+    float *p = A.part + (int64_t)blockIdx.y * 2 * A.cols + (int64_t)blockIdx.x * kLNThreads * V + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      p[k * kLNThreads] = dg[k];
+      p[A.cols + k * kLNThreads] = db[k];
+    }
+  }
+}
+
+// dgamma and dbeta: the partials' sums, in a fixed order.  A block takes 64
+// partial columns (of 2 * cols); its 16 waves take every 16th block of
+// partials each.
+constexpr int kReduceThreads = 1024;
+template <int WDT, int LANES, int V>
+__global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const LNArgs A) {
+  __shared__ float lds[kReduceThreads];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i = (int64_t)blockIdx.x * 64 + lane; // of 2 * cols
+  float s = 0.f;
+  if (i < 2 * (int64_t)A.cols) {
+    const float *p = A.part + i;
+#pragma unroll 4
+    for (int b = wave; b < A.nparts; b += kReduceThreads / 64) s += p[(int64_t)b * 2 * A.cols];
+  }
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (wave == 0 && i < 2 * (int64_t)A.cols) {
+#pragma unroll
+    for (int w = 1; w < kReduceThreads / 64; ++w) s += lds[w * 64 + lane];
+    const bool beta = i >= A.cols;
+    const uint32_t j = (uint32_t)(beta ? i - A.cols : i);
+    const uint32_t u = j / (LANES * V), k = j / LANES % V, l = j % LANES;
+    const int64_t col = ((int64_t)u * LANES + l) * V + k;
+    void *out = beta ? A.dbeta : A.dgamma;
+    if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(s);
+  }
+}
+
+template <int DT, int WDT> hipError_t launch_forward(const LNArgs &a, hipStream_t st) {
+  const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
+  hipLaunchKernelGGL((ln_loop_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT, int WDT> hipError_t launch_backward(const LNArgs &a, hipStream_t st) {
+  constexpr int V = kVec<DT>;
+  hipError_t e;
+  if (a.rows > 0) {
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
+    hipLaunchKernelGGL((ln_loop_rowstat_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((ln_columns_kernel<DT, WDT>), dim3((unsigned)(a.cols / (kLNThreads * V)), (unsigned)a.nparts),
+                       dim3(kLNThreads), 0, st, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.part) {
+    hipLaunchKernelGGL((ln_reduce_kernel<WDT, kLNThreads, V>), dim3((unsigned)((2 * (int64_t)a.cols + 63) / 64)),
+                       dim3(kReduceThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+} // namespace sb
+
+hipError_t sb_launch_layer_norm(const sb::LNArgs &a, int dtype, int wdtype, hipStream_t st) {
+  using namespace sb;
+  if (dtype == DT_F32) return launch_forward<DT_F32, DT_F32>(a, st);
+  if (dtype == DT_F16)
+    return wdtype == DT_F32 ? launch_forward<DT_F16, DT_F32>(a, st) : launch_forward<DT_F16, DT_F16>(a, st);
+  return wdtype == DT_F32 ? launch_forward<DT_BF16, DT_F32>(a, st) : launch_forward<DT_BF16, DT_BF16>(a, st);
+}
+
+hipError_t sb_launch_layer_norm_backward(const sb::LNArgs &a, int dtype, int wdtype, hipStream_t st) {
+  using namespace sb;
+  if (dtype == DT_F32) return launch_backward<DT_F32, DT_F32>(a, st);
+  if (dtype == DT_F16)
+    return wdtype == DT_F32 ? launch_backward<DT_F16, DT_F32>(a, st) : launch_backward<DT_F16, DT_F16>(a, st);
+  return wdtype == DT_F32 ? launch_backward<DT_BF16, DT_F32>(a, st) : launch_backward<DT_BF16, DT_BF16>(a, st);
+}

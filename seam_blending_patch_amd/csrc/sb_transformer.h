@@ -1,0 +1,91 @@
+// sb_transformer.h -- launch arguments shared by the host entry points and the
+// gfx950 kernels of the transformer operators (layer norm, rotary embedding,
+// gradient norm and clipping).
+#pragma once
+
+#include "sb_internal.h"
+
+namespace sb {
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+// Rows are indexed r = o * inner + i; a tensor's row r starts o * outer stride
+// + i * inner stride elements from its base.
+struct RowStride {
+  int64_t o, i;
+};
+
+struct LNArgs {
+  const void *x, *dy;
+  void *out; // y, or dx
+  const void *gamma, *beta;
+  RowStride sx, sdy, sout;
+  int64_t rows;
+  FastDiv inner;
+  int32_t D;
+  float eps, inv_d;
+  // backward
+  float *part;        // weight-gradient partials [blocks][2][columns] (nullptr: none wanted)
+  float *rowstat;     // per row: mean, 1/sigma, mean of g, mean of g h (the looping kernels)
+  void *dgamma, *dbeta;
+  int32_t nparts, cols; // blocks of partials; floats of each (the columns, rounded up to the block's)
+};
+
+constexpr int kLNThreads = 256; // threads of a looping or column block
+
+// ---------------------------------------------------------------------------
+// rotary position embedding
+// ---------------------------------------------------------------------------
+constexpr int kRotaryMaxAxes = 4;
+constexpr int kRotaryThreads = 256;
+
+struct RotaryTensor {
+  const void *in;
+  void *out;
+  int64_t in_b, in_t, in_h, out_b, out_t, out_h; // strides in elements
+};
+
+struct RotaryArgs {
+  RotaryTensor x[2];     // query heads, key heads
+  int32_t heads[2];
+  int64_t tokens;        // batch * length
+  FastDiv length;
+  int32_t D, part;       // head length, rotated elements (even)
+  int32_t units_turned, units; // 16-byte steps of a head: over its pairs, and with those over the rest
+  FastDiv div_units;
+  const double *freqs;   // radians per position, part / 2 of them
+  const void *positions;
+  int64_t pos_axis, pos_b, pos_t; // strides in elements
+  int32_t pos64;         // positions are int64 (else int32)
+  int32_t axes, ends[kRotaryMaxAxes]; // pairs [ends[a - 1], ends[a]) turn by the positions of axis a
+  float scale, scale_sin;  // cosines and sines are multiplied by these (the sign of the direction in the second)
+};
+
+// ---------------------------------------------------------------------------
+// gradient norm and clipping
+// ---------------------------------------------------------------------------
+constexpr int kClipTensors = 128; // tensors of a launch (their table is a kernel argument)
+constexpr int kClipThreads = 256;
+
+struct ClipArgs {
+  const void *in[kClipTensors];
+  void *out[kClipTensors];
+  int64_t n[kClipTensors];
+  uint32_t begin[kClipTensors + 1]; // first chunk of each tensor
+  uint8_t types[kClipTensors];      // dtype, and dtype of the output << 2
+  int64_t chunk;                    // elements of a chunk (a multiple of kClipThreads vectors)
+  double *partials;                 // sums of squares: this launch's first, or all of them (second pass)
+  int32_t tensors, npartials;
+  float max_norm, eps;
+  float *norm;                      // written by the first block of a second-pass launch that has it
+};
+static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments of at most 4 KiB");
+
+} // namespace sb
+
+hipError_t sb_launch_layer_norm(const sb::LNArgs &a, int dtype, int wdtype, hipStream_t st);
+hipError_t sb_launch_layer_norm_backward(const sb::LNArgs &a, int dtype, int wdtype, hipStream_t st);
+hipError_t sb_launch_rotary(const sb::RotaryArgs &a, int dtype, int interleaved, hipStream_t st);
+hipError_t sb_launch_square_sums(const sb::ClipArgs &a, unsigned blocks, hipStream_t st);
+hipError_t sb_launch_clip(const sb::ClipArgs &a, unsigned blocks, hipStream_t st);

@@ -26,6 +26,77 @@ __device__ __forceinline__ int64_t row_offset(uint32_t row, const FastDiv &inner
 }
 
 // ---------------------------------------------------------------------------
+// Rows that fit the registers of LANES threads, NV vectors each: every element
+// is read once.  A block of 256 threads (or LANES, if more) takes as many rows
+// as it has groups of LANES.
+// ---------------------------------------------------------------------------
+template <int LANES> constexpr int kRowThreads = LANES > kLNThreads ? LANES : kLNThreads;
+
+// A thread's vector u holds the elements of its row from (u * LANES + lane) * V
+// on.  Only rows that are no whole number of vectors (TAIL) have one cut by
+// the row's end; the others' are whole or absent.
+// x as fp32 -> d = x - m0 in place, zero where the row has no element
+template <int DT, int LANES, int NV, bool TAIL>
+__device__ __forceinline__ void subtract(float (&x)[NV][kVec<DT>], float m0, int lane, int D) {
+  constexpr int V = kVec<DT>;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int e = (u * LANES + lane) * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[u][k] = (TAIL ? e + k < D : e < D) ? x[u][k] - m0 : 0.f;
+  }
+}
+
+template <int DT, int WDT, int LANES, int NV, bool TAIL>
+__global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>, GROUPS = kRowThreads<LANES> / LANES;
+  __shared__ float lds[2][LANES > 64 ? 2 * kRowThreads<LANES> / 64 : 1];
+  int turn = 0;
+  const int lane = threadIdx.x % LANES;
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < A.rows; r0 += (int64_t)gridDim.x * GROUPS) {
+    const int64_t row = r0 + threadIdx.x / LANES;
+    const bool here = row < A.rows; // every lane takes part in the sums
+    const uint32_t at = (uint32_t)(here ? row : A.rows - 1);
+    const int64_t xo = row_offset(at, A.inner, A.sx);
+    float x[NV][V];
+    float s1[1] = {0.f};
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int e = (u * LANES + lane) * V;
+      unpack<DT, 16>(load_row<DT, TAIL>(A.x, xo + e, A.D - e), x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s1[0] += x[u][k];
+    group_sum<LANES>(s1, lds, turn);
+    subtract<DT, LANES, NV, TAIL>(x, s1[0] * A.inv_d, lane, A.D);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        s[0] += x[u][k];
+        s[1] = fmaf(x[u][k], x[u][k], s[1]);
+      }
+    group_sum<LANES>(s, lds, turn);
+    const float e = s[0] * A.inv_d;
+    const float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
+    const int64_t yo = row_offset(at, A.inner, A.sout);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = (u * LANES + lane) * V;
+      float w[V], b[V];
+      if (A.gamma) load_floats_row<WDT, V, TAIL>(A.gamma, c, A.D - c, w);
+      if (A.beta) load_floats_row<WDT, V, TAIL>(A.beta, c, A.D - c, b);
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[u][k] = fmaf((x[u][k] - e) * r, A.gamma ? w[k] : 1.f, A.beta ? b[k] : 0.f);
+      if (here) store_row<DT, TAIL>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Rows of any length: one block a row, looping over it (three times forward,
 // the second and third from cache).
 // ---------------------------------------------------------------------------
@@ -43,7 +114,7 @@ __device__ __forceinline__ float row_loop(const void *x, int64_t xo, int D, floa
 #pragma unroll
     for (int k = 0; k < V; ++k) s[0] += v[k];
   }
-  block_sum<1, kLoopWaves>(s, lds, turn);
+  group_sum<kLNThreads>(s, lds, turn);
   const float m0 = s[0] * inv_d;
 #pragma unroll
   for (int k = 0; k < K; ++k) sums[k] = 0.f;
@@ -54,7 +125,7 @@ __device__ __forceinline__ float row_loop(const void *x, int64_t xo, int D, floa
     for (int k = 0; k < V; ++k) v[k] = e + k < D ? v[k] - m0 : 0.f;
     f(e, v);
   }
-  block_sum<K, kLoopWaves>(sums, lds, turn);
+  group_sum<kLNThreads>(sums, lds, turn);
   return m0;
 }
 
@@ -189,7 +260,29 @@ __global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const LNArgs 
   }
 }
 
+template <int DT, int WDT, int LANES, int NV> hipError_t launch_rows(const LNArgs &a, hipStream_t st) {
+  constexpr int T = kRowThreads<LANES>, GROUPS = T / LANES;
+  const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + GROUPS - 1) / GROUPS, kMaxBlocksX / (T / kLNThreads));
+  if (a.D % kVec<DT>) hipLaunchKernelGGL((ln_row_kernel<DT, WDT, LANES, NV, true>), dim3(blocks), dim3(T), 0, st, a);
+  else hipLaunchKernelGGL((ln_row_kernel<DT, WDT, LANES, NV, false>), dim3(blocks), dim3(T), 0, st, a);
+  return hipGetLastError();
+}
+
 template <int DT, int WDT> hipError_t launch_forward(const LNArgs &a, hipStream_t st) {
+  const int nv = (a.D + kVec<DT> - 1) / kVec<DT>; // vectors of a row
+  if (nv <= 4) return launch_rows<DT, WDT, 4, 1>(a, st);
+  if (nv <= 8) return launch_rows<DT, WDT, 8, 1>(a, st);
+  if (nv <= 16) return launch_rows<DT, WDT, 16, 1>(a, st);
+  if (nv <= 32) return launch_rows<DT, WDT, 32, 1>(a, st);
+  if (nv <= 64) return launch_rows<DT, WDT, 64, 1>(a, st);
+  if (nv <= 128) return launch_rows<DT, WDT, 64, 2>(a, st);
+  if (nv <= 192) return launch_rows<DT, WDT, 64, 3>(a, st);
+  if (nv <= 256) return launch_rows<DT, WDT, 64, 4>(a, st);
+  if (nv <= 512) return launch_rows<DT, WDT, 256, 2>(a, st);
+  if (nv <= 768) return launch_rows<DT, WDT, 256, 3>(a, st);
+  if (nv <= 1024) return launch_rows<DT, WDT, 256, 4>(a, st);
+  if (nv <= 2048) return launch_rows<DT, WDT, 1024, 2>(a, st);
+  if (nv <= 4096) return launch_rows<DT, WDT, 1024, 4>(a, st);
   const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
   hipLaunchKernelGGL((ln_loop_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);
   return hipGetLastError();

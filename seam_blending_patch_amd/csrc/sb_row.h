@@ -54,12 +54,27 @@ template <int DT> __device__ __forceinline__ void store_part(void *p, int64_t e0
   }
 }
 
+// A vector of a row that has n elements from there on: where the row is a
+// whole number of vectors (no TAIL), it is whole or absent.
+template <int DT, bool TAIL> __device__ __forceinline__ Vec<16> load_row(const void *p, int64_t e0, int n) {
+  return load_part<DT>(p, e0, TAIL ? n : n > 0 ? kVec<DT> : 0);
+}
+template <int DT, bool TAIL>
+__device__ __forceinline__ void store_row(void *p, int64_t e0, int n, const Vec<16> &v) {
+  store_part<DT>(p, e0, TAIL ? n : n > 0 ? kVec<DT> : 0, v);
+}
+
 // N consecutive values of type DT (n of them present, zeros after) as fp32
 template <int DT, int N>
 __device__ __forceinline__ void load_floats(const void *p, int64_t e0, int n, float *f) {
   static_assert(N % kVec<DT> == 0, "whole vectors");
 #pragma unroll
   for (int j = 0; j < N; j += kVec<DT>) unpack<DT, 16>(load_part<DT>(p, e0 + j, n - j), f + j);
+}
+
+template <int DT, int N, bool TAIL>
+__device__ __forceinline__ void load_floats_row(const void *p, int64_t e0, int n, float *f) {
+  load_floats<DT, N>(p, e0, TAIL ? n : n > 0 ? N : 0, f);
 }
 
 // One value per lane summed over every aligned group of LANES lanes, returned
@@ -87,29 +102,33 @@ template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// K values summed over a whole block of W waves, returned in every thread.
-// The halves of `lds` are taken in turn (`turn` flips on every call): a wave
-// may still read one while another writes the other, so one barrier a sum is
-// enough.
-template <int K, int W, int N>
-__device__ __forceinline__ void block_sum(float (&v)[K], float (&lds)[2][N], int &turn) {
-  static_assert(N >= W * K, "room for every wave's sums");
+// K values summed over every group of LANES threads of a block of THREADS,
+// returned in each of the group's threads.  Up to 64 lanes no memory is used;
+// wider groups exchange their waves' sums through `lds`, whose halves are
+// taken in turn (`turn` flips on every call): a wave may still read one while
+// another writes the other, so one barrier a sum is enough.
+template <int LANES, int K, int N>
+__device__ __forceinline__ void group_sum(float (&v)[K], float (&lds)[2][N], int &turn) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = lanes_sum<64>(v[k]);
-  float *s = lds[turn];
-  turn ^= 1;
-  const int wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) {
+  for (int k = 0; k < K; ++k) v[k] = lanes_sum<(LANES < 64 ? LANES : 64)>(v[k]);
+  if constexpr (LANES > 64) {
+    constexpr int W = LANES / 64; // waves of a group
+    const int wave = threadIdx.x >> 6;
+    float *s = lds[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[wave * K + k] = v[k];
-  }
-  __syncthreads();
+      for (int k = 0; k < K; ++k) s[wave * K + k] = v[k];
+    }
+    __syncthreads();
+    s += wave / W * W * K;
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = s[k];
+    for (int k = 0; k < K; ++k) v[k] = s[k];
 #pragma unroll
-  for (int w = 1; w < W; ++w) {
+    for (int w = 1; w < W; ++w) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += s[w * K + k];
+      for (int k = 0; k < K; ++k) v[k] += s[w * K + k];
+    }
   }
 }
 

@@ -74,19 +74,28 @@ int check_eps(float eps) {
   return !(eps >= 0.0f) || eps == __builtin_inff() ? failf(SB_EARG, "eps must be finite and >= 0") : SB_OK;
 }
 
-// The backward pass's workspace: nparts blocks of 2 * cols floats, then 8
-// floats a row.
+// The backward pass's workspace: nparts blocks of 2 * cols floats, then, for
+// rows too long for registers, 8 floats a row.
 struct BackwardPlan {
   int64_t nparts, cols, part_bytes, rowstat_bytes;
 };
 
 BackwardPlan plan_backward(int64_t rows, int64_t d, int dtype) {
   BackwardPlan p;
-  const int64_t v = 16 / sb::elem_bytes(dtype), per = sb::kLNThreads * v;
-  p.cols = (d + per - 1) / per * per;
-  p.nparts = std::max<int64_t>(1, std::min<int64_t>(rows, 4 * sb_cu_count() / std::max<int64_t>(1, p.cols / per)));
+  const int64_t v = 16 / sb::elem_bytes(dtype), nv = (d + v - 1) / v;
+  const sb::LNLayout lay = sb::backward_layout(nv);
+  if (lay.lanes) {
+    p.cols = (int64_t)lay.lanes * lay.nv * v;
+    const int64_t blocks = (int64_t)sb_cu_count() * 4 / (lay.threads() / sb::kLNThreads);
+    p.nparts = std::max<int64_t>(1, std::min((rows + lay.rows() - 1) / lay.rows(), blocks));
+    p.rowstat_bytes = 0;
+  } else {
+    const int64_t per = sb::kLNThreads * v;
+    p.cols = (d + per - 1) / per * per;
+    p.nparts = std::max<int64_t>(1, std::min<int64_t>(rows, 4 * sb_cu_count() / std::max<int64_t>(1, p.cols / per)));
+    p.rowstat_bytes = rows * 8 * (int64_t)sizeof(float);
+  }
   p.part_bytes = p.nparts * 2 * p.cols * (int64_t)sizeof(float);
-  p.rowstat_bytes = rows * 8 * (int64_t)sizeof(float);
   return p;
 }
 

@@ -96,6 +96,124 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
   }
 }
 
+// dx and the columns' sums in one pass over x and dy.  A block keeps taking
+// rows, a thread the same columns of each, so dgamma and dbeta add up in
+// registers; at the end the block's rows are merged and written as one block of
+// partials.  The next row's vectors are requested before this row's are used.
+template <int DT, int WDT, int LANES, int NV, bool TAIL>
+__global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>, T = kRowThreads<LANES>, GROUPS = T / LANES, COLS = LANES * NV * V;
+  // partials to merge: one of each wave, or of each group where that is wider
+  constexpr int COPIES = LANES < 64 ? T / 64 : GROUPS;
+  __shared__ float lds[2][LANES > 64 ? 4 * T / 64 : 1];
+  __shared__ float merge[COPIES > 1 ? COPIES * COLS : 1];
+  int turn = 0;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  float w[NV][V], dg[NV][V], db[NV][V];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int c = (u * LANES + lane) * V;
+    if (A.gamma) load_floats_row<WDT, V, TAIL>(A.gamma, c, A.D - c, w[u]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (!A.gamma) w[u][k] = 1.f;
+      dg[u][k] = db[u][k] = 0.f;
+    }
+  }
+  Vec<16> xr[NV], gr[NV];
+  auto request = [&](int64_t row) {
+    // rows past the end read nothing and hold zeros
+    const uint32_t at = (uint32_t)(row < A.rows ? row : 0);
+    const int64_t xo = row_offset(at, A.inner, A.sx), go = row_offset(at, A.inner, A.sdy);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = (u * LANES + lane) * V, n = row < A.rows ? A.D - c : 0;
+      xr[u] = load_row<DT, TAIL>(A.x, xo + c, n);
+      gr[u] = load_row<DT, TAIL>(A.dy, go + c, n);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  request((int64_t)blockIdx.x * GROUPS + group);
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < A.rows; r0 += step) {
+    const int64_t row = r0 + group;
+    float x[NV][V], g[NV][V];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      unpack<DT, 16>(xr[u], x[u]);
+      unpack<DT, 16>(gr[u], g[u]);
+    }
+    request(row + step);
+    float s1[1] = {0.f};
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s1[0] += x[u][k];
+    group_sum<LANES>(s1, lds, turn);
+    subtract<DT, LANES, NV, TAIL>(x, s1[0] * A.inv_d, lane, A.D);
+    float s[4] = {0.f, 0.f, 0.f, 0.f}; // of d, d^2, g, g d
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float gw = g[u][k] * w[u][k];
+        s[0] += x[u][k];
+        s[1] = fmaf(x[u][k], x[u][k], s[1]);
+        s[2] += gw;
+        s[3] = fmaf(gw, x[u][k], s[3]);
+      }
+    group_sum<LANES>(s, lds, turn);
+    const float e = s[0] * A.inv_d, mg = s[2] * A.inv_d;
+    float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
+    const float mgh = r * fmaf(s[3], A.inv_d, -e * mg);
+    if (row >= A.rows) r = 0.f; // an absent row adds nothing, whatever eps is
+    const int64_t yo = row < A.rows ? row_offset((uint32_t)row, A.inner, A.sout) : 0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = (u * LANES + lane) * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float h = (x[u][k] - e) * r;
+        dg[u][k] = fmaf(g[u][k], h, dg[u][k]);
+        db[u][k] += g[u][k];
+        x[u][k] = r * (fmaf(-h, mgh, g[u][k] * w[u][k]) - mg);
+      }
+      if (row < A.rows) store_row<DT, TAIL>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
+    }
+  }
+  if (!A.part) return;
+  // columns in the order [u][k][lane], so that a wave's stores are contiguous
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float *part = A.part + ((int64_t)blockIdx.x * 2 + which) * COLS;
+    auto &v = which ? db : dg;
+    if constexpr (COPIES == 1) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) part[(u * V + k) * LANES + lane] = v[u][k];
+    } else {
+      if (which) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          float t = v[u][k];
+#pragma unroll
+          for (int o = LANES; o < 64; o <<= 1) t += __shfl_xor(t, o);
+          if (LANES >= 64 || (threadIdx.x & 63) < LANES)
+            merge[(LANES < 64 ? threadIdx.x / 64 : group) * COLS + (u * V + k) * LANES + lane] = t;
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < COLS; i += T) {
+        float t = merge[i];
+#pragma unroll
+        for (int c = 1; c < COPIES; ++c) t += merge[c * COLS + i];
+        part[i] = t;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Rows of any length: one block a row, looping over it (three times forward,
 // the second and third from cache).
@@ -288,23 +406,50 @@ template <int DT, int WDT> hipError_t launch_forward(const LNArgs &a, hipStream_
   return hipGetLastError();
 }
 
+template <int WDT, int LANES, int V> hipError_t launch_reduce(const LNArgs &a, hipStream_t st) {
+  if (!a.part) return hipSuccess;
+  hipLaunchKernelGGL((ln_reduce_kernel<WDT, LANES, V>), dim3((unsigned)((2 * (int64_t)a.cols + 63) / 64)),
+                     dim3(kReduceThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT, int WDT, int LANES, int NV> hipError_t launch_backward_rows(const LNArgs &a, hipStream_t st) {
+  constexpr int T = kRowThreads<LANES>;
+  if (a.nparts > 0) {
+    if (a.D % kVec<DT>)
+      hipLaunchKernelGGL((ln_backward_kernel<DT, WDT, LANES, NV, true>), dim3(a.nparts), dim3(T), 0, st, a);
+    else
+      hipLaunchKernelGGL((ln_backward_kernel<DT, WDT, LANES, NV, false>), dim3(a.nparts), dim3(T), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return launch_reduce<WDT, LANES, kVec<DT>>(a, st);
+}
+
 template <int DT, int WDT> hipError_t launch_backward(const LNArgs &a, hipStream_t st) {
   constexpr int V = kVec<DT>;
-  hipError_t e;
+  const LNLayout lay = backward_layout((a.D + V - 1) / V);
+  switch (lay.lanes) {
+  case 4: return launch_backward_rows<DT, WDT, 4, 1>(a, st);
+  case 8: return launch_backward_rows<DT, WDT, 8, 1>(a, st);
+  case 16: return launch_backward_rows<DT, WDT, 16, 1>(a, st);
+  case 32: return launch_backward_rows<DT, WDT, 32, 1>(a, st);
+  case 64: return lay.nv == 1 ? launch_backward_rows<DT, WDT, 64, 1>(a, st) : launch_backward_rows<DT, WDT, 64, 2>(a, st);
+  case 128: return launch_backward_rows<DT, WDT, 128, 2>(a, st);
+  case 256: return launch_backward_rows<DT, WDT, 256, 2>(a, st);
+  case 512: return launch_backward_rows<DT, WDT, 512, 2>(a, st);
+  case 1024: return launch_backward_rows<DT, WDT, 1024, 2>(a, st);
+  }
   if (a.rows > 0) {
     const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
     hipLaunchKernelGGL((ln_loop_rowstat_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((ln_columns_kernel<DT, WDT>), dim3((unsigned)(a.cols / (kLNThreads * V)), (unsigned)a.nparts),
                        dim3(kLNThreads), 0, st, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (a.part) {
-    hipLaunchKernelGGL((ln_reduce_kernel<WDT, kLNThreads, V>), dim3((unsigned)((2 * (int64_t)a.cols + 63) / 64)),
-                       dim3(kReduceThreads), 0, st, a);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  return launch_reduce<WDT, kLNThreads, V>(a, st);
 }
 
 } // namespace sb

@@ -34,6 +34,28 @@ struct LNArgs {
 
 constexpr int kLNThreads = 256; // threads of a looping or column block
 
+// How the backward pass lays rows of nv vectors over threads: NV vectors on
+// each of LANES threads, as many rows to a block as it has room for (lanes 0:
+// the row is too long for registers and the looping kernels take it).
+struct LNLayout {
+  int lanes, nv;
+  int threads() const { return lanes > kLNThreads ? lanes : kLNThreads; }
+  int rows() const { return threads() / lanes; } // of a block, at a time
+};
+inline LNLayout backward_layout(int64_t nv) {
+  if (nv <= 64) {
+    int lanes = 4;
+    while (lanes < nv) lanes *= 2;
+    return LNLayout{lanes, 1};
+  }
+  if (nv <= 128) return LNLayout{64, 2};
+  if (nv <= 256) return LNLayout{128, 2};
+  if (nv <= 512) return LNLayout{256, 2};
+  if (nv <= 1024) return LNLayout{512, 2};
+  if (nv <= 2048) return LNLayout{1024, 2};
+  return LNLayout{0, 0};
+}
+
 // ---------------------------------------------------------------------------
 // rotary position embedding
 // ---------------------------------------------------------------------------

@@ -86,7 +86,7 @@ BackwardPlan plan_backward(int64_t rows, int64_t d, int dtype) {
   const sb::LNLayout lay = sb::backward_layout(nv);
   if (lay.lanes) {
     p.cols = (int64_t)lay.lanes * lay.nv * v;
-    const int64_t blocks = (int64_t)sb_cu_count() * 4 / (lay.threads() / sb::kLNThreads);
+    const int64_t blocks = (int64_t)sb_cu_count() * lay.blocks_per_cu();
     p.nparts = std::max<int64_t>(1, std::min((rows + lay.rows() - 1) / lay.rows(), blocks));
     p.rowstat_bytes = 0;
   } else {

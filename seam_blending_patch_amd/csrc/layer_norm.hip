@@ -349,32 +349,41 @@ __global__ __launch_bounds__(kLNThreads) void ln_columns_kernel(const LNArgs A) 
   }
 }
 
-// dgamma and dbeta: the partials' sums, in a fixed order.  A block takes 64
-// partial columns (of 2 * cols); its 16 waves take every 16th block of
-// partials each.
-constexpr int kReduceThreads = 1024;
+// dgamma and dbeta: the partials' sums, in a fixed order.  A block takes 16
+// floats of a block of partials (of 2 * cols), as 4 vectors; its 256 groups of
+// 4 threads take every 256th block of partials each, so that a thousand of
+// them are four loads deep and a thousand columns are 128 blocks wide.
+constexpr int kReduceThreads = 1024, kReduceCols = 16;
 template <int WDT, int LANES, int V>
 __global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const LNArgs A) {
-  __shared__ float lds[kReduceThreads];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t i = (int64_t)blockIdx.x * 64 + lane; // of 2 * cols
-  float s = 0.f;
-  if (i < 2 * (int64_t)A.cols) {
-    const float *p = A.part + i;
+  static_assert(LANES * V % kReduceCols == 0, "cols is a multiple of kReduceCols");
+  __shared__ float lds[kReduceThreads / 64][kReduceCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = threadIdx.x & 3;
+  const float4 *p = reinterpret_cast<const float4 *>(A.part + (int64_t)blockIdx.x * kReduceCols) + quad;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int b = wave; b < A.nparts; b += kReduceThreads / 64) s += p[(int64_t)b * 2 * A.cols];
+  for (int b = threadIdx.x >> 2; b < A.nparts; b += kReduceThreads / 4) {
+    const float4 v = p[(int64_t)b * 2 * A.cols / 4];
+    s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
   }
-  lds[threadIdx.x] = s;
-  __syncthreads();
-  if (wave == 0 && i < 2 * (int64_t)A.cols) {
 #pragma unroll
-    for (int w = 1; w < kReduceThreads / 64; ++w) s += lds[w * 64 + lane];
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int o = 4; o < 64; o <<= 1) s[k] += __shfl_xor(s[k], o);
+    if (lane < 4) lds[wave][quad * 4 + k] = s[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < kReduceCols) {
+    float t = lds[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kReduceThreads / 64; ++w) t += lds[w][threadIdx.x];
+    const int64_t i = (int64_t)blockIdx.x * kReduceCols + threadIdx.x;
     const bool beta = i >= A.cols;
     const uint32_t j = (uint32_t)(beta ? i - A.cols : i);
     const uint32_t u = j / (LANES * V), k = j / LANES % V, l = j % LANES;
     const int64_t col = ((int64_t)u * LANES + l) * V + k;
     void *out = beta ? A.dbeta : A.dgamma;
-    if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(s);
+    if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(t);
   }
 }
 
@@ -408,7 +417,7 @@ template <int DT, int WDT> hipError_t launch_forward(const LNArgs &a, hipStream_
 
 template <int WDT, int LANES, int V> hipError_t launch_reduce(const LNArgs &a, hipStream_t st) {
   if (!a.part) return hipSuccess;
-  hipLaunchKernelGGL((ln_reduce_kernel<WDT, LANES, V>), dim3((unsigned)((2 * (int64_t)a.cols + 63) / 64)),
+  hipLaunchKernelGGL((ln_reduce_kernel<WDT, LANES, V>), dim3((unsigned)(2 * (int64_t)a.cols / kReduceCols)),
                      dim3(kReduceThreads), 0, st, a);
   return hipGetLastError();
 }
@@ -429,16 +438,19 @@ template <int DT, int WDT, int LANES, int NV> hipError_t launch_backward_rows(co
 template <int DT, int WDT> hipError_t launch_backward(const LNArgs &a, hipStream_t st) {
   constexpr int V = kVec<DT>;
   const LNLayout lay = backward_layout((a.D + V - 1) / V);
-  switch (lay.lanes) {
-  case 4: return launch_backward_rows<DT, WDT, 4, 1>(a, st);
-  case 8: return launch_backward_rows<DT, WDT, 8, 1>(a, st);
-  case 16: return launch_backward_rows<DT, WDT, 16, 1>(a, st);
-  case 32: return launch_backward_rows<DT, WDT, 32, 1>(a, st);
-  case 64: return lay.nv == 1 ? launch_backward_rows<DT, WDT, 64, 1>(a, st) : launch_backward_rows<DT, WDT, 64, 2>(a, st);
-  case 128: return launch_backward_rows<DT, WDT, 128, 2>(a, st);
-  case 256: return launch_backward_rows<DT, WDT, 256, 2>(a, st);
-  case 512: return launch_backward_rows<DT, WDT, 512, 2>(a, st);
-  case 1024: return launch_backward_rows<DT, WDT, 1024, 2>(a, st);
+  switch (lay.lanes * 16 + lay.nv) {
+  case 4 * 16 + 1: return launch_backward_rows<DT, WDT, 4, 1>(a, st);
+  case 8 * 16 + 1: return launch_backward_rows<DT, WDT, 8, 1>(a, st);
+  case 16 * 16 + 1: return launch_backward_rows<DT, WDT, 16, 1>(a, st);
+  case 32 * 16 + 1: return launch_backward_rows<DT, WDT, 32, 1>(a, st);
+  case 64 * 16 + 1: return launch_backward_rows<DT, WDT, 64, 1>(a, st);
+  case 64 * 16 + 2: return launch_backward_rows<DT, WDT, 64, 2>(a, st);
+  case 64 * 16 + 3: return launch_backward_rows<DT, WDT, 64, 3>(a, st);
+  case 64 * 16 + 4: return launch_backward_rows<DT, WDT, 64, 4>(a, st);
+  case 128 * 16 + 3: return launch_backward_rows<DT, WDT, 128, 3>(a, st);
+  case 128 * 16 + 4: return launch_backward_rows<DT, WDT, 128, 4>(a, st);
+  case 512 * 16 + 2: return launch_backward_rows<DT, WDT, 512, 2>(a, st);
+  case 1024 * 16 + 2: return launch_backward_rows<DT, WDT, 1024, 2>(a, st);
   }
   if (a.rows > 0) {
     const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);

@@ -307,7 +307,7 @@ int layer_norm_backward(const void *dy, const int64_t dy_stride[2], const void *
  * -a: the gradient of the forward call.
  *   q, k         device tensors [B, T, heads, D]; q_heads or k_heads may be 0
  *                (then its pointers and strides are not read).
- *   shape        {B, T, D}: B * T < 2^31, D <= 2^16, at most 2^12 heads each.
+ *   shape        {B, T, D}: B * T < 2^31, D <= 2^13, at most 2^12 heads each.
  *   *_stride     {B, T, head} strides in elements, 0..2^40; D is contiguous.
  *   *_out        each element held once; q_out is q itself or shares no element
  *                with q (k alike), and no output one with the other tensor's

@@ -15,7 +15,7 @@ using sb::failf;
 
 namespace {
 
-constexpr int64_t kMaxHead = 1 << 16;  // head length
+constexpr int64_t kMaxHead = 1 << 13;  // head length: two tokens' cosines and sines are at most 64 KiB
 constexpr int64_t kMaxHeads = 1 << 12; // heads of a tensor: steps of a token are 32-bit
 
 int read_tensor(const char *name, const void *p, const int64_t stride[3], const int64_t shape[3], int64_t heads,
@@ -105,14 +105,16 @@ extern "C" int rotary_apply(const void *q, const int64_t q_stride[3], void *q_ou
     }
 
   const int64_t V = 16 / sb::elem_bytes(dtype);
-  a.tokens = B * T;
   a.length = sb::make_fastdiv((uint32_t)T);
   a.D = (int32_t)D;
   a.part = (int32_t)rot_dim;
   const int64_t turned = layout == SB_ROTARY_INTERLEAVED ? rot_dim : rot_dim / 2;
   a.units_turned = (int32_t)((turned + V - 1) / V);
   a.units = a.units_turned + (int32_t)((D - rot_dim + V - 1) / V);
+  a.items = a.units * (a.heads[0] + a.heads[1]);
   a.div_units = sb::make_fastdiv((uint32_t)a.units);
+  a.div_items = sb::make_fastdiv((uint32_t)a.items);
+  a.div_half = sb::make_fastdiv((uint32_t)(rot_dim / 2));
   a.freqs = freqs;
   a.positions = positions;
   a.pos_axis = position_stride[0];
@@ -122,7 +124,13 @@ extern "C" int rotary_apply(const void *q, const int64_t q_stride[3], void *q_ou
   a.axes = n_sections;
   a.scale = scale;
   a.scale_sin = transpose ? -scale : scale;
-  const hipError_t e = sb_launch_rotary(a, dtype, layout == SB_ROTARY_INTERLEAVED, (hipStream_t)stream);
-  if (e != hipSuccess) return failf(SB_ELAUNCH, "rotary launch failed: %s", hipGetErrorString(e));
+  // launches of fewer than 2^31 steps: their indices are 32-bit
+  const int64_t most = (((int64_t)1 << 31) - 1) / a.items;
+  for (int64_t t0 = 0; t0 < B * T; t0 += most) {
+    a.token0 = (uint32_t)t0;
+    a.tokens = (uint32_t)std::min(most, B * T - t0);
+    const hipError_t e = sb_launch_rotary(a, dtype, layout == SB_ROTARY_INTERLEAVED, (hipStream_t)stream);
+    if (e != hipSuccess) return failf(SB_ELAUNCH, "rotary launch failed: %s", hipGetErrorString(e));
+  }
   return SB_OK;
 }

@@ -33,61 +33,97 @@ __device__ __forceinline__ float2 cos_sin(const RotaryArgs &A, int pair, uint32_
   return make_float2(c * A.scale, s * A.scale_sin);
 }
 
-// One block a token; a thread takes 16-byte steps of its heads (half layout:
-// a step of each half).
+// field by field, so that it is selects among scalar registers and no load at
+// an address that differs from lane to lane
+__device__ __forceinline__ RotaryTensor pick(const RotaryArgs &A, bool key) {
+  const RotaryTensor &q = A.x[0], &k = A.x[1];
+  return RotaryTensor{key ? k.in : q.in,     key ? k.out : q.out,     key ? k.in_b : q.in_b,  key ? k.in_t : q.in_t,
+                      key ? k.in_h : q.in_h, key ? k.out_b : q.out_b, key ? k.out_t : q.out_t, key ? k.out_h : q.out_h};
+}
+
+// A thread takes one 16-byte step of a head (in the half layout one of each
+// half), a block the next 256 of all tokens', wherever tokens begin and end, so
+// that no thread is idle.  The cosines and sines of the tokens it touches are
+// formed once, by all its threads, and kept in LDS for every head; the step is
+// requested before that.
+//
+// Bound by the copy of the heads: 20280 tokens of 24 x 128 bf16, interleaved,
+// 250 MB in 45.8 us (5.45 TB/s, the rate of a large copy), 16384 tokens of 40 x
+// 128 in halves 335 MB in 58 us.  Measured against it: whole tokens to a block
+// 61 us for the first of these (a third of the threads idle), an angle for
+// every head's step of its own 109 us; 2 and 4 steps a thread 44.3 and 46.2 us
+// for the first but 62 and 67 us for the second.  With one head to a key, 64
+// pairs of angles to every 256 bytes, the angles show (3.4 TB/s).
 template <int DT, bool INTER>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs A) {
   constexpr int V = kVec<DT>;
-  const int half = A.part / 2, items = (A.heads[0] + A.heads[1]) * A.units;
-  for (int64_t token = blockIdx.x; token < A.tokens; token += gridDim.x) {
-    const uint32_t b = fdiv((uint32_t)token, A.length), t = (uint32_t)token - b * A.length.d;
-    for (int item = threadIdx.x; item < items; item += kRotaryThreads) {
-      const int head = fdiv(item, A.div_units), unit = item - head * A.units;
-      const bool key = head >= A.heads[0];
-      const RotaryTensor &T = A.x[key];
-      const int h = key ? head - A.heads[0] : head;
-      const int64_t in = b * T.in_b + t * T.in_t + h * T.in_h, out = b * T.out_b + t * T.out_t + h * T.out_h;
-      if (unit >= A.units_turned) {
-        const int e = A.part + (unit - A.units_turned) * V;
-        if (T.in != T.out) store_part<DT>(T.out, out + e, A.D - e, load_part<DT>(T.in, in + e, A.D - e));
-        continue;
-      }
-      if constexpr (INTER) {
-        const int e = unit * V;
-        float f[V];
-        unpack<DT, 16>(load_part<DT>(T.in, in + e, A.part - e), f);
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          if (e + k >= A.part) break;
-          const float2 cs = cos_sin(A, (e + k) >> 1, b, t);
-          const float u = f[k], v = f[k + 1];
-          f[k] = fmaf(u, cs.x, -(v * cs.y));
-          f[k + 1] = fmaf(u, cs.y, v * cs.x);
-        }
-        store_part<DT>(T.out, out + e, A.part - e, pack<DT, 16>(f));
-      } else {
-        const int e = unit * V, n = half - e;
-        float u[V], v[V];
-        unpack<DT, 16>(load_part<DT>(T.in, in + e, n), u);
-        unpack<DT, 16>(load_part<DT>(T.in, in + half + e, n), v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          if (k >= n) break;
-          const float2 cs = cos_sin(A, e + k, b, t);
-          const float a = u[k];
-          u[k] = fmaf(a, cs.x, -(v[k] * cs.y));
-          v[k] = fmaf(a, cs.y, v[k] * cs.x);
-        }
-        store_part<DT>(T.out, out + e, n, pack<DT, 16>(u));
-        store_part<DT>(T.out, out + half + e, n, pack<DT, 16>(v));
-      }
-    }
+  extern __shared__ float2 turn[]; // [tokens of the block][pairs]
+  const int half = A.part / 2;
+  const uint32_t total = A.tokens * A.items; // below 2^31
+  const uint32_t base = blockIdx.x * kRotaryThreads, item = base + threadIdx.x;
+  const uint32_t row0 = fdiv(base, A.div_items), row = fdiv(item, A.div_items);
+  const uint32_t j = item - row * A.items, head = fdiv(j, A.div_units), unit = j - head * A.units;
+  const bool key = head >= (uint32_t)A.heads[0], turned = unit < (uint32_t)A.units_turned;
+  const RotaryTensor T = pick(A, key);
+  const int e = turned ? unit * V : A.part + (unit - A.units_turned) * V;
+  int64_t out = 0;
+  int count = 0; // elements to read and write (no more than a vector of them)
+  Vec<16> first, second;
+  if (item < total) {
+    const uint32_t b = fdiv(A.token0 + row, A.length), t = A.token0 + row - b * A.length.d;
+    const uint32_t h = key ? head - A.heads[0] : head;
+    const int64_t in = b * T.in_b + t * T.in_t + h * T.in_h + e;
+    out = b * T.out_b + t * T.out_t + h * T.out_h + e;
+    if (turned) count = (INTER ? A.part : half) - e;
+    else if (T.in != T.out) count = A.D - e; // what is not turned stays where it is in place
+    first = load_part<DT>(T.in, in, count);
+    if (!INTER && turned) second = load_part<DT>(T.in, in + half, count);
   }
+  const uint32_t rows = fdiv(min(base + kRotaryThreads, total) - 1, A.div_items) + 1 - row0;
+  for (uint32_t i = threadIdx.x; i < rows * half; i += kRotaryThreads) {
+    const uint32_t r = fdiv(i, A.div_half), token = A.token0 + row0 + r, b = fdiv(token, A.length);
+    turn[i] = cos_sin(A, i - r * half, b, token - b * A.length.d);
+  }
+  __syncthreads();
+  if (count <= 0) return;
+  if (turned) {
+    float u[V], v[V];
+    unpack<DT, 16>(first, u);
+    if constexpr (INTER) {
+      const float2 *cs = turn + (row - row0) * half + e / 2;
+#pragma unroll
+      for (int k = 0; k < V; k += 2)
+        if (k < count) {
+          const float2 c = cs[k / 2];
+          const float a = u[k];
+          u[k] = fmaf(a, c.x, -(u[k + 1] * c.y));
+          u[k + 1] = fmaf(a, c.y, u[k + 1] * c.x);
+        }
+    } else {
+      const float2 *cs = turn + (row - row0) * half + e;
+      unpack<DT, 16>(second, v);
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (k < count) {
+          const float2 c = cs[k];
+          const float a = u[k];
+          u[k] = fmaf(a, c.x, -(v[k] * c.y));
+          v[k] = fmaf(a, c.y, v[k] * c.x);
+        }
+      store_part<DT>(T.out, out + half, count, pack<DT, 16>(v));
+    }
+    first = pack<DT, 16>(u);
+  }
+  store_part<DT>(T.out, out, count, first);
 }
 
 template <int DT, bool INTER> hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st) {
-  const unsigned blocks = (unsigned)std::min<int64_t>(a.tokens, kMaxBlocksX);
-  hipLaunchKernelGGL((rotary_kernel<DT, INTER>), dim3(blocks), dim3(kRotaryThreads), 0, st, a);
+  const int64_t total = a.tokens * (int64_t)a.items;
+  // tokens that a block can touch; a token has at least half / V steps, so
+  // their angles are at most 64 KiB (for heads of up to 2^13 elements)
+  const int64_t rows = std::min<int64_t>((a.items - 1 + kRotaryThreads - 1) / a.items + 1, a.tokens);
+  hipLaunchKernelGGL((rotary_kernel<DT, INTER>), dim3((unsigned)((total + kRotaryThreads - 1) / kRotaryThreads)),
+                     dim3(kRotaryThreads), rows * (a.part / 2) * sizeof(float2), st, a);
   return hipGetLastError();
 }
 

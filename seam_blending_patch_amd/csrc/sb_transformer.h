@@ -81,11 +81,12 @@ struct RotaryTensor {
 struct RotaryArgs {
   RotaryTensor x[2];     // query heads, key heads
   int32_t heads[2];
-  int64_t tokens;        // batch * length
+  uint32_t token0, tokens; // of this launch, of all batch * length
   FastDiv length;
   int32_t D, part;       // head length, rotated elements (even)
   int32_t units_turned, units; // 16-byte steps of a head: over its pairs, and with those over the rest
-  FastDiv div_units;
+  int32_t items;         // steps of a token (all its heads)
+  FastDiv div_units, div_items, div_half;
   const double *freqs;   // radians per position, part / 2 of them
   const void *positions;
   int64_t pos_axis, pos_b, pos_t; // strides in elements

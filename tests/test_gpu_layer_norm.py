@@ -142,6 +142,19 @@ def test_three_axes_batch_slices_and_broadcast_rows(sb):
     check(sb, row, draw((6, 96), F16, 5), *weights(96, F16, 3), what="broadcast")
 
 
+@pytest.mark.parametrize("d", [128, 1001])
+def test_offsets_past_32_bits(sb, d):
+    far = torch.empty((1 << 31) + 4096, dtype=BF16, device="cuda")  # rows 2^30 elements apart
+    x = far.as_strided((3, d), (1 << 30, 1))
+    x.copy_(draw((3, d), BF16, 1))
+    near, dy = x.clone(), draw((3, d), BF16, 2)
+    want = [sb.layer_norm(near), *sb.layer_norm_backward(dy, near, weight_grads=True)]
+    got = [sb.layer_norm(x), *sb.layer_norm_backward(dy, x, weight_grads=True)]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    sb.layer_norm(x, out=x)
+    assert torch.equal(x, want[0])
+
+
 @pytest.mark.parametrize("offset", [1, 2, 3, 5])
 @pytest.mark.parametrize("d", [129, 1027])
 def test_odd_offsets(sb, offset, d):

@@ -113,6 +113,19 @@ def test_views_in_place_and_between_views(sb, interleaved):
     check(sb, q, k, positions, f, interleaved, what="head-major")
 
 
+def test_offsets_past_32_bits(sb):
+    f, _ = sb.rotary_frequencies(64)
+    far = torch.empty((1 << 31) + 4096, dtype=BF16, device="cuda")  # elements 2^30 and 2^31 bytes apart and more
+    q = far.as_strided((3, 2, 64), (1 << 30, 64, 1))
+    q.copy_(draw((3, 2, 64), BF16, 1))
+    near = q.clone()
+    positions = torch.tensor([5, 6, 7], device="cuda")
+    want = sb.rotary(near, positions, f)
+    assert torch.equal(sb.rotary(q, positions, f), want)
+    sb.rotary(q, positions, f, out=q)
+    assert torch.equal(q, want)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_odd_offsets_and_neighbours_untouched(sb, interleaved):
     f, _ = sb.rotary_frequencies(26)

@@ -3,21 +3,20 @@
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional, Sequence
 
 import torch
 
-from . import _DTYPE, _check, _lib, _stream_ptr, SeamBlendError
+from . import _DTYPE, _lib, SeamBlendError
+from ._call import call
 
-_i64p = ctypes.POINTER(ctypes.c_int64)
-_intp = ctypes.POINTER(ctypes.c_int)
-_ptr = ctypes.c_void_p
-_ptrp = ctypes.POINTER(ctypes.c_void_p)
-_lib.grad_norm_workspace_bytes.argtypes = [_i64p, ctypes.c_int64]
+_ptr = ctypes.c_void_p  # of the tables too, which are array.array's
+_lib.grad_norm_workspace_bytes.argtypes = [_ptr, ctypes.c_int64]
 _lib.grad_norm_workspace_bytes.restype = ctypes.c_size_t
-_lib.grad_norm.argtypes = [_ptrp, _i64p, _intp, ctypes.c_int64, _ptr, _ptr, ctypes.c_size_t, _ptr]
+_lib.grad_norm.argtypes = [_ptr, _ptr, _ptr, ctypes.c_int64, _ptr, _ptr, ctypes.c_size_t, _ptr]
 _lib.grad_norm.restype = ctypes.c_int
-_lib.grad_norm_clip.argtypes = [_ptrp, _ptrp, _i64p, _intp, _intp, ctypes.c_int64, ctypes.c_float, ctypes.c_float,
+_lib.grad_norm_clip.argtypes = [_ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_int64, ctypes.c_float, ctypes.c_float,
                                 _ptr, _ptr, ctypes.c_size_t, _ptr]
 _lib.grad_norm_clip.restype = ctypes.c_int
 
@@ -32,16 +31,61 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _table(tensors: Sequence[torch.Tensor], name: str, device):
-    codes = []
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE or t.device != device:
-            raise TypeError(f"{name} must be float32, float16 or bfloat16 tensors on one GPU")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{name} must be dense")
-        codes.append(_DTYPE[t.dtype])
-    n = len(codes)
-    return (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int * n)(*codes)
+def _table(tensors: Sequence[torch.Tensor], name: str, index: int):
+    """Pointers and dtype codes of the tensors, checked.  A list comprehension a
+    property: a model has hundreds of tensors."""
+    try:
+        codes = array("i", [_DTYPE[t.dtype] for t in tensors])
+        where = [t.get_device() for t in tensors]
+        whole = [t.is_contiguous() for t in tensors]
+        ptrs = array("Q", [t.data_ptr() for t in tensors])
+    except (AttributeError, KeyError):
+        codes = None
+    if codes is None or where.count(index) != len(where):
+        raise TypeError(f"{name} must be float32, float16 or bfloat16 tensors on one GPU")
+    if False in whole and not all(w or _dense(t) for w, t in zip(whole, tensors)):
+        raise ValueError(f"{name} must be dense")
+    return ptrs, codes, whole
+
+
+def _at(a: array) -> int:
+    return a.buffer_info()[0]
+
+
+def _clip(grads, max_norm, eps, out):
+    """(norm, outputs, device index, function, its name, its arguments, what they point to)"""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    if not isinstance(grads[0], torch.Tensor) or not grads[0].is_cuda:
+        raise TypeError("grads must be GPU (HIP) tensors")
+    index, n = grads[0].get_device(), len(grads)
+    ptrs, codes, whole = _table(grads, "grads", index)
+    numels = array("q", [t.numel() for t in grads])
+    outs = out_codes = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError("one output for each gradient")
+        outs, out_codes, out_whole = _table(out, "out", index)
+        if [t.shape for t in grads] != [t.shape for t in out] or any(
+                not (a and b) and g.stride() != o.stride() for a, b, g, o in zip(whole, out_whole, grads, out)):
+            raise ValueError("each output must have its gradient's shape and strides")
+        if out_codes != codes and any(a != b and b != 0 for a, b in zip(codes, out_codes)):
+            raise ValueError("each output must be of its gradient's dtype or float32")
+    need = _lib.grad_norm_workspace_bytes(_at(numels), n)
+    if need == 0:
+        raise SeamBlendError(-1, "grad_norm_workspace_bytes")
+    work = grads[0].new_empty(need // 4, dtype=torch.float32)
+    norm = grads[0].new_empty((), dtype=torch.float32)
+    tail = (norm.data_ptr(), work.data_ptr(), need)
+    keep = (ptrs, codes, numels, outs, out_codes, work)
+    out = grads if out is None else out
+    if max_norm is None:
+        return norm, out, index, _lib.grad_norm, "grad_norm", (_at(ptrs), _at(numels), _at(codes), n, *tail), keep
+    return norm, out, index, _lib.grad_norm_clip, "grad_norm_clip", (
+        _at(ptrs), None if outs is None else _at(outs), _at(numels), _at(codes),
+        None if outs is None else _at(out_codes), n, max_norm, eps, *tail), keep
 
 
 class GradNormClip:
@@ -52,49 +96,21 @@ class GradNormClip:
     def __init__(self, grads: Sequence[torch.Tensor], max_norm: Optional[float], eps: float = 1e-6,
                  out: Optional[Sequence[torch.Tensor]] = None):
         grads = list(grads)
-        if not grads:
-            raise ValueError("no gradients")
-        dev = grads[0].device
-        if dev.type != "cuda":
-            raise TypeError("grads must be GPU (HIP) tensors")
-        ptrs, codes = _table(grads, "grads", dev)
-        n = len(grads)
-        numels = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
-        outs = out_codes = None
-        if out is not None:
-            out = list(out)
-            if len(out) != n:
-                raise ValueError("one output for each gradient")
-            outs, out_codes = _table(out, "out", dev)
-            for g, o in zip(grads, out):
-                if g.shape != o.shape or (g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous())):
-                    raise ValueError("each output must have its gradient's shape and strides")
-                if o.dtype is not g.dtype and o.dtype is not torch.float32:
-                    raise ValueError("each output must be of its gradient's dtype or float32")
-        need = _lib.grad_norm_workspace_bytes(numels, n)
-        if need == 0:
-            raise SeamBlendError(-1, "grad_norm_workspace_bytes")
-        work = torch.empty(need // 4 + 4, dtype=torch.float32, device=dev)
-        self.norm, self.device, self.out = work[need // 4], dev, (grads if out is None else out)
-        self._keep = (grads, work)
-        tail = (self.norm.data_ptr(), work.data_ptr(), need)
-        if max_norm is None:
-            self._call, self._name, self._args = _lib.grad_norm, "grad_norm", (ptrs, numels, codes, n, *tail)
-        else:
-            self._call, self._name = _lib.grad_norm_clip, "grad_norm_clip"
-            self._args = (ptrs, outs, numels, codes, out_codes, n, max_norm, eps, *tail)
+        self.norm, self.out, index, self._function, self._name, self._args, keep = _clip(grads, max_norm, eps, out)
+        self.device = torch.device("cuda", index)
+        self._keep = (grads, keep)
 
     def __call__(self) -> torch.Tensor:
-        _check(self._call(*self._args, _stream_ptr(self.device)), self._name)
+        call(self._function, self._name, self.device.index, self._args)
         return self.norm
 
 
 def grad_norm(grads: Sequence[torch.Tensor]) -> torch.Tensor:
     """The 2-norm over every element of ``grads`` (dense GPU tensors, dtypes
     mixed as they come): a float32 scalar on the GPU, not waited for."""
-    plan = GradNormClip(grads, None)
-    with torch.cuda.device(plan.device):
-        return plan()
+    norm, _, index, function, name, args, keep = _clip(grads, None, 0.0, None)
+    call(function, name, index, args)
+    return norm
 
 
 def grad_norm_clip(grads: Sequence[torch.Tensor], max_norm: float, eps: float = 1e-6,
@@ -105,6 +121,6 @@ def grad_norm_clip(grads: Sequence[torch.Tensor], max_norm: float, eps: float = 
     optimizer takes).  Returns the norm before clipping, a float32 scalar on the
     GPU.  Nothing is waited for: a norm that is NaN or infinite shows in it and,
     as the formula says, in the gradients."""
-    plan = GradNormClip(grads, max_norm, eps, out)
-    with torch.cuda.device(plan.device):
-        return plan()
+    norm, _, index, function, name, args, keep = _clip(grads, max_norm, eps, out)
+    call(function, name, index, args)
+    return norm

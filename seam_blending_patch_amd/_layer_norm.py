@@ -3,11 +3,13 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
 
-from . import _DTYPE, _check, _lib, _stream_ptr, SeamBlendError
+from . import _DTYPE, _lib, SeamBlendError
+from ._call import call
 
 _i64 = ctypes.c_int64
 _i64p = ctypes.POINTER(_i64)
@@ -22,6 +24,7 @@ _lib.layer_norm_backward.argtypes = [_ptr, _i64p, _ptr, _i64p, _i64p, ctypes.c_f
 _lib.layer_norm_backward.restype = ctypes.c_int
 _2 = _i64 * 2
 _3 = _i64 * 3
+_DENSE = torch.contiguous_format
 
 
 def _require_rows(t: torch.Tensor, name: str):
@@ -37,13 +40,10 @@ def _outer_axes(*tensors: torch.Tensor):
     """The leading axes of tensors of one shape merged into at most two:
     (outer, inner) extents and each tensor's strides for them."""
     shape = tensors[0].shape
-    if all(t.is_contiguous() for t in tensors):
-        d = shape[-1]
-        return (1, tensors[0].numel() // d), [(0, d)] * len(tensors)
+    ext, strides = [], [[] for _ in tensors]
     for t in tensors:
         if t.stride(-1) != 1 and shape[-1] != 1:
             raise ValueError("the last axis must be contiguous")
-    ext, strides = [], [[] for _ in tensors]
     for k in range(len(shape) - 1):
         if shape[k] == 1:
             continue
@@ -59,23 +59,29 @@ def _outer_axes(*tensors: torch.Tensor):
     if len(ext) > 2:
         raise ValueError("the axes before the last must merge into at most two strided ones")
     pad = 2 - len(ext)
-    return (1,) * pad + tuple(ext), [(0,) * pad + tuple(s) for s in strides]
+    return _3(*(1,) * pad, *ext, shape[-1]), [_2(*(0,) * pad, *s) for s in strides]
 
 
-def _weights(x: torch.Tensor, **weights):
-    """The dtype code of the weights given (x's where there are none)."""
-    dtype = None
-    for name, t in weights.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor on x's device")
-        if t.numel() != x.shape[-1] or t.dtype not in (x.dtype, torch.float32):
-            raise ValueError(f"{name} must be [{x.shape[-1]}] of x's dtype or float32")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError("the weights and their gradients must be of one dtype")
-        dtype = t.dtype
-    return _DTYPE[x.dtype if dtype is None else dtype]
+def _geometry(*tensors: torch.Tensor):
+    """The library's shape and strides arguments for tensors of one shape."""
+    for t in tensors:
+        if not t.is_contiguous():
+            return _outer_axes(*tensors)
+    d = tensors[0].shape[-1]
+    s = _2(0, d)
+    return _3(1, tensors[0].numel() // d, d), (s,) * len(tensors)
+
+
+def _weight(x: torch.Tensor, d: int, t: torch.Tensor, name: str, dtype):
+    """Checks one weight or its gradient; the dtype it shares with the others."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != x.get_device() or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on x's device")
+    own = t.dtype
+    if t.numel() != d or (own is not x.dtype and own is not torch.float32):
+        raise ValueError(f"{name} must be [{d}] of x's dtype or float32")
+    if dtype is not None and own is not dtype:
+        raise ValueError("the weights and their gradients must be of one dtype")
+    return own
 
 
 def _like(x: torch.Tensor, t: torch.Tensor, name: str):
@@ -84,8 +90,22 @@ def _like(x: torch.Tensor, t: torch.Tensor, name: str):
         raise ValueError(f"{name} must match x")
 
 
-def _data(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _forward(x, gamma, beta, eps, out):
+    """(out, arguments of the library's call)"""
+    _require_rows(x, "x")
+    d, dtype, gp, bp = x.shape[-1], None, None, None
+    if gamma is not None:
+        dtype, gp = _weight(x, d, gamma, "gamma", dtype), gamma.data_ptr()
+    if beta is not None:
+        dtype, bp = _weight(x, d, beta, "beta", dtype), beta.data_ptr()
+    if out is None:
+        out = torch.empty_like(x, memory_format=_DENSE)
+    else:
+        _like(x, out, "out")
+    shape, (sx, so) = _geometry(x, out)
+    code = _DTYPE[x.dtype]
+    return out, (x.data_ptr(), sx, shape, eps, gp, bp, code, code if dtype is None else _DTYPE[dtype],
+                 out.data_ptr(), so)
 
 
 class LayerNorm:
@@ -94,20 +114,12 @@ class LayerNorm:
 
     def __init__(self, x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
                  eps: float = 1e-6, out: Optional[torch.Tensor] = None):
-        _require_rows(x, "x")
-        wdtype = _weights(x, gamma=gamma, beta=beta)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _like(x, out, "out")
-        ext, (sx, so) = _outer_axes(x, out)
-        self.out, self.device = out, x.device
+        self.out, self._args = _forward(x, gamma, beta, eps, out)
+        self.device = x.device
         self._keep = (x, gamma, beta)
-        self._args = (x.data_ptr(), _2(*sx), _3(*ext, x.shape[-1]), eps, _data(gamma), _data(beta), _DTYPE[x.dtype],
-                      wdtype, out.data_ptr(), _2(*so))
 
     def __call__(self) -> torch.Tensor:
-        _check(_lib.layer_norm_forward(*self._args, _stream_ptr(self.device)), "layer_norm_forward")
+        call(_lib.layer_norm_forward, "layer_norm_forward", self.device.index, self._args)
         return self.out
 
 
@@ -118,20 +130,66 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     once.  The last axis must be contiguous; the others may be strided (views
     of a packed projection) as long as they merge into two.  gamma / beta: [D]
     of x's dtype or float32, or None.  ``out`` may be ``x``."""
-    plan = LayerNorm(x, gamma, beta, eps, out)
-    with torch.cuda.device(plan.device):
-        return plan()
+    out, args = _forward(x, gamma, beta, eps, out)
+    call(_lib.layer_norm_forward, "layer_norm_forward", x.get_device(), args)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(index: int, rows: int, d: int, code: int) -> int:
+    with torch.cuda.device(index):
+        n = _lib.layer_norm_backward_workspace_bytes(_3(1, rows, d), code)
+    if n == 0:
+        raise SeamBlendError(-1, "layer_norm_backward_workspace_bytes")
+    return int(n)
 
 
 def layer_norm_backward_workspace_bytes(x: torch.Tensor) -> int:
     """Bytes of workspace layer_norm_backward needs for x."""
     _require_rows(x, "x")
     d = x.shape[-1]
-    with torch.cuda.device(x.device):
-        n = _lib.layer_norm_backward_workspace_bytes(_3(1, x.numel() // d, d), _DTYPE[x.dtype])
-    if n == 0:
-        raise SeamBlendError(-1, "layer_norm_backward_workspace_bytes")
-    return int(n)
+    return _workspace_bytes(x.get_device(), x.numel() // d, d, _DTYPE[x.dtype])
+
+
+def _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace):
+    """((dx, dgamma, dbeta), workspace, arguments of the library's call)"""
+    _require_rows(x, "x")
+    _like(x, dy, "dy")
+    if weight_grads is None:
+        weight_grads = gamma is not None or dgamma is not None or dbeta is not None
+    elif not weight_grads and (dgamma is not None or dbeta is not None):
+        raise ValueError("dgamma or dbeta given with weight_grads=False")
+    d, dtype, gp = x.shape[-1], None, None
+    if gamma is not None:
+        dtype, gp = _weight(x, d, gamma, "gamma", dtype), gamma.data_ptr()
+    if dgamma is not None:
+        dtype = _weight(x, d, dgamma, "dgamma", dtype)
+    if dbeta is not None:
+        dtype = _weight(x, d, dbeta, "dbeta", dtype)
+    if weight_grads:
+        if dtype is None:
+            dtype = torch.float32
+        if dgamma is None:
+            dgamma = x.new_empty(d, dtype=dtype)
+        if dbeta is None:
+            dbeta = x.new_empty(d, dtype=dtype)
+    if dx is None:
+        dx = torch.empty_like(x, memory_format=_DENSE)
+    else:
+        _like(x, dx, "dx")
+    code = _DTYPE[x.dtype]
+    need = _workspace_bytes(x.get_device(), x.numel() // d, d, code)
+    if workspace is None:
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    elif workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor on x's device")
+    else:
+        need = workspace.numel() * workspace.element_size()
+    shape, (sdy, sx, sdx) = _geometry(dy, x, dx)
+    return (dx, dgamma, dbeta), workspace, (
+        dy.data_ptr(), sdy, x.data_ptr(), sx, shape, eps, gp, code, code if dtype is None else _DTYPE[dtype],
+        dx.data_ptr(), sdx, None if dgamma is None else dgamma.data_ptr(),
+        None if dbeta is None else dbeta.data_ptr(), workspace.data_ptr(), need)
 
 
 class LayerNormBackward:
@@ -142,39 +200,12 @@ class LayerNormBackward:
                  dx: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
                  dbeta: Optional[torch.Tensor] = None, weight_grads: Optional[bool] = None,
                  workspace: Optional[torch.Tensor] = None):
-        _require_rows(x, "x")
-        _like(x, dy, "dy")
-        if weight_grads is None:
-            weight_grads = gamma is not None or dgamma is not None or dbeta is not None
-        wdtype = _weights(x, gamma=gamma, dgamma=dgamma, dbeta=dbeta)
-        if weight_grads:
-            given = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
-            wt = torch.float32 if given is None else given.dtype
-            wdtype = _DTYPE[wt]
-            if dgamma is None:
-                dgamma = torch.empty(x.shape[-1], dtype=wt, device=x.device)
-            if dbeta is None:
-                dbeta = torch.empty(x.shape[-1], dtype=wt, device=x.device)
-        elif dgamma is not None or dbeta is not None:
-            raise ValueError("dgamma or dbeta given with weight_grads=False")
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _like(x, dx, "dx")
-        need = layer_norm_backward_workspace_bytes(x)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        elif workspace.device != x.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous GPU tensor on x's device")
-        ext, (sdy, sx, sdx) = _outer_axes(dy, x, dx)
-        self.out, self.device = (dx, dgamma, dbeta), x.device
+        self.out, workspace, self._args = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
+        self.device = x.device
         self._keep = (dy, x, gamma, workspace)
-        self._args = (dy.data_ptr(), _2(*sdy), x.data_ptr(), _2(*sx), _3(*ext, x.shape[-1]), eps, _data(gamma),
-                      _DTYPE[x.dtype], wdtype, dx.data_ptr(), _2(*sdx), _data(dgamma), _data(dbeta),
-                      workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
     def __call__(self) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
-        _check(_lib.layer_norm_backward(*self._args, _stream_ptr(self.device)), "layer_norm_backward")
+        call(_lib.layer_norm_backward, "layer_norm_backward", self.device.index, self._args)
         return self.out
 
 
@@ -189,6 +220,6 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
     or one of them is given, None in their place otherwise.  They are written,
     not added to.  ``dx`` may be ``dy`` or ``x``.  ``workspace``: optional uint8
     GPU tensor of at least layer_norm_backward_workspace_bytes(x) bytes."""
-    plan = LayerNormBackward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
-    with torch.cuda.device(plan.device):
-        return plan()
+    out, workspace, args = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
+    call(_lib.layer_norm_backward, "layer_norm_backward", x.get_device(), args)
+    return out

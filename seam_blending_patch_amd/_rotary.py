@@ -8,7 +8,8 @@ from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from . import _DTYPE, _check, _lib, _stream_ptr
+from . import _DTYPE, _lib
+from ._call import call
 
 _i64 = ctypes.c_int64
 _i64p = ctypes.POINTER(_i64)
@@ -18,6 +19,7 @@ _lib.rotary_apply.argtypes = [_ptr, _i64p, _ptr, _i64p, _i64, _ptr, _i64p, _ptr,
                               ctypes.c_float, ctypes.c_int, _ptr]
 _lib.rotary_apply.restype = ctypes.c_int
 _3 = _i64 * 3
+_DENSE = torch.contiguous_format
 _NONE = _3(0, 0, 0)
 
 
@@ -67,23 +69,71 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
     return f.to(device), scale
 
 
-def _heads(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
+def _heads(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU (HIP) tensor")
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if t.dim() not in (3, 4):
         raise ValueError(f"{name} must be [B, T, heads, D] or [T, heads, D]")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"the last axis of {name} must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or t.dim() != like.dim()
-                             or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]):
-        raise ValueError(f"{name} must match q in all but its heads")
-
-
-def _strides(t: torch.Tensor):
     s = t.stride()
-    return _3(*s[:3]) if len(s) == 4 else _3(0, s[0], s[1])
+    if s[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return _3(s[0], s[1], s[2]) if len(s) == 4 else _3(0, s[0], s[1])
+
+
+def _like(t: torch.Tensor, name: str, like: torch.Tensor):
+    s = _heads(t, name)
+    if t.dtype != like.dtype or t.device != like.device or t.shape != like.shape:
+        raise ValueError(f"{name} must match {'k' if name == 'k_out' else 'q'}")
+    return s
+
+
+def _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, transpose):
+    """(outputs, arguments of the library's call)"""
+    q_strides = _heads(q, "q")
+    shape, index, dtype = q.shape, q.get_device(), q.dtype
+    batch, length = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    if not isinstance(freqs, torch.Tensor) or freqs.get_device() != index or freqs.dtype is not torch.float64 \
+            or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous 1-D float64 tensor on q's device")
+    if not isinstance(positions, torch.Tensor) or positions.get_device() != index \
+            or positions.dtype not in (torch.int64, torch.int32):
+        raise ValueError("positions must be an int64 or int32 tensor on q's device")
+    pairs = freqs.numel()
+    ps, pn = positions.stride(), positions.shape
+    if sections is None:
+        parts, ps, pn = (pairs,), (0, *ps), (1, *pn)
+    else:
+        parts = tuple(int(n) for n in sections)
+    if len(pn) not in (2, 3) or pn[0] != len(parts) or pn[-1] != length or (len(pn) == 3 and pn[1] not in (1, batch)):
+        raise ValueError("positions must be [T] or [B, T], with a leading axis for sections")
+    if out is None:
+        out = torch.empty_like(q, memory_format=_DENSE)
+        out_strides = _heads(out, "out")
+    else:
+        out_strides = _like(out, "out", q)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        k_args = (None, _NONE, None, _NONE, 0)
+    else:
+        k_strides = _heads(k, "k")
+        ks = k.shape
+        if k.dtype is not dtype or k.get_device() != index or ks[:-2] != shape[:-2] or ks[-1] != shape[-1]:
+            raise ValueError("k must match q in all but its heads")
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=_DENSE)
+            k_out_strides = _heads(k_out, "k_out")
+        else:
+            k_out_strides = _like(k_out, "k_out", k)
+        k_args = (k.data_ptr(), k_strides, k_out.data_ptr(), k_out_strides, ks[-2])
+    n = len(parts)
+    return (out if k is None else (out, k_out)), (
+        q.data_ptr(), q_strides, out.data_ptr(), out_strides, shape[-2], *k_args, _3(batch, length, shape[-1]),
+        _DTYPE[dtype], freqs.data_ptr(), 2 * pairs, 1 if interleaved else 0, positions.data_ptr(),
+        positions.element_size(), _3(ps[0], ps[1] if len(ps) == 3 and pn[1] > 1 else 0, ps[-1]), (_i64 * n)(*parts),
+        n, scale, 1 if transpose else 0)
 
 
 class Rotary:
@@ -95,49 +145,12 @@ class Rotary:
                  k: Optional[torch.Tensor] = None, interleaved: bool = False,
                  sections: Optional[Sequence[int]] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None,
                  k_out: Optional[torch.Tensor] = None, transpose: bool = False):
-        _heads(q, "q")
-        dev, dim = q.device, q.dim()
-        batch, length = (q.shape[0], q.shape[1]) if dim == 4 else (1, q.shape[0])
-        if not isinstance(freqs, torch.Tensor) or freqs.device != dev or freqs.dtype != torch.float64 \
-                or freqs.dim() != 1 or not freqs.is_contiguous():
-            raise ValueError("freqs must be a contiguous 1-D float64 tensor on q's device")
-        if not isinstance(positions, torch.Tensor) or positions.device != dev \
-                or positions.dtype not in (torch.int64, torch.int32):
-            raise ValueError("positions must be an int64 or int32 tensor on q's device")
-        parts = (freqs.numel(),) if sections is None else tuple(int(n) for n in sections)
-        p = positions if sections is not None else positions.unsqueeze(0)
-        if p.dim() not in (2, 3) or p.shape[0] != len(parts) or p.shape[-1] != length \
-                or (p.dim() == 3 and p.shape[1] not in (1, batch)):
-            raise ValueError("positions must be [T] or [B, T], with a leading axis for sections")
-        ps = p.stride()
-        pos_strides = _3(ps[0], ps[1] if p.dim() == 3 and p.shape[1] > 1 else 0, ps[-1])
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _heads(out, "out", q)
-            if out.shape != q.shape:
-                raise ValueError("out must match q")
-        k_args = (None, _NONE, None, _NONE, 0)
-        if k is not None:
-            _heads(k, "k", q)
-            if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-            else:
-                _heads(k_out, "k_out", k)
-                if k_out.shape != k.shape:
-                    raise ValueError("k_out must match k")
-            k_args = (k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out), k.shape[-2])
-        elif k_out is not None:
-            raise ValueError("k_out without k")
-        self.out, self.device = (out if k is None else (out, k_out)), dev
+        self.out, self._args = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, transpose)
+        self.device = q.device
         self._keep = (q, k, positions, freqs)
-        self._args = (q.data_ptr(), _strides(q), out.data_ptr(), _strides(out), q.shape[-2], *k_args,
-                      _3(batch, length, q.shape[-1]), _DTYPE[q.dtype], freqs.data_ptr(), 2 * freqs.numel(),
-                      int(bool(interleaved)), p.data_ptr(), p.element_size(), pos_strides,
-                      (_i64 * len(parts))(*parts), len(parts), scale, int(bool(transpose)))
 
     def __call__(self) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
-        _check(_lib.rotary_apply(*self._args, _stream_ptr(self.device)), "rotary_apply")
+        call(_lib.rotary_apply, "rotary_apply", self.device.index, self._args)
         return self.out
 
 
@@ -153,9 +166,9 @@ def rotary(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, k: Opt
     with ``sections`` (pair counts) a leading axis holds the positions each
     section turns by.  ``out`` / ``k_out`` may be ``q`` / ``k``.  Returns the
     turned q, or (q, k)."""
-    plan = Rotary(q, positions, freqs, k, interleaved, sections, scale, out, k_out)
-    with torch.cuda.device(plan.device):
-        return plan()
+    out, args = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, False)
+    call(_lib.rotary_apply, "rotary_apply", q.get_device(), args)
+    return out
 
 
 def rotary_backward(dq: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
@@ -164,6 +177,6 @@ def rotary_backward(dq: torch.Tensor, positions: torch.Tensor, freqs: torch.Tens
                     out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
     """Gradient of rotary: the gradients of its outputs (dq, and k's as ``k``)
     turned back.  Arguments as rotary's."""
-    plan = Rotary(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, transpose=True)
-    with torch.cuda.device(plan.device):
-        return plan()
+    out, args = _rotation(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, True)
+    call(_lib.rotary_apply, "rotary_apply", dq.get_device(), args)
+    return out

@@ -70,6 +70,13 @@ int check_types(int dtype, int wdtype, const void *const *weights, int n) {
   return SB_OK;
 }
 
+// Stores pass the caches where the output alone fills the last-level one:
+// 65536 x 2048 fp16 forward 99.4 -> 97.5 us, backward 155.5 -> 151.  Below that
+// the next operator finds the rows there.
+bool past_caches(const sb::LNArgs &a, int dtype) {
+  return a.rows * (int64_t)a.D * sb::elem_bytes(dtype) >= sb::kLastLevelBytes;
+}
+
 int check_eps(float eps) {
   return !(eps >= 0.0f) || eps == __builtin_inff() ? failf(SB_EARG, "eps must be finite and >= 0") : SB_OK;
 }
@@ -120,6 +127,7 @@ extern "C" int layer_norm_forward(const void *x, const int64_t x_stride[2], cons
   a.gamma = gamma;
   a.beta = beta;
   a.eps = eps;
+  a.far = past_caches(a, dtype);
   const hipError_t e = sb_launch_layer_norm(a, dtype, weight_dtype, (hipStream_t)stream);
   if (e != hipSuccess) return failf(SB_ELAUNCH, "layer norm launch failed: %s", hipGetErrorString(e));
   return SB_OK;
@@ -168,6 +176,7 @@ extern "C" int layer_norm_backward(const void *dy, const int64_t dy_stride[2], c
   a.dgamma = dgamma;
   a.dbeta = dbeta;
   a.eps = eps;
+  a.far = past_caches(a, dtype);
   a.part = wanted ? (float *)workspace : nullptr;
   a.rowstat = (float *)((char *)workspace + p.part_bytes);
   a.nparts = a.rows > 0 ? (int32_t)p.nparts : 0;

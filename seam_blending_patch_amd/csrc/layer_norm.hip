@@ -31,6 +31,9 @@ __device__ __forceinline__ int64_t row_offset(uint32_t row, const FastDiv &inner
 // as it has groups of LANES.
 // ---------------------------------------------------------------------------
 template <int LANES> constexpr int kRowThreads = LANES > kLNThreads ? LANES : kLNThreads;
+// Row lengths that have a kernel whose stores pass the caches, for outputs that
+// those could not hold (a branch at the store instead loses what it gains).
+template <int LANES> constexpr bool kFarRows = LANES >= 64;
 
 // A thread's vector u holds the elements of its row from (u * LANES + lane) * V
 // on.  Only rows that are no whole number of vectors (TAIL) have one cut by
@@ -47,7 +50,7 @@ __device__ __forceinline__ void subtract(float (&x)[NV][kVec<DT>], float m0, int
   }
 }
 
-template <int DT, int WDT, int LANES, int NV, bool TAIL>
+template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs A) {
   constexpr int V = kVec<DT>, GROUPS = kRowThreads<LANES> / LANES;
   __shared__ float lds[2][LANES > 64 ? 2 * kRowThreads<LANES> / 64 : 1];
@@ -91,7 +94,7 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
       if (A.beta) load_floats_row<WDT, V, TAIL>(A.beta, c, A.D - c, b);
 #pragma unroll
       for (int k = 0; k < V; ++k) x[u][k] = fmaf((x[u][k] - e) * r, A.gamma ? w[k] : 1.f, A.beta ? b[k] : 0.f);
-      if (here) store_row<DT, TAIL>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
+      if (here) store_row<DT, TAIL, NT>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
     }
   }
 }
@@ -100,7 +103,7 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
 // rows, a thread the same columns of each, so dgamma and dbeta add up in
 // registers; at the end the block's rows are merged and written as one block of
 // partials.  The next row's vectors are requested before this row's are used.
-template <int DT, int WDT, int LANES, int NV, bool TAIL>
+template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const LNArgs A) {
   constexpr int V = kVec<DT>, T = kRowThreads<LANES>, GROUPS = T / LANES, COLS = LANES * NV * V;
   // partials to merge: one of each wave, or of each group where that is wider
@@ -177,7 +180,7 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
         db[u][k] += g[u][k];
         x[u][k] = r * (fmaf(-h, mgh, g[u][k] * w[u][k]) - mg);
       }
-      if (row < A.rows) store_row<DT, TAIL>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
+      if (row < A.rows) store_row<DT, TAIL, NT>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
     }
   }
   if (!A.part) return;
@@ -390,8 +393,10 @@ __global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const LNArgs 
 template <int DT, int WDT, int LANES, int NV> hipError_t launch_rows(const LNArgs &a, hipStream_t st) {
   constexpr int T = kRowThreads<LANES>, GROUPS = T / LANES;
   const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + GROUPS - 1) / GROUPS, kMaxBlocksX / (T / kLNThreads));
-  if (a.D % kVec<DT>) hipLaunchKernelGGL((ln_row_kernel<DT, WDT, LANES, NV, true>), dim3(blocks), dim3(T), 0, st, a);
-  else hipLaunchKernelGGL((ln_row_kernel<DT, WDT, LANES, NV, false>), dim3(blocks), dim3(T), 0, st, a);
+  const auto kernel = a.D % kVec<DT>               ? ln_row_kernel<DT, WDT, LANES, NV, true>
+                      : kFarRows<LANES> && a.far ? ln_row_kernel<DT, WDT, LANES, NV, false, kFarRows<LANES>>
+                                                 : ln_row_kernel<DT, WDT, LANES, NV, false>;
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(T), 0, st, a);
   return hipGetLastError();
 }
 
@@ -425,10 +430,10 @@ template <int WDT, int LANES, int V> hipError_t launch_reduce(const LNArgs &a, h
 template <int DT, int WDT, int LANES, int NV> hipError_t launch_backward_rows(const LNArgs &a, hipStream_t st) {
   constexpr int T = kRowThreads<LANES>;
   if (a.nparts > 0) {
-    if (a.D % kVec<DT>)
-      hipLaunchKernelGGL((ln_backward_kernel<DT, WDT, LANES, NV, true>), dim3(a.nparts), dim3(T), 0, st, a);
-    else
-      hipLaunchKernelGGL((ln_backward_kernel<DT, WDT, LANES, NV, false>), dim3(a.nparts), dim3(T), 0, st, a);
+    const auto kernel = a.D % kVec<DT>               ? ln_backward_kernel<DT, WDT, LANES, NV, true>
+                        : kFarRows<LANES> && a.far ? ln_backward_kernel<DT, WDT, LANES, NV, false, kFarRows<LANES>>
+                                                   : ln_backward_kernel<DT, WDT, LANES, NV, false>;
+    hipLaunchKernelGGL(kernel, dim3(a.nparts), dim3(T), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

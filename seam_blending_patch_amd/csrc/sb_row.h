@@ -39,11 +39,15 @@ template <int DT> __device__ __forceinline__ Vec<16> load_part(const void *p, in
   return v;
 }
 
-template <int DT> __device__ __forceinline__ void store_part(void *p, int64_t e0, int n, const Vec<16> &v) {
+// NT: a store past the caches, for results that they could not hold anyway
+template <int DT, bool NT = false>
+__device__ __forceinline__ void store_part(void *p, int64_t e0, int n, const Vec<16> &v) {
   typedef typename El<DT>::bits bits;
   if (n >= kVec<DT>) {
     const u32x4 q = {v.w[0], v.w[1], v.w[2], v.w[3]};
-    *reinterpret_cast<typename El<DT>::vec *>((bits *)p + e0) = q;
+    typename El<DT>::vec *at = reinterpret_cast<typename El<DT>::vec *>((bits *)p + e0);
+    if constexpr (NT) __builtin_nontemporal_store(q, at);
+    else *at = q;
   } else {
 #pragma unroll
     for (int k = 0; k < kVec<DT>; ++k)
@@ -59,9 +63,9 @@ template <int DT> __device__ __forceinline__ void store_part(void *p, int64_t e0
 template <int DT, bool TAIL> __device__ __forceinline__ Vec<16> load_row(const void *p, int64_t e0, int n) {
   return load_part<DT>(p, e0, TAIL ? n : n > 0 ? kVec<DT> : 0);
 }
-template <int DT, bool TAIL>
+template <int DT, bool TAIL, bool NT = false>
 __device__ __forceinline__ void store_row(void *p, int64_t e0, int n, const Vec<16> &v) {
-  store_part<DT>(p, e0, TAIL ? n : n > 0 ? kVec<DT> : 0, v);
+  store_part<DT, NT>(p, e0, TAIL ? n : n > 0 ? kVec<DT> : 0, v);
 }
 
 // N consecutive values of type DT (n of them present, zeros after) as fp32

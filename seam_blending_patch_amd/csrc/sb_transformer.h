@@ -7,6 +7,8 @@
 
 namespace sb {
 
+constexpr int64_t kLastLevelBytes = (int64_t)256 << 20; // the memory-side cache
+
 // ---------------------------------------------------------------------------
 // layer norm
 // ---------------------------------------------------------------------------
@@ -25,6 +27,7 @@ struct LNArgs {
   FastDiv inner;
   int32_t D;
   float eps, inv_d;
+  int32_t far;        // the output is more than the caches hold
   // backward
   float *part;        // weight-gradient partials [blocks][2][columns] (nullptr: none wanted)
   float *rowstat;     // per row: mean, 1/sigma, mean of g, mean of g h (the looping kernels)
@@ -109,7 +112,7 @@ struct ClipArgs {
   uint8_t types[kClipTensors];      // dtype, and dtype of the output << 2
   int64_t chunk;                    // elements of a chunk (a multiple of kClipThreads vectors)
   double *partials;                 // sums of squares: this launch's first, or all of them (second pass)
-  int32_t tensors, npartials;
+  int32_t tensors, npartials, nt;   // nt: store the outputs past the caches
   float max_norm, eps;
   float *norm;                      // written by the first block of a second-pass launch that has it
 };

@@ -2,15 +2,25 @@
 its current stream."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _check
 
-_current_device = torch.cuda.current_device
+# the current device without a check that HIP is initialised: tensors are on it
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # the current stream as a plain number, without a Stream object around it (2 us
 # of a call of 7)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) \
     or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+@functools.lru_cache(maxsize=512)
+def like(index: int, n: int, dtype: torch.dtype) -> torch.Tensor:
+    """n elements on a device that take the memory of one, to be given to
+    torch.empty_like (half the time of torch.empty with a size and a dtype)."""
+    return torch.empty(1, dtype=dtype, device=f"cuda:{index}").expand(n)
 
 
 def call(function, name: str, index: int, args):

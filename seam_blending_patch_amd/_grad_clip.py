@@ -9,7 +9,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _DTYPE, _lib, SeamBlendError
-from ._call import call
+from ._call import call, like
 
 _ptr = ctypes.c_void_p  # of the tables too, which are array.array's
 _lib.grad_norm_workspace_bytes.argtypes = [_ptr, ctypes.c_int64]
@@ -32,14 +32,14 @@ def _dense(t: torch.Tensor) -> bool:
 
 
 def _table(tensors: Sequence[torch.Tensor], name: str, index: int):
-    """Pointers and dtype codes of the tensors, checked.  A list comprehension a
-    property: a model has hundreds of tensors."""
+    """Pointers and dtype codes of the tensors, checked, a pass over them for a
+    property: a model has hundreds."""
     try:
         codes = array("i", [_DTYPE[t.dtype] for t in tensors])
-        where = [t.get_device() for t in tensors]
-        whole = [t.is_contiguous() for t in tensors]
-        ptrs = array("Q", [t.data_ptr() for t in tensors])
-    except (AttributeError, KeyError):
+        where = list(map(torch.Tensor.get_device, tensors))
+        whole = list(map(torch.Tensor.is_contiguous, tensors))
+        ptrs = array("Q", list(map(torch.Tensor.data_ptr, tensors)))
+    except (AttributeError, KeyError, TypeError):
         codes = None
     if codes is None or where.count(index) != len(where):
         raise TypeError(f"{name} must be float32, float16 or bfloat16 tensors on one GPU")
@@ -61,7 +61,7 @@ def _clip(grads, max_norm, eps, out):
         raise TypeError("grads must be GPU (HIP) tensors")
     index, n = grads[0].get_device(), len(grads)
     ptrs, codes, whole = _table(grads, "grads", index)
-    numels = array("q", [t.numel() for t in grads])
+    numels = array("q", list(map(torch.Tensor.numel, grads)))
     outs = out_codes = None
     if out is not None:
         out = list(out)
@@ -76,8 +76,8 @@ def _clip(grads, max_norm, eps, out):
     need = _lib.grad_norm_workspace_bytes(_at(numels), n)
     if need == 0:
         raise SeamBlendError(-1, "grad_norm_workspace_bytes")
-    work = grads[0].new_empty(need // 4, dtype=torch.float32)
-    norm = grads[0].new_empty((), dtype=torch.float32)
+    work = torch.empty_like(like(index, need, torch.uint8), memory_format=torch.contiguous_format)
+    norm = torch.empty_like(like(index, 1, torch.float32).squeeze(0))
     tail = (norm.data_ptr(), work.data_ptr(), need)
     keep = (ptrs, codes, numels, outs, out_codes, work)
     out = grads if out is None else out

@@ -4,41 +4,42 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from array import array
 from typing import Optional, Tuple
 
 import torch
 
 from . import _DTYPE, _lib, SeamBlendError
-from ._call import call
+from ._call import call, like
 
-_i64 = ctypes.c_int64
-_i64p = ctypes.POINTER(_i64)
-_ptr = ctypes.c_void_p
-_lib.layer_norm_forward.argtypes = [_ptr, _i64p, _i64p, ctypes.c_float, _ptr, _ptr, ctypes.c_int, ctypes.c_int, _ptr,
-                                    _i64p, _ptr]
+_ptr = ctypes.c_void_p  # of shapes and strides too: places in one array.array
+_lib.layer_norm_forward.argtypes = [_ptr, _ptr, _ptr, ctypes.c_float, _ptr, _ptr, ctypes.c_int, ctypes.c_int, _ptr,
+                                    _ptr, _ptr]
 _lib.layer_norm_forward.restype = ctypes.c_int
-_lib.layer_norm_backward_workspace_bytes.argtypes = [_i64p, ctypes.c_int]
+_lib.layer_norm_backward_workspace_bytes.argtypes = [_ptr, ctypes.c_int]
 _lib.layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
-_lib.layer_norm_backward.argtypes = [_ptr, _i64p, _ptr, _i64p, _i64p, ctypes.c_float, _ptr, ctypes.c_int,
-                                     ctypes.c_int, _ptr, _i64p, _ptr, _ptr, _ptr, ctypes.c_size_t, _ptr]
+_lib.layer_norm_backward.argtypes = [_ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_float, _ptr, ctypes.c_int,
+                                     ctypes.c_int, _ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_size_t, _ptr]
 _lib.layer_norm_backward.restype = ctypes.c_int
-_2 = _i64 * 2
-_3 = _i64 * 3
 _DENSE = torch.contiguous_format
 
 
-def _require_rows(t: torch.Tensor, name: str):
+def _rows(t: torch.Tensor, name: str):
+    """(shape, dtype code) of a tensor of rows"""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU (HIP) tensor")
-    if t.dtype not in _DTYPE:
+    code = _DTYPE.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() < 1 or t.shape[-1] < 1:
+    shape = t.shape
+    if not shape or shape[-1] < 1:
         raise ValueError(f"{name} must have a last axis of at least one element")
+    return shape, code
 
 
-def _outer_axes(*tensors: torch.Tensor):
+def _outer_axes(tensors):
     """The leading axes of tensors of one shape merged into at most two:
-    (outer, inner) extents and each tensor's strides for them."""
+    (outer, inner, D), then each tensor's strides for the two."""
     shape = tensors[0].shape
     ext, strides = [], [[] for _ in tensors]
     for t in tensors:
@@ -58,54 +59,52 @@ def _outer_axes(*tensors: torch.Tensor):
                 s.append(h)
     if len(ext) > 2:
         raise ValueError("the axes before the last must merge into at most two strided ones")
-    pad = 2 - len(ext)
-    return _3(*(1,) * pad, *ext, shape[-1]), [_2(*(0,) * pad, *s) for s in strides]
+    pad = [0] * (2 - len(ext))
+    return array("q", [1] * len(pad) + ext + [shape[-1]] + [v for s in strides for v in pad + s])
 
 
-def _geometry(*tensors: torch.Tensor):
-    """The library's shape and strides arguments for tensors of one shape."""
+def _geometry(d: int, *tensors: torch.Tensor):
+    """The library's shape and strides for tensors of one shape, in one array:
+    the shape at its start, the k-th tensor's strides 24 + 16 k bytes on."""
     for t in tensors:
         if not t.is_contiguous():
-            return _outer_axes(*tensors)
-    d = tensors[0].shape[-1]
-    s = _2(0, d)
-    return _3(1, tensors[0].numel() // d, d), (s,) * len(tensors)
+            return _outer_axes(tensors)
+    return array("q", (1, t.numel() // d, d, 0, d, 0, d, 0, d))
 
 
-def _weight(x: torch.Tensor, d: int, t: torch.Tensor, name: str, dtype):
+def _weight(t: torch.Tensor, name: str, d: int, x_dtype, index: int, dtype):
     """Checks one weight or its gradient; the dtype it shares with the others."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != x.get_device() or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on x's device")
     own = t.dtype
-    if t.numel() != d or (own is not x.dtype and own is not torch.float32):
+    if t.numel() != d or (own is not x_dtype and own is not torch.float32):
         raise ValueError(f"{name} must be [{d}] of x's dtype or float32")
     if dtype is not None and own is not dtype:
         raise ValueError("the weights and their gradients must be of one dtype")
     return own
 
 
-def _like(x: torch.Tensor, t: torch.Tensor, name: str):
-    _require_rows(t, name)
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+def _like(t: torch.Tensor, name: str, shape, code: int, index: int):
+    if _rows(t, name) != (shape, code) or t.get_device() != index:
         raise ValueError(f"{name} must match x")
 
 
 def _forward(x, gamma, beta, eps, out):
-    """(out, arguments of the library's call)"""
-    _require_rows(x, "x")
-    d, dtype, gp, bp = x.shape[-1], None, None, None
+    """(out, device index, arguments of the library's call, what they point to)"""
+    shape, code = _rows(x, "x")
+    index, d, dtype, gp, bp = x.get_device(), shape[-1], None, None, None
     if gamma is not None:
-        dtype, gp = _weight(x, d, gamma, "gamma", dtype), gamma.data_ptr()
+        dtype, gp = _weight(gamma, "gamma", d, x.dtype, index, None), gamma.data_ptr()
     if beta is not None:
-        dtype, bp = _weight(x, d, beta, "beta", dtype), beta.data_ptr()
+        dtype, bp = _weight(beta, "beta", d, x.dtype, index, dtype), beta.data_ptr()
     if out is None:
         out = torch.empty_like(x, memory_format=_DENSE)
     else:
-        _like(x, out, "out")
-    shape, (sx, so) = _geometry(x, out)
-    code = _DTYPE[x.dtype]
-    return out, (x.data_ptr(), sx, shape, eps, gp, bp, code, code if dtype is None else _DTYPE[dtype],
-                 out.data_ptr(), so)
+        _like(out, "out", shape, code, index)
+    geometry = _geometry(d, x, out)
+    at = geometry.buffer_info()[0]
+    return out, index, (x.data_ptr(), at + 24, at, eps, gp, bp, code, code if dtype is None else _DTYPE[dtype],
+                        out.data_ptr(), at + 40), geometry
 
 
 class LayerNorm:
@@ -114,9 +113,9 @@ class LayerNorm:
 
     def __init__(self, x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
                  eps: float = 1e-6, out: Optional[torch.Tensor] = None):
-        self.out, self._args = _forward(x, gamma, beta, eps, out)
+        self.out, _, self._args, geometry = _forward(x, gamma, beta, eps, out)
         self.device = x.device
-        self._keep = (x, gamma, beta)
+        self._keep = (x, gamma, beta, geometry)
 
     def __call__(self) -> torch.Tensor:
         call(_lib.layer_norm_forward, "layer_norm_forward", self.device.index, self._args)
@@ -130,15 +129,16 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     once.  The last axis must be contiguous; the others may be strided (views
     of a packed projection) as long as they merge into two.  gamma / beta: [D]
     of x's dtype or float32, or None.  ``out`` may be ``x``."""
-    out, args = _forward(x, gamma, beta, eps, out)
-    call(_lib.layer_norm_forward, "layer_norm_forward", x.get_device(), args)
+    out, index, args, geometry = _forward(x, gamma, beta, eps, out)
+    call(_lib.layer_norm_forward, "layer_norm_forward", index, args)
     return out
 
 
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(index: int, rows: int, d: int, code: int) -> int:
     with torch.cuda.device(index):
-        n = _lib.layer_norm_backward_workspace_bytes(_3(1, rows, d), code)
+        shape = array("q", (1, rows, d))
+        n = _lib.layer_norm_backward_workspace_bytes(shape.buffer_info()[0], code)
     if n == 0:
         raise SeamBlendError(-1, "layer_norm_backward_workspace_bytes")
     return int(n)
@@ -146,50 +146,49 @@ def _workspace_bytes(index: int, rows: int, d: int, code: int) -> int:
 
 def layer_norm_backward_workspace_bytes(x: torch.Tensor) -> int:
     """Bytes of workspace layer_norm_backward needs for x."""
-    _require_rows(x, "x")
-    d = x.shape[-1]
-    return _workspace_bytes(x.get_device(), x.numel() // d, d, _DTYPE[x.dtype])
+    shape, code = _rows(x, "x")
+    return _workspace_bytes(x.get_device(), x.numel() // shape[-1], shape[-1], code)
 
 
 def _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace):
-    """((dx, dgamma, dbeta), workspace, arguments of the library's call)"""
-    _require_rows(x, "x")
-    _like(x, dy, "dy")
+    """((dx, dgamma, dbeta), device index, arguments of the library's call, what they point to)"""
+    shape, code = _rows(x, "x")
+    index, d, x_dtype, dtype, gp = x.get_device(), shape[-1], x.dtype, None, None
+    _like(dy, "dy", shape, code, index)
     if weight_grads is None:
         weight_grads = gamma is not None or dgamma is not None or dbeta is not None
     elif not weight_grads and (dgamma is not None or dbeta is not None):
         raise ValueError("dgamma or dbeta given with weight_grads=False")
-    d, dtype, gp = x.shape[-1], None, None
     if gamma is not None:
-        dtype, gp = _weight(x, d, gamma, "gamma", dtype), gamma.data_ptr()
+        dtype, gp = _weight(gamma, "gamma", d, x_dtype, index, None), gamma.data_ptr()
     if dgamma is not None:
-        dtype = _weight(x, d, dgamma, "dgamma", dtype)
+        dtype = _weight(dgamma, "dgamma", d, x_dtype, index, dtype)
     if dbeta is not None:
-        dtype = _weight(x, d, dbeta, "dbeta", dtype)
+        dtype = _weight(dbeta, "dbeta", d, x_dtype, index, dtype)
     if weight_grads:
         if dtype is None:
             dtype = torch.float32
         if dgamma is None:
-            dgamma = x.new_empty(d, dtype=dtype)
+            dgamma = torch.empty_like(like(index, d, dtype), memory_format=_DENSE)
         if dbeta is None:
-            dbeta = x.new_empty(d, dtype=dtype)
+            dbeta = torch.empty_like(like(index, d, dtype), memory_format=_DENSE)
     if dx is None:
         dx = torch.empty_like(x, memory_format=_DENSE)
     else:
-        _like(x, dx, "dx")
-    code = _DTYPE[x.dtype]
-    need = _workspace_bytes(x.get_device(), x.numel() // d, d, code)
+        _like(dx, "dx", shape, code, index)
     if workspace is None:
-        workspace = x.new_empty(need, dtype=torch.uint8)
-    elif workspace.device != x.device or not workspace.is_contiguous():
+        need = _workspace_bytes(index, x.numel() // d, d, code)
+        workspace = torch.empty_like(like(index, need, torch.uint8), memory_format=_DENSE)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor on x's device")
     else:
         need = workspace.numel() * workspace.element_size()
-    shape, (sdy, sx, sdx) = _geometry(dy, x, dx)
-    return (dx, dgamma, dbeta), workspace, (
-        dy.data_ptr(), sdy, x.data_ptr(), sx, shape, eps, gp, code, code if dtype is None else _DTYPE[dtype],
-        dx.data_ptr(), sdx, None if dgamma is None else dgamma.data_ptr(),
-        None if dbeta is None else dbeta.data_ptr(), workspace.data_ptr(), need)
+    geometry = _geometry(d, dy, x, dx)
+    at = geometry.buffer_info()[0]
+    return (dx, dgamma, dbeta), index, (
+        dy.data_ptr(), at + 24, x.data_ptr(), at + 40, at, eps, gp, code, code if dtype is None else _DTYPE[dtype],
+        dx.data_ptr(), at + 56, None if dgamma is None else dgamma.data_ptr(),
+        None if dbeta is None else dbeta.data_ptr(), workspace.data_ptr(), need), (geometry, workspace)
 
 
 class LayerNormBackward:
@@ -200,9 +199,9 @@ class LayerNormBackward:
                  dx: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
                  dbeta: Optional[torch.Tensor] = None, weight_grads: Optional[bool] = None,
                  workspace: Optional[torch.Tensor] = None):
-        self.out, workspace, self._args = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
+        self.out, _, self._args, keep = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
         self.device = x.device
-        self._keep = (dy, x, gamma, workspace)
+        self._keep = (dy, x, gamma, keep)
 
     def __call__(self) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
         call(_lib.layer_norm_backward, "layer_norm_backward", self.device.index, self._args)
@@ -220,6 +219,6 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
     or one of them is given, None in their place otherwise.  They are written,
     not added to.  ``dx`` may be ``dy`` or ``x``.  ``workspace``: optional uint8
     GPU tensor of at least layer_norm_backward_workspace_bytes(x) bytes."""
-    out, workspace, args = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
-    call(_lib.layer_norm_backward, "layer_norm_backward", x.get_device(), args)
+    out, index, args, keep = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
+    call(_lib.layer_norm_backward, "layer_norm_backward", index, args)
     return out

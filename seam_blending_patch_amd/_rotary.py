@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from array import array
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
@@ -12,15 +13,12 @@ from . import _DTYPE, _lib
 from ._call import call
 
 _i64 = ctypes.c_int64
-_i64p = ctypes.POINTER(_i64)
-_ptr = ctypes.c_void_p
-_lib.rotary_apply.argtypes = [_ptr, _i64p, _ptr, _i64p, _i64, _ptr, _i64p, _ptr, _i64p, _i64, _i64p, ctypes.c_int,
-                              _ptr, _i64, ctypes.c_int, _ptr, ctypes.c_int, _i64p, _i64p, ctypes.c_int,
+_ptr = ctypes.c_void_p  # of shapes, strides and sections too: places in one array.array
+_lib.rotary_apply.argtypes = [_ptr, _ptr, _ptr, _ptr, _i64, _ptr, _ptr, _ptr, _ptr, _i64, _ptr, ctypes.c_int,
+                              _ptr, _i64, ctypes.c_int, _ptr, ctypes.c_int, _ptr, _ptr, ctypes.c_int,
                               ctypes.c_float, ctypes.c_int, _ptr]
 _lib.rotary_apply.restype = ctypes.c_int
-_3 = _i64 * 3
 _DENSE = torch.contiguous_format
-_NONE = _3(0, 0, 0)
 
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -70,29 +68,36 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
 
 
 def _heads(t: torch.Tensor, name: str):
+    """(shape, strides [B, T, heads]) of a tensor of heads"""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU (HIP) tensor")
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() not in (3, 4):
+    shape, s = t.shape, t.stride()
+    n = len(s)
+    if n != 3 and n != 4:
         raise ValueError(f"{name} must be [B, T, heads, D] or [T, heads, D]")
-    s = t.stride()
-    if s[-1] != 1 and t.shape[-1] != 1:
+    if s[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return _3(s[0], s[1], s[2]) if len(s) == 4 else _3(0, s[0], s[1])
+    return shape, s[:3] if n == 4 else (0, s[0], s[1])
 
 
-def _like(t: torch.Tensor, name: str, like: torch.Tensor):
-    s = _heads(t, name)
-    if t.dtype != like.dtype or t.device != like.device or t.shape != like.shape:
+def _output(like: torch.Tensor, shape, out: Optional[torch.Tensor], name: str):
+    """(output, its strides)"""
+    if out is None:
+        out = torch.empty_like(like, memory_format=_DENSE)
+        s = out.stride()
+        return out, s[:3] if len(s) == 4 else (0, s[0], s[1])
+    out_shape, s = _heads(out, name)
+    if out.dtype != like.dtype or out.device != like.device or out_shape != shape:
         raise ValueError(f"{name} must match {'k' if name == 'k_out' else 'q'}")
-    return s
+    return out, s
 
 
 def _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, transpose):
-    """(outputs, arguments of the library's call)"""
-    q_strides = _heads(q, "q")
-    shape, index, dtype = q.shape, q.get_device(), q.dtype
+    """(outputs, device index, arguments of the library's call, what they point to)"""
+    shape, q_strides = _heads(q, "q")
+    index, dtype = q.get_device(), q.dtype
     batch, length = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
     if not isinstance(freqs, torch.Tensor) or freqs.get_device() != index or freqs.dtype is not torch.float64 \
             or freqs.dim() != 1 or not freqs.is_contiguous():
@@ -100,40 +105,40 @@ def _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, 
     if not isinstance(positions, torch.Tensor) or positions.get_device() != index \
             or positions.dtype not in (torch.int64, torch.int32):
         raise ValueError("positions must be an int64 or int32 tensor on q's device")
-    pairs = freqs.numel()
-    ps, pn = positions.stride(), positions.shape
+    pairs, ps, pn = freqs.numel(), positions.stride(), positions.shape
     if sections is None:
         parts, ps, pn = (pairs,), (0, *ps), (1, *pn)
     else:
-        parts = tuple(int(n) for n in sections)
+        parts = tuple(sections)
     if len(pn) not in (2, 3) or pn[0] != len(parts) or pn[-1] != length or (len(pn) == 3 and pn[1] not in (1, batch)):
         raise ValueError("positions must be [T] or [B, T], with a leading axis for sections")
-    if out is None:
-        out = torch.empty_like(q, memory_format=_DENSE)
-        out_strides = _heads(out, "out")
-    else:
-        out_strides = _like(out, "out", q)
+    out, out_strides = _output(q, shape, out, "out")
+    # shape at 0, then strides of positions, q, its output, k, its output, then sections
+    numbers = [batch, length, shape[-1], ps[0], ps[1] if len(ps) == 3 and pn[1] > 1 else 0, ps[-1], *q_strides,
+               *out_strides]
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
-        k_args = (None, _NONE, None, _NONE, 0)
+        numbers += parts
+        table = array("q", numbers)
+        at = table.buffer_info()[0]
+        k_args = (None, None, None, None, 0)
     else:
-        k_strides = _heads(k, "k")
-        ks = k.shape
-        if k.dtype is not dtype or k.get_device() != index or ks[:-2] != shape[:-2] or ks[-1] != shape[-1]:
+        k_shape, k_strides = _heads(k, "k")
+        if k.dtype is not dtype or k.get_device() != index or k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
             raise ValueError("k must match q in all but its heads")
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=_DENSE)
-            k_out_strides = _heads(k_out, "k_out")
-        else:
-            k_out_strides = _like(k_out, "k_out", k)
-        k_args = (k.data_ptr(), k_strides, k_out.data_ptr(), k_out_strides, ks[-2])
+        k_out, k_out_strides = _output(k, k_shape, k_out, "k_out")
+        numbers += k_strides
+        numbers += k_out_strides
+        numbers += parts
+        table = array("q", numbers)
+        at = table.buffer_info()[0]
+        k_args = (k.data_ptr(), at + 96, k_out.data_ptr(), at + 120, k_shape[-2])
     n = len(parts)
-    return (out if k is None else (out, k_out)), (
-        q.data_ptr(), q_strides, out.data_ptr(), out_strides, shape[-2], *k_args, _3(batch, length, shape[-1]),
-        _DTYPE[dtype], freqs.data_ptr(), 2 * pairs, 1 if interleaved else 0, positions.data_ptr(),
-        positions.element_size(), _3(ps[0], ps[1] if len(ps) == 3 and pn[1] > 1 else 0, ps[-1]), (_i64 * n)(*parts),
-        n, scale, 1 if transpose else 0)
+    return (out if k is None else (out, k_out)), index, (
+        q.data_ptr(), at + 48, out.data_ptr(), at + 72, shape[-2], *k_args, at, _DTYPE[dtype], freqs.data_ptr(),
+        2 * pairs, 1 if interleaved else 0, positions.data_ptr(), positions.element_size(), at + 24,
+        at + 8 * (len(numbers) - n), n, scale, 1 if transpose else 0), table
 
 
 class Rotary:
@@ -145,9 +150,10 @@ class Rotary:
                  k: Optional[torch.Tensor] = None, interleaved: bool = False,
                  sections: Optional[Sequence[int]] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None,
                  k_out: Optional[torch.Tensor] = None, transpose: bool = False):
-        self.out, self._args = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, transpose)
+        self.out, _, self._args, table = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out,
+                                                   transpose)
         self.device = q.device
-        self._keep = (q, k, positions, freqs)
+        self._keep = (q, k, positions, freqs, table)
 
     def __call__(self) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
         call(_lib.rotary_apply, "rotary_apply", self.device.index, self._args)
@@ -166,8 +172,8 @@ def rotary(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, k: Opt
     with ``sections`` (pair counts) a leading axis holds the positions each
     section turns by.  ``out`` / ``k_out`` may be ``q`` / ``k``.  Returns the
     turned q, or (q, k)."""
-    out, args = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, False)
-    call(_lib.rotary_apply, "rotary_apply", q.get_device(), args)
+    out, index, args, table = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, False)
+    call(_lib.rotary_apply, "rotary_apply", index, args)
     return out
 
 
@@ -177,6 +183,6 @@ def rotary_backward(dq: torch.Tensor, positions: torch.Tensor, freqs: torch.Tens
                     out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
     """Gradient of rotary: the gradients of its outputs (dq, and k's as ``k``)
     turned back.  Arguments as rotary's."""
-    out, args = _rotation(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, True)
-    call(_lib.rotary_apply, "rotary_apply", dq.get_device(), args)
+    out, index, args, table = _rotation(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, True)
+    call(_lib.rotary_apply, "rotary_apply", index, args)
     return out

@@ -38,6 +38,7 @@ template <int LANES> constexpr bool kFarRows = LANES >= 64;
 // A thread's vector u holds the elements of its row from (u * LANES + lane) * V
 // on.  Only rows that are no whole number of vectors (TAIL) have one cut by
 // the row's end; the others' are whole or absent.
+
 // x as fp32 -> d = x - m0 in place, zero where the row has no element
 template <int DT, int LANES, int NV, bool TAIL>
 __device__ __forceinline__ void subtract(float (&x)[NV][kVec<DT>], float m0, int lane, int D) {
@@ -50,51 +51,88 @@ __device__ __forceinline__ void subtract(float (&x)[NV][kVec<DT>], float m0, int
   }
 }
 
+// Rows that a group works on together: two where a row is a single vector of a
+// thread, so that one fills what the other waits for (243360 rows of 128 bf16:
+// one 26.0 us, two 23.8, four 24.5).
+template <int LANES, int NV> constexpr int kRowsTogether = NV == 1 && LANES <= 64 ? 2 : 1;
+// Whether gamma and beta are requested beside the row, not after its sums: up to
+// 24 elements a thread (65536 x 512 bf16 26.2 -> 23.4 us, 131072 x 1536 148 ->
+// 144; with 32 elements 65536 x 2048 fp16 100 -> 113), and not where a block of
+// 1024 has one row (4096 x 16384 73 -> 78).
+template <int LANES, int ELEMENTS> constexpr bool kWeightsEarly = ELEMENTS <= 24 && LANES <= 256;
+
+// Forward.  Bound by the copy of the rows: 65536 x 2048 fp16, 537 MB in 100 us
+// (5.4 TB/s, a large copy's rate 5.2), 20280 x 12 heads of 128 bf16 out of a
+// packed projection, 125 MB in 23.8 us (5.2 TB/s), 20280 x 1536 bf16 in 20.5 us
+// (within the last-level cache).  A wave to a row up to 256 vectors: no barrier.
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs A) {
-  constexpr int V = kVec<DT>, GROUPS = kRowThreads<LANES> / LANES;
+  constexpr int V = kVec<DT>, GROUPS = kRowThreads<LANES> / LANES, R = kRowsTogether<LANES, NV>;
   __shared__ float lds[2][LANES > 64 ? 2 * kRowThreads<LANES> / 64 : 1];
   int turn = 0;
   const int lane = threadIdx.x % LANES;
-  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < A.rows; r0 += (int64_t)gridDim.x * GROUPS) {
-    const int64_t row = r0 + threadIdx.x / LANES;
-    const bool here = row < A.rows; // every lane takes part in the sums
-    const uint32_t at = (uint32_t)(here ? row : A.rows - 1);
-    const int64_t xo = row_offset(at, A.inner, A.sx);
-    float x[NV][V];
-    float s1[1] = {0.f};
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS * R; r0 < A.rows; r0 += (int64_t)gridDim.x * GROUPS * R) {
+    const int64_t row = r0 + threadIdx.x / LANES; // and R - 1 more, GROUPS apart
+    float x[R][NV][V], s1[R];
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int e = (u * LANES + lane) * V;
-      unpack<DT, 16>(load_row<DT, TAIL>(A.x, xo + e, A.D - e), x[u]);
+    for (int i = 0; i < R; ++i) {
+      // every lane takes part in the sums
+      const int64_t xo = row_offset((uint32_t)min(row + i * GROUPS, A.rows - 1), A.inner, A.sx);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int e = (u * LANES + lane) * V;
+        unpack<DT, 16>(load_row<DT, TAIL>(A.x, xo + e, A.D - e), x[i][u]);
+      }
+    }
+    constexpr bool EARLY = kWeightsEarly<LANES, NV * V>;
+    float w[NV][V], b[NV][V];
+    auto weights = [&](int u) {
+      const int c = (u * LANES + lane) * V;
+      if (A.gamma) load_floats_row<WDT, V, TAIL>(A.gamma, c, A.D - c, w[u]);
+      if (A.beta) load_floats_row<WDT, V, TAIL>(A.beta, c, A.D - c, b[u]);
+    };
+    if (EARLY) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) weights(u);
     }
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
+    for (int i = 0; i < R; ++i) {
+      s1[i] = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) s1[0] += x[u][k];
+      for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) s1[i] += x[i][u][k];
+    }
     group_sum<LANES>(s1, lds, turn);
-    subtract<DT, LANES, NV, TAIL>(x, s1[0] * A.inv_d, lane, A.D);
-    float s[2] = {0.f, 0.f};
+    float s[2 * R];
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
+    for (int i = 0; i < R; ++i) {
+      subtract<DT, LANES, NV, TAIL>(x[i], s1[i] * A.inv_d, lane, A.D);
+      s[2 * i] = s[2 * i + 1] = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        s[0] += x[u][k];
-        s[1] = fmaf(x[u][k], x[u][k], s[1]);
-      }
+      for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          s[2 * i] += x[i][u][k];
+          s[2 * i + 1] = fmaf(x[i][u][k], x[i][u][k], s[2 * i + 1]);
+        }
+    }
     group_sum<LANES>(s, lds, turn);
-    const float e = s[0] * A.inv_d;
-    const float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
-    const int64_t yo = row_offset(at, A.inner, A.sout);
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int c = (u * LANES + lane) * V;
-      float w[V], b[V];
-      if (A.gamma) load_floats_row<WDT, V, TAIL>(A.gamma, c, A.D - c, w);
-      if (A.beta) load_floats_row<WDT, V, TAIL>(A.beta, c, A.D - c, b);
+    for (int i = 0; i < R; ++i) {
+      const float e = s[2 * i] * A.inv_d;
+      const float r = 1.0f / sqrtf(fmaxf(fmaf(s[2 * i + 1], A.inv_d, -e * e), 0.f) + A.eps);
+      if (row + i * GROUPS >= A.rows) break;
+      const int64_t yo = row_offset((uint32_t)(row + i * GROUPS), A.inner, A.sout);
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[u][k] = fmaf((x[u][k] - e) * r, A.gamma ? w[k] : 1.f, A.beta ? b[k] : 0.f);
-      if (here) store_row<DT, TAIL, NT>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
+      for (int u = 0; u < NV; ++u) {
+        const int c = (u * LANES + lane) * V;
+        if (!EARLY) weights(u);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          x[i][u][k] = fmaf((x[i][u][k] - e) * r, A.gamma ? w[u][k] : 1.f, A.beta ? b[u][k] : 0.f);
+        store_row<DT, TAIL, NT>(A.out, yo + c, A.D - c, pack<DT, 16>(x[i][u]));
+      }
     }
   }
 }
@@ -391,8 +429,8 @@ __global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const LNArgs 
 }
 
 template <int DT, int WDT, int LANES, int NV> hipError_t launch_rows(const LNArgs &a, hipStream_t st) {
-  constexpr int T = kRowThreads<LANES>, GROUPS = T / LANES;
-  const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + GROUPS - 1) / GROUPS, kMaxBlocksX / (T / kLNThreads));
+  constexpr int T = kRowThreads<LANES>, ROWS = T / LANES * kRowsTogether<LANES, NV>; // of a block
+  const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + ROWS - 1) / ROWS, kMaxBlocksX / (T / kLNThreads));
   const auto kernel = a.D % kVec<DT>               ? ln_row_kernel<DT, WDT, LANES, NV, true>
                       : kFarRows<LANES> && a.far ? ln_row_kernel<DT, WDT, LANES, NV, false, kFarRows<LANES>>
                                                  : ln_row_kernel<DT, WDT, LANES, NV, false>;

@@ -95,7 +95,6 @@ __device__ __forceinline__ void chunk_scale(const void *in, void *out, int64_t e
 // 16-bit gradients into fp32 ones, 4 elements a thread: a wave's stores are one
 // run of 1 KiB.  (With 8 elements a thread, in two stores 32 bytes apart from
 // lane to lane, 251 M bf16 elements took 428 us past the caches; these 298.)
-typedef uint32_t u32x2_el2 __attribute__((ext_vector_type(2), aligned(2)));
 template <int DT, bool NT>
 __device__ __forceinline__ void chunk_widen(const void *in, void *out, int64_t e0, int64_t e1, float c) {
   constexpr int STEP = kClipThreads * 4, BATCH = 2 * kClipBatch;

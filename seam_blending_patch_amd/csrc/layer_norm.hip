@@ -17,6 +17,7 @@
 #include "sb_transformer.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sb {
 
@@ -36,8 +37,16 @@ template <int LANES> constexpr int kRowThreads = LANES > kLNThreads ? LANES : kL
 template <int LANES> constexpr bool kFarRows = LANES >= 64;
 
 // A thread's vector u holds the elements of its row from (u * LANES + lane) * V
-// on.  Only rows that are no whole number of vectors (TAIL) have one cut by
-// the row's end; the others' are whole or absent.
+// on.  NV is never more than the row needs, so only the last one can pass the
+// row's end, and be cut by it where the row is no whole number of vectors (TAIL).
+template <int NV, bool TAIL> constexpr Cover cover(int u) { return u < NV - 1 ? WHOLE : TAIL ? CUT : WHOLE_OR_NONE; }
+// f<u>() for every u below NV
+template <int NV, class F, int U = 0> __device__ __forceinline__ void each(F f) {
+  if constexpr (U < NV) {
+    f(std::integral_constant<int, U>());
+    each<NV, F, U + 1>(f);
+  }
+}
 
 // x as fp32 -> d = x - m0 in place, zero where the row has no element
 template <int DT, int LANES, int NV, bool TAIL>
@@ -47,7 +56,7 @@ __device__ __forceinline__ void subtract(float (&x)[NV][kVec<DT>], float m0, int
   for (int u = 0; u < NV; ++u) {
     const int e = (u * LANES + lane) * V;
 #pragma unroll
-    for (int k = 0; k < V; ++k) x[u][k] = (TAIL ? e + k < D : e < D) ? x[u][k] - m0 : 0.f;
+    for (int k = 0; k < V; ++k) x[u][k] = u < NV - 1 || (TAIL ? e + k < D : e < D) ? x[u][k] - m0 : 0.f;
   }
 }
 
@@ -73,31 +82,29 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
   const int lane = threadIdx.x % LANES;
   for (int64_t r0 = (int64_t)blockIdx.x * GROUPS * R; r0 < A.rows; r0 += (int64_t)gridDim.x * GROUPS * R) {
     const int64_t row = r0 + threadIdx.x / LANES; // and R - 1 more, GROUPS apart
+    Vec<16> raw[R][NV];
     float x[R][NV][V], s1[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       // every lane takes part in the sums
       const int64_t xo = row_offset((uint32_t)min(row + i * GROUPS, A.rows - 1), A.inner, A.sx);
-#pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int e = (u * LANES + lane) * V;
-        unpack<DT, 16>(load_row<DT, TAIL>(A.x, xo + e, A.D - e), x[i][u]);
-      }
+      each<NV>([&](auto u) { raw[i][u] = request_row<DT, cover<NV, TAIL>(u)>(A.x, xo, (u * LANES + lane) * V, A.D); });
     }
     constexpr bool EARLY = kWeightsEarly<LANES, NV * V>;
     float w[NV][V], b[NV][V];
-    auto weights = [&](int u) {
+    auto weights = [&](auto u) {
       const int c = (u * LANES + lane) * V;
-      if (A.gamma) load_floats_row<WDT, V, TAIL>(A.gamma, c, A.D - c, w[u]);
-      if (A.beta) load_floats_row<WDT, V, TAIL>(A.beta, c, A.D - c, b[u]);
+      if (A.gamma) load_weights<WDT, V, cover<NV, TAIL>(u)>(A.gamma, c, A.D, w[u]);
+      if (A.beta) load_weights<WDT, V, cover<NV, TAIL>(u)>(A.beta, c, A.D, b[u]);
     };
-    if (EARLY) {
-#pragma unroll
-      for (int u = 0; u < NV; ++u) weights(u);
-    }
+    if (EARLY) each<NV>(weights);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       s1[i] = 0.f;
+      each<NV>([&](auto u) {
+        settle_row<DT, cover<NV, TAIL>(u)>(raw[i][u], (u * LANES + lane) * V, A.D);
+        unpack<DT, 16>(raw[i][u], x[i][u]);
+      });
 #pragma unroll
       for (int u = 0; u < NV; ++u)
 #pragma unroll
@@ -124,15 +131,13 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
       const float r = 1.0f / sqrtf(fmaxf(fmaf(s[2 * i + 1], A.inv_d, -e * e), 0.f) + A.eps);
       if (row + i * GROUPS >= A.rows) break;
       const int64_t yo = row_offset((uint32_t)(row + i * GROUPS), A.inner, A.sout);
-#pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int c = (u * LANES + lane) * V;
+      each<NV>([&](auto u) {
         if (!EARLY) weights(u);
 #pragma unroll
         for (int k = 0; k < V; ++k)
           x[i][u][k] = fmaf((x[i][u][k] - e) * r, A.gamma ? w[u][k] : 1.f, A.beta ? b[u][k] : 0.f);
-        store_row<DT, TAIL, NT>(A.out, yo + c, A.D - c, pack<DT, 16>(x[i][u]));
-      }
+        store_row<DT, cover<NV, TAIL>(u), NT>(A.out, yo, (u * LANES + lane) * V, A.D, pack<DT, 16>(x[i][u]));
+      });
     }
   }
 }
@@ -151,39 +156,42 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
   int turn = 0;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   float w[NV][V], dg[NV][V], db[NV][V];
-#pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const int c = (u * LANES + lane) * V;
-    if (A.gamma) load_floats_row<WDT, V, TAIL>(A.gamma, c, A.D - c, w[u]);
+  each<NV>([&](auto u) {
+    if (A.gamma) load_weights<WDT, V, cover<NV, TAIL>(u)>(A.gamma, (u * LANES + lane) * V, A.D, w[u]);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       if (!A.gamma) w[u][k] = 1.f;
       dg[u][k] = db[u][k] = 0.f;
     }
-  }
+  });
   Vec<16> xr[NV], gr[NV];
   auto request = [&](int64_t row) {
-    // rows past the end read nothing and hold zeros
-    const uint32_t at = (uint32_t)(row < A.rows ? row : 0);
+    // after the last row that one again, unused
+    const uint32_t at = (uint32_t)min(row, A.rows - 1);
     const int64_t xo = row_offset(at, A.inner, A.sx), go = row_offset(at, A.inner, A.sdy);
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int c = (u * LANES + lane) * V, n = row < A.rows ? A.D - c : 0;
-      xr[u] = load_row<DT, TAIL>(A.x, xo + c, n);
-      gr[u] = load_row<DT, TAIL>(A.dy, go + c, n);
-    }
+    each<NV>([&](auto u) {
+      xr[u] = request_row<DT, cover<NV, TAIL>(u)>(A.x, xo, (u * LANES + lane) * V, A.D);
+      gr[u] = request_row<DT, cover<NV, TAIL>(u)>(A.dy, go, (u * LANES + lane) * V, A.D);
+    });
   };
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   request((int64_t)blockIdx.x * GROUPS + group);
   for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < A.rows; r0 += step) {
     const int64_t row = r0 + group;
     float x[NV][V], g[NV][V];
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
+    each<NV>([&](auto u) {
+      settle_row<DT, cover<NV, TAIL>(u)>(xr[u], (u * LANES + lane) * V, A.D);
+      settle_row<DT, cover<NV, TAIL>(u)>(gr[u], (u * LANES + lane) * V, A.D);
       unpack<DT, 16>(xr[u], x[u]);
       unpack<DT, 16>(gr[u], g[u]);
-    }
+    });
     request(row + step);
+    if (row >= A.rows) { // an absent row adds nothing
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[u][k] = g[u][k] = 0.f;
+    }
     float s1[1] = {0.f};
 #pragma unroll
     for (int u = 0; u < NV; ++u)
@@ -206,11 +214,9 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
     const float e = s[0] * A.inv_d, mg = s[2] * A.inv_d;
     float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
     const float mgh = r * fmaf(s[3], A.inv_d, -e * mg);
-    if (row >= A.rows) r = 0.f; // an absent row adds nothing, whatever eps is
+    if (row >= A.rows) r = 0.f; // nor where eps is 0
     const int64_t yo = row < A.rows ? row_offset((uint32_t)row, A.inner, A.sout) : 0;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int c = (u * LANES + lane) * V;
+    each<NV>([&](auto u) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const float h = (x[u][k] - e) * r;
@@ -218,8 +224,9 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
         db[u][k] += g[u][k];
         x[u][k] = r * (fmaf(-h, mgh, g[u][k] * w[u][k]) - mg);
       }
-      if (row < A.rows) store_row<DT, TAIL, NT>(A.out, yo + c, A.D - c, pack<DT, 16>(x[u]));
-    }
+      if (row < A.rows)
+        store_row<DT, cover<NV, TAIL>(u), NT>(A.out, yo, (u * LANES + lane) * V, A.D, pack<DT, 16>(x[u]));
+    });
   }
   if (!A.part) return;
   // columns in the order [u][k][lane], so that a wave's stores are contiguous
@@ -452,6 +459,7 @@ template <int DT, int WDT> hipError_t launch_forward(const LNArgs &a, hipStream_
   if (nv <= 768) return launch_rows<DT, WDT, 256, 3>(a, st);
   if (nv <= 1024) return launch_rows<DT, WDT, 256, 4>(a, st);
   if (nv <= 2048) return launch_rows<DT, WDT, 1024, 2>(a, st);
+  if (nv <= 3072) return launch_rows<DT, WDT, 1024, 3>(a, st);
   if (nv <= 4096) return launch_rows<DT, WDT, 1024, 4>(a, st);
   const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
   hipLaunchKernelGGL((ln_loop_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);

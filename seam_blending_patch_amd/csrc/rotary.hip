@@ -35,7 +35,7 @@ __device__ __forceinline__ float2 cos_sin(const RotaryArgs &A, int pair, uint32_
 
 // field by field, so that it is selects among scalar registers and no load at
 // an address that differs from lane to lane
-__device__ __forceinline__ RotaryTensor pick(const RotaryArgs &A, bool key) {
+__device__ __forceinline__ RotaryTensor tensor_of(const RotaryArgs &A, bool key) {
   const RotaryTensor &q = A.x[0], &k = A.x[1];
   return RotaryTensor{key ? k.in : q.in,     key ? k.out : q.out,     key ? k.in_b : q.in_b,  key ? k.in_t : q.in_t,
                       key ? k.in_h : q.in_h, key ? k.out_b : q.out_b, key ? k.out_t : q.out_t, key ? k.out_h : q.out_h};
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs
   const uint32_t row0 = fdiv(base, A.div_items), row = fdiv(item, A.div_items);
   const uint32_t j = item - row * A.items, head = fdiv(j, A.div_units), unit = j - head * A.units;
   const bool key = head >= (uint32_t)A.heads[0], turned = unit < (uint32_t)A.units_turned;
-  const RotaryTensor T = pick(A, key);
+  const RotaryTensor T = tensor_of(A, key);
   const int e = turned ? unit * V : A.part + (unit - A.units_turned) * V;
   int64_t out = 0;
   int count = 0; // elements to read and write (no more than a vector of them)
@@ -72,12 +72,14 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs
   if (item < total) {
     const uint32_t b = fdiv(A.token0 + row, A.length), t = A.token0 + row - b * A.length.d;
     const uint32_t h = key ? head - A.heads[0] : head;
-    const int64_t in = b * T.in_b + t * T.in_t + h * T.in_h + e;
+    const int64_t in = b * T.in_b + t * T.in_t + h * T.in_h;
     out = b * T.out_b + t * T.out_t + h * T.out_h + e;
     if (turned) count = (INTER ? A.part : half) - e;
     else if (T.in != T.out) count = A.D - e; // what is not turned stays where it is in place
-    first = load_part<DT>(T.in, in, count);
-    if (!INTER && turned) second = load_part<DT>(T.in, in + half, count);
+    // whole vectors of the head, also where fewer elements are the step's own;
+    // where the head ends, moved into place below
+    if (count > 0) first = request_row<DT, CUT>(T.in, in, e, A.D);
+    if (!INTER && turned) second = request_row<DT, CUT>(T.in, in, half + e, A.D);
   }
   const uint32_t rows = fdiv(min(base + kRotaryThreads, total) - 1, A.div_items) + 1 - row0;
   for (uint32_t i = threadIdx.x; i < rows * half; i += kRotaryThreads) {
@@ -86,6 +88,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs
   }
   __syncthreads();
   if (count <= 0) return;
+  settle_row<DT, CUT>(first, e, A.D);
   if (turned) {
     float u[V], v[V];
     unpack<DT, 16>(first, u);
@@ -101,6 +104,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs
         }
     } else {
       const float2 *cs = turn + (row - row0) * half + e;
+      settle_row<DT, CUT>(second, half + e, A.D);
       unpack<DT, 16>(second, v);
 #pragma unroll
       for (int k = 0; k < V; ++k)

@@ -265,6 +265,9 @@ int vae_tile_layout(int64_t L, int rule, const int64_t params[4], int64_t max_ti
  *   dtype        of x and out; weight_dtype: dtype, or SB_F32.
  *   out          each element held once; x itself (same pointer and strides), or
  *                sharing no element with it (checked; SB_EARG).
+ *   workspace    caller-owned device scratch of layer_norm_forward_workspace_bytes()
+ *                bytes, 16-byte aligned; not looked at where that is 0 (rows of
+ *                up to 64 KiB).
  * Any element alignment is taken; 16-byte aligned rows are fastest.  Statistics
  * are fp32 and corrected two-pass (sums about a first mean, then its rounding
  * error taken out), so a mean that is large against the spread costs no
@@ -272,7 +275,11 @@ int vae_tile_layout(int64_t L, int rule, const int64_t params[4], int64_t max_ti
  */
 int layer_norm_forward(const void *x, const int64_t x_stride[2], const int64_t shape[3], float eps,
                        const void *gamma, const void *beta, int dtype, int weight_dtype, void *out,
-                       const int64_t out_stride[2], void *stream);
+                       const int64_t out_stride[2], void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace (bytes) layer_norm_forward needs: 0 for rows of up to 64
+ * KiB; (size_t)-1 with an error message for invalid arguments. */
+size_t layer_norm_forward_workspace_bytes(const int64_t shape[3], int dtype);
 
 /* Device workspace (bytes) layer_norm_backward needs; 0 with an error message
  * for invalid arguments. */

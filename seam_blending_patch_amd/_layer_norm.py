@@ -14,10 +14,11 @@ from ._call import call, like
 
 _ptr = ctypes.c_void_p  # of shapes and strides too: places in one array.array
 _lib.layer_norm_forward.argtypes = [_ptr, _ptr, _ptr, ctypes.c_float, _ptr, _ptr, ctypes.c_int, ctypes.c_int, _ptr,
-                                    _ptr, _ptr]
+                                    _ptr, _ptr, ctypes.c_size_t, _ptr]
 _lib.layer_norm_forward.restype = ctypes.c_int
-_lib.layer_norm_backward_workspace_bytes.argtypes = [_ptr, ctypes.c_int]
-_lib.layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+for _f in (_lib.layer_norm_forward_workspace_bytes, _lib.layer_norm_backward_workspace_bytes):
+    _f.argtypes = [_ptr, ctypes.c_int]
+    _f.restype = ctypes.c_size_t
 _lib.layer_norm_backward.argtypes = [_ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_float, _ptr, ctypes.c_int,
                                      ctypes.c_int, _ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_size_t, _ptr]
 _lib.layer_norm_backward.restype = ctypes.c_int
@@ -89,6 +90,15 @@ def _like(t: torch.Tensor, name: str, shape, code: int, index: int):
         raise ValueError(f"{name} must match x")
 
 
+_LONG = 16384  # rows of up to 64 KiB need no workspace
+
+
+@functools.lru_cache(maxsize=256)
+def _forward_workspace_bytes(rows: int, d: int, code: int) -> int:
+    shape = array("q", (1, rows, d))
+    return max(16, _lib.layer_norm_forward_workspace_bytes(shape.buffer_info()[0], code))
+
+
 def _forward(x, gamma, beta, eps, out):
     """(out, device index, arguments of the library's call, what they point to)"""
     shape, code = _rows(x, "x")
@@ -103,8 +113,13 @@ def _forward(x, gamma, beta, eps, out):
         _like(out, "out", shape, code, index)
     geometry = _geometry(d, x, out)
     at = geometry.buffer_info()[0]
+    need, wp = 0, None
+    if d > _LONG:  # such rows are split, their statistics merged through a workspace
+        need = _forward_workspace_bytes(geometry[0] * geometry[1], d, code)
+        geometry = (geometry, torch.empty_like(like(index, need, torch.uint8), memory_format=_DENSE))
+        wp = geometry[1].data_ptr()
     return out, index, (x.data_ptr(), at + 24, at, eps, gp, bp, code, code if dtype is None else _DTYPE[dtype],
-                        out.data_ptr(), at + 40), geometry
+                        out.data_ptr(), at + 40, wp, need), geometry
 
 
 class LayerNorm:

@@ -81,11 +81,25 @@ int check_eps(float eps) {
   return !(eps >= 0.0f) || eps == __builtin_inff() ? failf(SB_EARG, "eps must be finite and >= 0") : SB_OK;
 }
 
-// The backward pass's workspace: nparts blocks of 2 * cols floats, then, for
-// rows too long for registers, 8 floats a row.
+// workspace of rows too long for registers: 8 floats a row and 8 a chunk of it
+int64_t split_bytes(int64_t rows, int64_t d, int dtype, int64_t most) {
+  const int64_t v = 16 / sb::elem_bytes(dtype), chunk = sb::kLNThreads * sb::kChunkVectors * v;
+  return (d + v - 1) / v <= most ? 0 : rows * (1 + (d + chunk - 1) / chunk) * 8 * (int64_t)sizeof(float);
+}
+
+// The backward pass's workspace: nparts blocks of 2 * cols floats, then
+// split_bytes.
 struct BackwardPlan {
   int64_t nparts, cols, part_bytes, rowstat_bytes;
 };
+
+int check_workspace(const void *workspace, size_t bytes, int64_t need) {
+  if (need > 0 && (!workspace || !sb::aligned(workspace, 16)))
+    return failf(SB_EARG, "workspace must be 16-byte aligned device memory");
+  if (need > 0 && bytes < (size_t)need)
+    return failf(SB_EWORKSPACE, "workspace too small: %zu bytes given, %lld needed", bytes, (long long)need);
+  return SB_OK;
+}
 
 BackwardPlan plan_backward(int64_t rows, int64_t d, int dtype) {
   BackwardPlan p;
@@ -95,22 +109,32 @@ BackwardPlan plan_backward(int64_t rows, int64_t d, int dtype) {
     p.cols = (int64_t)lay.lanes * lay.nv * v;
     const int64_t blocks = (int64_t)sb_cu_count() * lay.blocks_per_cu();
     p.nparts = std::max<int64_t>(1, std::min((rows + lay.rows() - 1) / lay.rows(), blocks));
-    p.rowstat_bytes = 0;
   } else {
     const int64_t per = sb::kLNThreads * v;
     p.cols = (d + per - 1) / per * per;
     p.nparts = std::max<int64_t>(1, std::min<int64_t>(rows, 4 * sb_cu_count() / std::max<int64_t>(1, p.cols / per)));
-    p.rowstat_bytes = rows * 8 * (int64_t)sizeof(float);
   }
+  p.rowstat_bytes = split_bytes(rows, d, dtype, sb::kBackwardVectors);
   p.part_bytes = p.nparts * 2 * p.cols * (int64_t)sizeof(float);
   return p;
 }
 
 } // namespace
 
+extern "C" size_t layer_norm_forward_workspace_bytes(const int64_t shape[3], int dtype) {
+  sb::LNArgs a;
+  if (!sb::known_dtype(dtype)) {
+    failf(SB_EARG, "unknown dtype %d", dtype);
+    return (size_t)-1;
+  }
+  if (read_shape(shape, a)) return (size_t)-1;
+  return (size_t)split_bytes(a.rows, a.D, dtype, sb::kForwardVectors);
+}
+
 extern "C" int layer_norm_forward(const void *x, const int64_t x_stride[2], const int64_t shape[3], float eps,
                                   const void *gamma, const void *beta, int dtype, int weight_dtype, void *out,
-                                  const int64_t out_stride[2], void *stream) {
+                                  const int64_t out_stride[2], void *workspace, size_t workspace_bytes,
+                                  void *stream) {
   sb::LNArgs a;
   int rc;
   const void *weights[2] = {gamma, beta};
@@ -122,6 +146,10 @@ extern "C" int layer_norm_forward(const void *x, const int64_t x_stride[2], cons
       (rc = read_rows("out", out, out_stride, shape, dtype, a.sout, so)) ||
       (rc = check_output("out", out, so, "x", x, sx, dtype)))
     return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes, split_bytes(a.rows, a.D, dtype, sb::kForwardVectors))))
+    return rc;
+  a.rowstat = (float *)workspace;
+  a.chunks = a.rowstat + a.rows * 8;
   a.x = x;
   a.out = out;
   a.gamma = gamma;
@@ -165,10 +193,7 @@ extern "C" int layer_norm_backward(const void *dy, const int64_t dy_stride[2], c
       return rc;
   }
   const BackwardPlan p = plan_backward(a.rows, a.D, dtype);
-  if (!workspace || !sb::aligned(workspace, 16)) return failf(SB_EARG, "workspace must be 16-byte aligned device memory");
-  if (workspace_bytes < (size_t)(p.part_bytes + p.rowstat_bytes))
-    return failf(SB_EWORKSPACE, "workspace too small: %zu bytes given, %lld needed", workspace_bytes,
-                 (long long)(p.part_bytes + p.rowstat_bytes));
+  if ((rc = check_workspace(workspace, workspace_bytes, p.part_bytes + p.rowstat_bytes))) return rc;
   a.x = x;
   a.dy = dy;
   a.out = dx;
@@ -179,6 +204,7 @@ extern "C" int layer_norm_backward(const void *dy, const int64_t dy_stride[2], c
   a.far = past_caches(a, dtype);
   a.part = wanted ? (float *)workspace : nullptr;
   a.rowstat = (float *)((char *)workspace + p.part_bytes);
+  a.chunks = a.rowstat + a.rows * 8;
   a.nparts = a.rows > 0 ? (int32_t)p.nparts : 0;
   a.cols = (int32_t)p.cols;
   const hipError_t e = sb_launch_layer_norm_backward(a, dtype, weight_dtype, (hipStream_t)stream);

@@ -146,6 +146,9 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
 // rows, a thread the same columns of each, so dgamma and dbeta add up in
 // registers; at the end the block's rows are merged and written as one block of
 // partials.  The next row's vectors are requested before this row's are used.
+// Bound by the three rows it moves: 65536 x 2048 fp16, 805 MB in 148 us (5.4
+// TB/s, a large copy's rate 5.2) and 5 us for the reduction; 20280 x 1536 bf16,
+// 187 MB in 37.8 and 4.3 us.  (LNLayout has the layouts measured.)
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const LNArgs A) {
   constexpr int V = kVec<DT>, T = kRowThreads<LANES>, GROUPS = T / LANES, COLS = LANES * NV * V;
@@ -263,100 +266,131 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
 }
 
 // ---------------------------------------------------------------------------
-// Rows of any length: one block a row, looping over it (three times forward,
-// the second and third from cache).
+// Longer rows: split into chunks that fit a block's registers, however few rows
+// there are.  A chunk's statistics are corrected two-pass about its own m0;
+// a row's are merged from its chunks' (Chan, Golub & LeVeque), about the first
+// chunk's m0, called K: with a chunk's mean K + delta,
+//   E = sum n delta / D,  M2 = sum (M2_c + n (delta - E)^2),  x - m = (x - K) - E.
+// 4 rows of 798720 bf16: 14 us forward, 35 backward with its reduction (a block
+// of 1024 threads to a row: 178 and 435); 1000 rows of 40000: 49 and 100 (54 and
+// 108), of which reading the rows twice is the bound.
 // ---------------------------------------------------------------------------
-constexpr int kLoopWaves = kLNThreads / 64;
+template <int DT> constexpr int kChunk = kLNThreads * kChunkVectors * kVec<DT>;
+struct ChunkStat { // 8 floats of workspace
+  float m0, e, m2, g, gd; // mean m0 + e, squares about it, sums of g and g (x - m0)
+  float unused[3];
+};
 
-// m0 of the row, then whatever `f` adds up over d = x - m0
-template <int DT, int K, int N, class F>
-__device__ __forceinline__ float row_loop(const void *x, int64_t xo, int D, float inv_d, float (&lds)[2][N],
-                                          int &turn, float (&sums)[K], F f) {
-  constexpr int V = kVec<DT>;
-  float s[1] = {0.f};
-  for (int e = threadIdx.x * V; e < D; e += kLNThreads * V) {
-    float v[V];
-    load_floats<DT, V>(x, xo + e, D - e, v);
-#pragma unroll
-    for (int k = 0; k < V; ++k) s[0] += v[k];
-  }
-  group_sum<kLNThreads>(s, lds, turn);
-  const float m0 = s[0] * inv_d;
-#pragma unroll
-  for (int k = 0; k < K; ++k) sums[k] = 0.f;
-  for (int e = threadIdx.x * V; e < D; e += kLNThreads * V) {
-    float v[V];
-    load_floats<DT, V>(x, xo + e, D - e, v);
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = e + k < D ? v[k] - m0 : 0.f;
-    f(e, v);
-  }
-  group_sum<kLNThreads>(sums, lds, turn);
-  return m0;
-}
-
-template <int DT, int WDT>
-__global__ __launch_bounds__(kLNThreads) void ln_loop_kernel(const LNArgs A) {
-  constexpr int V = kVec<DT>;
-  __shared__ float lds[2][2 * kLoopWaves];
+// one block a chunk (blockIdx.x) of every gridDim.y-th row
+template <int DT, int WDT, bool BACKWARD> __global__ __launch_bounds__(kLNThreads) void ln_chunk_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>, NV = kChunkVectors, SUMS = BACKWARD ? 4 : 2;
+  __shared__ float lds[2][SUMS * kLNThreads / 64];
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
-    const int64_t xo = row_offset((uint32_t)row, A.inner, A.sx), yo = row_offset((uint32_t)row, A.inner, A.sout);
-    float s[2];
-    const float m0 = row_loop<DT>(A.x, xo, A.D, A.inv_d, lds, turn, s, [&](int, const float (&d)[V]) {
+  const int c0 = blockIdx.x * kChunk<DT> + threadIdx.x * V, here = min(kChunk<DT>, A.D - (int)blockIdx.x * kChunk<DT>);
+  for (int64_t row = blockIdx.y; row < A.rows; row += gridDim.y) {
+    const int64_t xo = row_offset((uint32_t)row, A.inner, A.sx);
+    float x[NV][V], g[NV][V], s1[1] = {0.f};
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        s[0] += d[k];
-        s[1] = fmaf(d[k], d[k], s[1]);
-      }
-    });
-    const float e = s[0] * A.inv_d;
-    const float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
-    for (int c = threadIdx.x * V; c < A.D; c += kLNThreads * V) {
-      float v[V], w[V], b[V];
-      load_floats<DT, V>(A.x, xo + c, A.D - c, v);
-      if (A.gamma) load_floats<WDT, V>(A.gamma, c, A.D - c, w);
-      if (A.beta) load_floats<WDT, V>(A.beta, c, A.D - c, b);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float h = ((v[k] - m0) - e) * r;
-        v[k] = fmaf(h, A.gamma ? w[k] : 1.f, A.beta ? b[k] : 0.f);
-      }
-      store_part<DT>(A.out, yo + c, A.D - c, pack<DT, 16>(v));
+    for (int u = 0; u < NV; ++u) {
+      const int c = c0 + u * kLNThreads * V;
+      load_floats<DT, V>(A.x, xo + c, A.D - c, x[u]);
     }
-  }
-}
-
-// per-row (m, r, mean g, mean g h): the sums over d = x - m0 of d, d^2, g and
-// g d give all of them
-template <int DT, int WDT>
-__global__ __launch_bounds__(kLNThreads) void ln_loop_rowstat_kernel(const LNArgs A) {
-  constexpr int V = kVec<DT>;
-  __shared__ float lds[2][4 * kLoopWaves];
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
-    const int64_t xo = row_offset((uint32_t)row, A.inner, A.sx), go = row_offset((uint32_t)row, A.inner, A.sdy);
-    float s[4];
-    const float m0 = row_loop<DT>(A.x, xo, A.D, A.inv_d, lds, turn, s, [&](int c, const float (&d)[V]) {
-      float g[V], w[V];
-      load_floats<DT, V>(A.dy, go + c, A.D - c, g);
-      if (A.gamma) load_floats<WDT, V>(A.gamma, c, A.D - c, w);
+    if constexpr (BACKWARD) {
+      const int64_t go = row_offset((uint32_t)row, A.inner, A.sdy);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int c = c0 + u * kLNThreads * V;
+        load_floats<DT, V>(A.dy, go + c, A.D - c, g[u]);
+        if (A.gamma) {
+          float w[V];
+          load_floats<WDT, V>(A.gamma, c, A.D - c, w);
+#pragma unroll
+          for (int k = 0; k < V; ++k) g[u][k] *= w[k];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s1[0] += x[u][k];
+    group_sum<kLNThreads>(s1, lds, turn);
+    const float m0 = s1[0] / (float)here;
+    float s[SUMS] = {};
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        if (A.gamma) g[k] *= w[k];
-        s[0] += d[k];
-        s[1] = fmaf(d[k], d[k], s[1]);
-        s[2] += g[k];
-        s[3] = fmaf(g[k], d[k], s[3]);
+        const float d = c0 + u * kLNThreads * V + k < A.D ? x[u][k] - m0 : 0.f;
+        s[0] += d;
+        s[1] = fmaf(d, d, s[1]);
+        if constexpr (BACKWARD) {
+          s[SUMS - 2] += g[u][k];
+          s[SUMS - 1] = fmaf(g[u][k], d, s[SUMS - 1]);
+        }
       }
-    });
+    group_sum<kLNThreads>(s, lds, turn);
     if (threadIdx.x == 0) {
-      const float e = s[0] * A.inv_d, mg = s[2] * A.inv_d;
-      const float r = 1.0f / sqrtf(fmaxf(fmaf(s[1], A.inv_d, -e * e), 0.f) + A.eps);
-      // m0 and e apart: their sum would round e away when m0 is large
-      reinterpret_cast<float4 *>(A.rowstat)[2 * row] = make_float4(m0, e, r, mg);
-      A.rowstat[8 * row + 4] = r * fmaf(s[3], A.inv_d, -e * mg);
+      const float e = s[0] / (float)here;
+      ChunkStat *st = reinterpret_cast<ChunkStat *>(A.chunks) + row * gridDim.x + blockIdx.x;
+      st->m0 = m0;
+      st->e = e;
+      st->m2 = fmaf(-e, s[0], s[1]);
+      if constexpr (BACKWARD) {
+        st->g = s[SUMS - 2];
+        st->gd = s[SUMS - 1];
+      }
     }
+  }
+}
+
+// a row's statistics from its chunks': (K, E, r, mean of g) and the mean of g h
+template <int DT, bool BACKWARD> __global__ __launch_bounds__(kLNThreads) void ln_merge_kernel(const LNArgs A, int chunks) {
+  constexpr int SUMS = BACKWARD ? 3 : 1;
+  __shared__ float lds[2][SUMS * kLNThreads / 64];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const ChunkStat *st = reinterpret_cast<const ChunkStat *>(A.chunks) + row * chunks;
+    const float K = st[0].m0;
+    float s1[1] = {0.f};
+    for (int c = threadIdx.x; c < chunks; c += kLNThreads)
+      s1[0] = fmaf((float)min(kChunk<DT>, A.D - c * kChunk<DT>), (st[c].m0 - K) + st[c].e, s1[0]);
+    group_sum<kLNThreads>(s1, lds, turn);
+    const float E = s1[0] * A.inv_d;
+    float s[SUMS] = {};
+    for (int c = threadIdx.x; c < chunks; c += kLNThreads) {
+      const float off = (st[c].m0 - K) - E, d = off + st[c].e;
+      s[0] += fmaf((float)min(kChunk<DT>, A.D - c * kChunk<DT>) * d, d, st[c].m2);
+      if constexpr (BACKWARD) {
+        s[SUMS - 2] += st[c].g;
+        s[SUMS - 1] += fmaf(st[c].g, off, st[c].gd); // g (x - m), x - m = (x - m0) + off
+      }
+    }
+    group_sum<kLNThreads>(s, lds, turn);
+    if (threadIdx.x == 0) {
+      const float r = 1.0f / sqrtf(fmaxf(s[0] * A.inv_d, 0.f) + A.eps);
+      const float mg = BACKWARD ? s[SUMS - 2] * A.inv_d : 0.f;
+      reinterpret_cast<float4 *>(A.rowstat)[2 * row] = make_float4(K, E, r, mg);
+      if constexpr (BACKWARD) A.rowstat[8 * row + 4] = r * s[SUMS - 1] * A.inv_d;
+    }
+  }
+}
+
+// y: a block has 256 vectors of columns (blockIdx.x) and every gridDim.y-th row
+template <int DT, int WDT> __global__ __launch_bounds__(kLNThreads) void ln_apply_kernel(const LNArgs A) {
+  constexpr int V = kVec<DT>;
+  const int c = (blockIdx.x * kLNThreads + threadIdx.x) * V;
+  float w[V], b[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) w[k] = 1.f, b[k] = 0.f;
+  if (A.gamma) load_floats<WDT, V>(A.gamma, c, A.D - c, w);
+  if (A.beta) load_floats<WDT, V>(A.beta, c, A.D - c, b);
+  for (int64_t row = blockIdx.y; row < A.rows; row += gridDim.y) {
+    const float4 st = reinterpret_cast<const float4 *>(A.rowstat)[2 * row];
+    float x[V];
+    load_floats<DT, V>(A.x, row_offset((uint32_t)row, A.inner, A.sx) + c, A.D - c, x);
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = fmaf(((x[k] - st.x) - st.y) * st.z, w[k], b[k]);
+    store_part<DT>(A.out, row_offset((uint32_t)row, A.inner, A.sout) + c, A.D - c, pack<DT, 16>(x));
   }
 }
 
@@ -397,6 +431,16 @@ __global__ __launch_bounds__(kLNThreads) void ln_columns_kernel(const LNArgs A) 
   }
 }
 
+// the total of float i of the blocks of partials, to where it belongs
+template <int WDT, int LANES, int V> __device__ __forceinline__ void store_column(const LNArgs &A, int64_t i, float t) {
+  const bool beta = i >= A.cols;
+  const uint32_t j = (uint32_t)(beta ? i - A.cols : i);
+  const uint32_t u = j / (LANES * V), k = j / LANES % V, l = j % LANES;
+  const int64_t col = ((int64_t)u * LANES + l) * V + k;
+  void *out = beta ? A.dbeta : A.dgamma;
+  if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(t);
+}
+
 // dgamma and dbeta: the partials' sums, in a fixed order.  A block takes 16
 // floats of a block of partials (of 2 * cols), as 4 vectors; its 256 groups of
 // 4 threads take every 256th block of partials each, so that a thousand of
@@ -425,14 +469,19 @@ __global__ __launch_bounds__(kReduceThreads) void ln_reduce_kernel(const LNArgs 
     float t = lds[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < kReduceThreads / 64; ++w) t += lds[w][threadIdx.x];
-    const int64_t i = (int64_t)blockIdx.x * kReduceCols + threadIdx.x;
-    const bool beta = i >= A.cols;
-    const uint32_t j = (uint32_t)(beta ? i - A.cols : i);
-    const uint32_t u = j / (LANES * V), k = j / LANES % V, l = j % LANES;
-    const int64_t col = ((int64_t)u * LANES + l) * V + k;
-    void *out = beta ? A.dbeta : A.dgamma;
-    if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(t);
+    store_column<WDT, LANES, V>(A, (int64_t)blockIdx.x * kReduceCols + threadIdx.x, t);
   }
+}
+
+// the same where there are columns enough to fill the chip: a thread a column
+template <int WDT, int LANES, int V>
+__global__ __launch_bounds__(kLNThreads) void ln_reduce_columns_kernel(const LNArgs A) {
+  const int64_t i = (int64_t)blockIdx.x * kLNThreads + threadIdx.x;
+  if (i >= 2 * (int64_t)A.cols) return;
+  float t = 0.f;
+#pragma unroll 4
+  for (int b = 0; b < A.nparts; ++b) t += A.part[(int64_t)b * 2 * A.cols + i];
+  store_column<WDT, LANES, V>(A, i, t);
 }
 
 template <int DT, int WDT, int LANES, int NV> hipError_t launch_rows(const LNArgs &a, hipStream_t st) {
@@ -442,6 +491,18 @@ template <int DT, int WDT, int LANES, int NV> hipError_t launch_rows(const LNArg
                       : kFarRows<LANES> && a.far ? ln_row_kernel<DT, WDT, LANES, NV, false, kFarRows<LANES>>
                                                  : ln_row_kernel<DT, WDT, LANES, NV, false>;
   hipLaunchKernelGGL(kernel, dim3(blocks), dim3(T), 0, st, a);
+  return hipGetLastError();
+}
+
+// of rows split into chunks, to A.rowstat
+template <int DT, int WDT, bool BACKWARD> hipError_t launch_statistics(const LNArgs &a, hipStream_t st) {
+  const int chunks = (a.D + kChunk<DT> - 1) / kChunk<DT>;
+  hipLaunchKernelGGL((ln_chunk_kernel<DT, WDT, BACKWARD>), dim3((unsigned)chunks, (unsigned)std::min<int64_t>(a.rows, kMaxGridY)),
+                     dim3(kLNThreads), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((ln_merge_kernel<DT, BACKWARD>), dim3((unsigned)std::min<int64_t>(a.rows, kMaxBlocksX)),
+                     dim3(kLNThreads), 0, st, a, chunks);
   return hipGetLastError();
 }
 
@@ -460,14 +521,23 @@ template <int DT, int WDT> hipError_t launch_forward(const LNArgs &a, hipStream_
   if (nv <= 1024) return launch_rows<DT, WDT, 256, 4>(a, st);
   if (nv <= 2048) return launch_rows<DT, WDT, 1024, 2>(a, st);
   if (nv <= 3072) return launch_rows<DT, WDT, 1024, 3>(a, st);
-  if (nv <= 4096) return launch_rows<DT, WDT, 1024, 4>(a, st);
-  const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
-  hipLaunchKernelGGL((ln_loop_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);
+  if (nv <= kForwardVectors) return launch_rows<DT, WDT, 1024, 4>(a, st);
+  const hipError_t e = launch_statistics<DT, WDT, false>(a, st);
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((nv + kLNThreads - 1) / kLNThreads), (unsigned)std::min<int64_t>(a.rows, 1024));
+  hipLaunchKernelGGL((ln_apply_kernel<DT, WDT>), grid, dim3(kLNThreads), 0, st, a);
   return hipGetLastError();
 }
 
 template <int WDT, int LANES, int V> hipError_t launch_reduce(const LNArgs &a, hipStream_t st) {
   if (!a.part) return hipSuccess;
+  // (40960 columns and 51 blocks of partials: 6.9 us by columns, 19 by blocks of
+  // 16; 16384 and 256 of them 12.9 by blocks)
+  if (a.cols >= 32768) {
+    hipLaunchKernelGGL((ln_reduce_columns_kernel<WDT, LANES, V>),
+                       dim3((unsigned)((2 * (int64_t)a.cols + kLNThreads - 1) / kLNThreads)), dim3(kLNThreads), 0, st, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL((ln_reduce_kernel<WDT, LANES, V>), dim3((unsigned)(2 * (int64_t)a.cols / kReduceCols)),
                      dim3(kReduceThreads), 0, st, a);
   return hipGetLastError();
@@ -504,9 +574,7 @@ template <int DT, int WDT> hipError_t launch_backward(const LNArgs &a, hipStream
   case 1024 * 16 + 2: return launch_backward_rows<DT, WDT, 1024, 2>(a, st);
   }
   if (a.rows > 0) {
-    const unsigned blocks = (unsigned)std::min<int64_t>(a.rows, kMaxBlocksX);
-    hipLaunchKernelGGL((ln_loop_rowstat_kernel<DT, WDT>), dim3(blocks), dim3(kLNThreads), 0, st, a);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch_statistics<DT, WDT, true>(a, st);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((ln_columns_kernel<DT, WDT>), dim3((unsigned)(a.cols / (kLNThreads * V)), (unsigned)a.nparts),
                        dim3(kLNThreads), 0, st, a);

@@ -28,18 +28,23 @@ struct LNArgs {
   int32_t D;
   float eps, inv_d;
   int32_t far;        // the output is more than the caches hold
+  // rows split into chunks
+  float *rowstat;     // 8 floats a row: K, E, 1/sigma, mean of g, mean of g h
+  float *chunks;      // 8 floats a chunk of a row
   // backward
   float *part;        // weight-gradient partials [blocks][2][columns] (nullptr: none wanted)
-  float *rowstat;     // per row: mean, 1/sigma, mean of g, mean of g h (the looping kernels)
   void *dgamma, *dbeta;
   int32_t nparts, cols; // blocks of partials; floats of each (the columns, rounded up to the block's)
 };
 
-constexpr int kLNThreads = 256; // threads of a looping or column block
+constexpr int kLNThreads = 256; // threads of a block of rows, of a chunk or of columns
+// rows of more vectors are split: forward, and (backward_layout) backward
+constexpr int64_t kForwardVectors = 4096, kBackwardVectors = 2048;
+constexpr int kChunkVectors = 4; // vectors of a chunk on each of kLNThreads threads
 
 // How the backward pass lays rows of nv 16-byte vectors over threads: NV
 // vectors on each of LANES threads, as many rows to a block as it has room for
-// (lanes 0: the row is too long for registers and the looping kernels take it).
+// (lanes 0: the row is too long for registers and is split into chunks).
 // A wave to a row as long as the sums of its columns fit its registers: it
 // needs no barrier.  Measured in us, kernel and reduction (copy rate: 156 us for
 // each of these but the last, 37):
@@ -65,7 +70,7 @@ inline LNLayout backward_layout(int64_t nv) {
   if (nv <= 256) return LNLayout{64, (int)(nv + 63) / 64};
   if (nv <= 512) return LNLayout{128, nv <= 384 ? 3 : 4};
   if (nv <= 1024) return LNLayout{512, 2};
-  if (nv <= 2048) return LNLayout{1024, 2};
+  if (nv <= kBackwardVectors) return LNLayout{1024, 2};
   return LNLayout{0, 0};
 }
 

@@ -83,10 +83,17 @@ def test_weights_given_or_not(sb, dtype, given):
     check(sb, x, dy, gamma if given == "gamma" else None, beta if given == "beta" else None, what=given)
 
 
-@pytest.mark.parametrize("d", [64, 100, 1536, 9001])
+@pytest.mark.parametrize("d", [64, 100, 1536, 9001, 50000])
 def test_mean_large_against_the_spread(sb, d):
     x = draw((6, d), F32, d, mean=3000.0)
     check(sb, x, draw((6, d), F32, d + 1), *weights(d, F32, 3), what="mean 3000")
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("d", [65536, 300001])
+def test_few_long_rows(sb, rows, d):
+    check(sb, draw((rows, d), BF16, d), draw((rows, d), BF16, d + 1), *weights(d, F32, 3), what="long")
+    check(sb, draw((rows, d), F32, d, mean=3000.0), draw((rows, d), F32, d + 1), None, None, what="long, mean 3000")
 
 
 def test_loud_feature_first(sb):
@@ -104,7 +111,7 @@ def test_constant_rows_give_beta_and_no_gradient_through_the_spread(sb):
     check(sb, x, draw((5, 96), F32, 2), gamma, beta, what="constant")
 
 
-@pytest.mark.parametrize("d", [24, 200, 1536, 9000])
+@pytest.mark.parametrize("d", [24, 200, 1536, 9000, 40000])
 def test_nan_and_infinity_stay_in_their_row(sb, d):
     x, dy = draw((7, d), F32, 1), draw((7, d), F32, 2)
     clean, clean_dx, _ = sb.layer_norm(x), *sb.layer_norm_backward(dy, x)[:2]

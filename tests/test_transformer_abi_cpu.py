@@ -64,7 +64,21 @@ def test_layer_norm_forward_refusals(lib, change, code, word):
     a = dict(x=X, x_stride=i64(192, 64), shape=i64(2, 3, 64), eps=1e-6, gamma=G, beta=B, dtype=0, wdtype=0, out=Y,
              out_stride=i64(192, 64)) | change
     refused(lib, code, lib.layer_norm_forward(a["x"], a["x_stride"], a["shape"], a["eps"], a["gamma"], a["beta"],
-                                              a["dtype"], a["wdtype"], a["out"], a["out_stride"], None), word)
+                                              a["dtype"], a["wdtype"], a["out"], a["out_stride"], None, 0, None), word)
+
+
+def test_layer_norm_forward_workspace(lib):
+    assert lib.layer_norm_forward_workspace_bytes(i64(1, 60000, 16384), 0) == 0
+    assert lib.layer_norm_forward_workspace_bytes(i64(1, 60000, 32768), 2) == 0
+    need = lib.layer_norm_forward_workspace_bytes(i64(1, 3, 40000), 2)
+    assert need >= 3 * 6 * 32
+    assert lib.layer_norm_forward_workspace_bytes(i64(1, 3, 0), 2) == ctypes.c_size_t(-1).value
+    assert lib.layer_norm_forward_workspace_bytes(i64(1, 3, 64), 7) == ctypes.c_size_t(-1).value
+    st = i64(0, 40000)
+    call = lambda w, n: lib.layer_norm_forward(X, st, i64(1, 3, 40000), 1e-6, None, None, 2, 2, Y, st, w, n, None)  # noqa: E731
+    refused(lib, -1, call(None, 0), b"workspace")
+    refused(lib, -1, call(P(0x4000008), need), b"16-byte")
+    refused(lib, -3, call(W, need - 1), b"too small")
 
 
 @pytest.mark.parametrize("change,code,word", [
@@ -97,7 +111,7 @@ def test_layer_norm_workspace(lib):
 
 def test_layer_norm_without_rows_reads_nothing(lib):
     st = i64(0, 64)
-    assert lib.layer_norm_forward(None, st, i64(4, 0, 64), 1e-6, None, None, 0, 0, None, st, None) == 0
+    assert lib.layer_norm_forward(None, st, i64(4, 0, 64), 1e-6, None, None, 0, 0, None, st, None, 0, None) == 0
     assert lib.layer_norm_backward(None, st, None, st, i64(0, 4, 64), 1e-6, None, 0, 0, None, st, None, None, None, 0,
                                    None) == 0
 

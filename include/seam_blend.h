@@ -39,6 +39,9 @@
  *    execution surface asynchronously on the stream, as for any HIP kernel.
  *  - Tensors are dense, contiguous, row-major (last index fastest), except
  *    where an entry point takes strides.
+ *  - What a call writes (outputs, workspace) overlaps nothing else that it reads
+ *    or writes, except where an entry point says so; what is checked of that is
+ *    said there.
  */
 #ifndef SEAM_BLEND_H
 #define SEAM_BLEND_H

@@ -48,6 +48,12 @@ def _table(tensors: Sequence[torch.Tensor], name: str, index: int):
     return ptrs, codes, whole
 
 
+def _repeated(ptrs: array, numels: array) -> bool:
+    """Whether a tensor with elements is written to twice."""
+    return len(set(ptrs)) != len(ptrs) and len(set(p for p, n in zip(ptrs, numels) if n)) != sum(
+        1 for n in numels if n)
+
+
 def _at(a: array) -> int:
     return a.buffer_info()[0]
 
@@ -73,6 +79,8 @@ def _clip(grads, max_norm, eps, out):
             raise ValueError("each output must have its gradient's shape and strides")
         if out_codes != codes and any(a != b and b != 0 for a, b in zip(codes, out_codes)):
             raise ValueError("each output must be of its gradient's dtype or float32")
+    if max_norm is not None and _repeated(ptrs if outs is None else outs, numels):
+        raise ValueError("a tensor to be written is given twice")
     need = _lib.grad_norm_workspace_bytes(_at(numels), n)
     if need == 0:
         raise SeamBlendError(-1, "grad_norm_workspace_bytes")

@@ -163,6 +163,11 @@ def test_refusals(sb):
         sb.grad_norm_clip([g], 1.0, out=[torch.zeros(6, 4, device="cuda")])
     with pytest.raises(ValueError):
         sb.grad_norm_clip([g], 1.0, out=[g.half()])
+    with pytest.raises(ValueError):
+        sb.grad_norm_clip([g, g], 1.0)
+    with pytest.raises(ValueError):
+        sb.grad_norm_clip([g, g.clone()], 1.0, out=[g, g])
+    assert sb.grad_norm([g, g]).item() == 0  # nothing is written
     flat = torch.zeros(40, device="cuda")
     for bad in (dict(max_norm=-1.0), dict(max_norm=float("nan")), dict(max_norm=1.0, eps=-1.0)):
         with pytest.raises(sb.SeamBlendError):

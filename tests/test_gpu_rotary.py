@@ -54,6 +54,16 @@ def test_head_shapes(sb, dtype, interleaved, d, part):
     check(sb, q, k, positions, f, interleaved, what=f"d={d} part={part}")
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,part", [(8192, 8192), (8191, 8190), (5000, 4096)])
+def test_longest_heads(sb, interleaved, d, part):
+    f, _ = sb.rotary_frequencies(part)
+    check(sb, draw((3, 1, d), BF16, 1), draw((3, 2, d), BF16, 2), torch.tensor([0, 5, 70000], device="cuda"), f,
+          interleaved, what="long heads")
+    with pytest.raises(sb.SeamBlendError):
+        sb.rotary(draw((1, 1, 8194), F32, 1), torch.zeros(1, dtype=torch.int64, device="cuda"), f)
+
+
 @pytest.mark.parametrize("heads", [(1, 1), (2, 1), (8, 2), (12, 12), (32, 8), (40, 40), (130, 2)])
 @pytest.mark.parametrize("tokens", [1, 2, 33, 257])
 def test_head_and_token_counts(sb, heads, tokens):

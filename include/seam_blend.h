@@ -346,7 +346,7 @@ size_t grad_norm_workspace_bytes(const int64_t *numels, int64_t n);
 /*
  * norm = sqrt(sum of g^2 over every element of n tensors), written to a device
  * float.  grads: host array of device pointers, each to numels[k] contiguous
- * elements of dtypes[k] (not read where numels[k] == 0); at most 2^20 tensors
+ * elements of dtypes[k] (not read where numels[k] == 0); at most 2^16 tensors
  * and 2^44 elements.  Squares are formed and summed in 64 bits, in a fixed
  * order.  workspace: device scratch, 16-byte aligned.
  */

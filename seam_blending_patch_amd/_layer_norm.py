@@ -8,6 +8,7 @@ from array import array
 from typing import Optional, Tuple
 
 import torch
+from torch import Tensor, empty_like
 
 from . import _DTYPE, _lib, SeamBlendError
 from ._call import call, like
@@ -23,11 +24,12 @@ _lib.layer_norm_backward.argtypes = [_ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_floa
                                      ctypes.c_int, _ptr, _ptr, _ptr, _ptr, _ptr, ctypes.c_size_t, _ptr]
 _lib.layer_norm_backward.restype = ctypes.c_int
 _DENSE = torch.contiguous_format
+_F32 = torch.float32
 
 
 def _rows(t: torch.Tensor, name: str):
     """(shape, dtype code) of a tensor of rows"""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU (HIP) tensor")
     code = _DTYPE.get(t.dtype)
     if code is None:
@@ -64,21 +66,29 @@ def _outer_axes(tensors):
     return array("q", [1] * len(pad) + ext + [shape[-1]] + [v for s in strides for v in pad + s])
 
 
-def _geometry(d: int, *tensors: torch.Tensor):
-    """The library's shape and strides for tensors of one shape, in one array:
-    the shape at its start, the k-th tensor's strides 24 + 16 k bytes on."""
+@functools.lru_cache(maxsize=256)
+def _whole_rows(rows: int, d: int):
+    a = array("q", (1, rows, d, 0, d, 0, d, 0, d))
+    return a, a.buffer_info()[0]
+
+
+def _geometry(rows: int, d: int, *tensors: torch.Tensor):
+    """The library's shape and strides for tensors of one shape, in one array
+    (with its address): the shape at its start, the k-th tensor's strides
+    24 + 16 k bytes on."""
     for t in tensors:
         if not t.is_contiguous():
-            return _outer_axes(tensors)
-    return array("q", (1, t.numel() // d, d, 0, d, 0, d, 0, d))
+            a = _outer_axes(tensors)
+            return a, a.buffer_info()[0]
+    return _whole_rows(rows, d)
 
 
 def _weight(t: torch.Tensor, name: str, d: int, x_dtype, index: int, dtype):
     """Checks one weight or its gradient; the dtype it shares with the others."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+    if not isinstance(t, Tensor) or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on x's device")
     own = t.dtype
-    if t.numel() != d or (own is not x_dtype and own is not torch.float32):
+    if t.numel() != d or (own is not x_dtype and own is not _F32):
         raise ValueError(f"{name} must be [{d}] of x's dtype or float32")
     if dtype is not None and own is not dtype:
         raise ValueError("the weights and their gradients must be of one dtype")
@@ -108,15 +118,15 @@ def _forward(x, gamma, beta, eps, out):
     if beta is not None:
         dtype, bp = _weight(beta, "beta", d, x.dtype, index, dtype), beta.data_ptr()
     if out is None:
-        out = torch.empty_like(x, memory_format=_DENSE)
+        out = empty_like(x, memory_format=_DENSE)
     else:
         _like(out, "out", shape, code, index)
-    geometry = _geometry(d, x, out)
-    at = geometry.buffer_info()[0]
+    rows = x.numel() // d
+    geometry, at = _geometry(rows, d, x, out)
     need, wp = 0, None
     if d > _LONG:  # such rows are split, their statistics merged through a workspace
-        need = _forward_workspace_bytes(geometry[0] * geometry[1], d, code)
-        geometry = (geometry, torch.empty_like(like(index, need, torch.uint8), memory_format=_DENSE))
+        need = _forward_workspace_bytes(rows, d, code)
+        geometry = (geometry, empty_like(like(index, need, torch.uint8), memory_format=_DENSE))
         wp = geometry[1].data_ptr()
     return out, index, (x.data_ptr(), at + 24, at, eps, gp, bp, code, code if dtype is None else _DTYPE[dtype],
                         out.data_ptr(), at + 40, wp, need), geometry
@@ -184,22 +194,22 @@ def _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace):
         if dtype is None:
             dtype = torch.float32
         if dgamma is None:
-            dgamma = torch.empty_like(like(index, d, dtype), memory_format=_DENSE)
+            dgamma = empty_like(like(index, d, dtype), memory_format=_DENSE)
         if dbeta is None:
-            dbeta = torch.empty_like(like(index, d, dtype), memory_format=_DENSE)
+            dbeta = empty_like(like(index, d, dtype), memory_format=_DENSE)
     if dx is None:
-        dx = torch.empty_like(x, memory_format=_DENSE)
+        dx = empty_like(x, memory_format=_DENSE)
     else:
         _like(dx, "dx", shape, code, index)
+    rows = x.numel() // d
     if workspace is None:
-        need = _workspace_bytes(index, x.numel() // d, d, code)
-        workspace = torch.empty_like(like(index, need, torch.uint8), memory_format=_DENSE)
+        need = _workspace_bytes(index, rows, d, code)
+        workspace = empty_like(like(index, need, torch.uint8), memory_format=_DENSE)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor on x's device")
     else:
         need = workspace.numel() * workspace.element_size()
-    geometry = _geometry(d, dy, x, dx)
-    at = geometry.buffer_info()[0]
+    geometry, at = _geometry(rows, d, dy, x, dx)
     return (dx, dgamma, dbeta), index, (
         dy.data_ptr(), at + 24, x.data_ptr(), at + 40, at, eps, gp, code, code if dtype is None else _DTYPE[dtype],
         dx.data_ptr(), at + 56, None if dgamma is None else dgamma.data_ptr(),

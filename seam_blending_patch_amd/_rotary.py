@@ -8,6 +8,7 @@ from array import array
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
+from torch import Tensor, empty_like
 
 from . import _DTYPE, _lib
 from ._call import call
@@ -19,6 +20,7 @@ _lib.rotary_apply.argtypes = [_ptr, _ptr, _ptr, _ptr, _i64, _ptr, _ptr, _ptr, _p
                               ctypes.c_float, ctypes.c_int, _ptr]
 _lib.rotary_apply.restype = ctypes.c_int
 _DENSE = torch.contiguous_format
+_INTEGERS = (torch.int64, torch.int32)
 
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -69,7 +71,7 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
 
 def _heads(t: torch.Tensor, name: str):
     """(shape, strides [B, T, heads]) of a tensor of heads"""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU (HIP) tensor")
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
@@ -85,7 +87,7 @@ def _heads(t: torch.Tensor, name: str):
 def _output(like: torch.Tensor, shape, out: Optional[torch.Tensor], name: str):
     """(output, its strides)"""
     if out is None:
-        out = torch.empty_like(like, memory_format=_DENSE)
+        out = empty_like(like, memory_format=_DENSE)
         s = out.stride()
         return out, s[:3] if len(s) == 4 else (0, s[0], s[1])
     out_shape, s = _heads(out, name)
@@ -99,11 +101,11 @@ def _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, 
     shape, q_strides = _heads(q, "q")
     index, dtype = q.get_device(), q.dtype
     batch, length = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
-    if not isinstance(freqs, torch.Tensor) or freqs.get_device() != index or freqs.dtype is not torch.float64 \
+    if not isinstance(freqs, Tensor) or freqs.get_device() != index or freqs.dtype is not torch.float64 \
             or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous 1-D float64 tensor on q's device")
-    if not isinstance(positions, torch.Tensor) or positions.get_device() != index \
-            or positions.dtype not in (torch.int64, torch.int32):
+    if not isinstance(positions, Tensor) or positions.get_device() != index \
+            or positions.dtype not in _INTEGERS:
         raise ValueError("positions must be an int64 or int32 tensor on q's device")
     pairs, ps, pn = freqs.numel(), positions.stride(), positions.shape
     if sections is None:

@@ -16,7 +16,7 @@ using sb::failf;
 
 namespace {
 
-constexpr int64_t kMaxTensors = 1 << 20;
+constexpr int64_t kMaxTensors = 1 << 16; // every block adds up a sum of each
 constexpr int64_t kMaxElements = (int64_t)1 << 44; // over all tensors
 
 struct ClipPlan {
@@ -24,7 +24,7 @@ struct ClipPlan {
 };
 
 int plan_clip(const int64_t *numels, int64_t n, ClipPlan &p) {
-  if (n < 0 || n > kMaxTensors) return failf(SB_EGEOM, "0..2^20 tensors (got %lld)", (long long)n);
+  if (n < 0 || n > kMaxTensors) return failf(SB_EGEOM, "0..2^16 tensors (got %lld)", (long long)n);
   if (n > 0 && !numels) return failf(SB_EARG, "null element counts");
   int64_t total = 0;
   for (int64_t k = 0; k < n; ++k) {

@@ -142,6 +142,16 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs
   }
 }
 
+// the total of float i of the blocks of partials, to where it belongs
+template <int WDT, int LANES, int V> __device__ __forceinline__ void store_column(const LNArgs &A, int64_t i, float t) {
+  const bool beta = i >= A.cols;
+  const uint32_t j = (uint32_t)(beta ? i - A.cols : i);
+  const uint32_t u = j / (LANES * V), k = j / LANES % V, l = j % LANES;
+  const int64_t col = ((int64_t)u * LANES + l) * V + k;
+  void *out = beta ? A.dbeta : A.dgamma;
+  if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(t);
+}
+
 // dx and the columns' sums in one pass over x and dy.  A block keeps taking
 // rows, a thread the same columns of each, so dgamma and dbeta add up in
 // registers; at the end the block's rows are merged and written as one block of
@@ -232,16 +242,22 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
     });
   }
   if (!A.part) return;
-  // columns in the order [u][k][lane], so that a wave's stores are contiguous
+  // Columns in the order [u][k][lane], so that a wave's stores are contiguous.
+  // A single block's sums are the weights' gradients themselves.
+  const bool alone = gridDim.x == 1;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float *part = A.part + ((int64_t)blockIdx.x * 2 + which) * COLS;
+    auto put = [&](int i, float t) {
+      if (alone) store_column<WDT, LANES, V>(A, which * COLS + i, t);
+      else part[i] = t;
+    };
     auto &v = which ? db : dg;
     if constexpr (COPIES == 1) {
 #pragma unroll
       for (int u = 0; u < NV; ++u)
 #pragma unroll
-        for (int k = 0; k < V; ++k) part[(u * V + k) * LANES + lane] = v[u][k];
+        for (int k = 0; k < V; ++k) put((u * V + k) * LANES + lane, v[u][k]);
     } else {
       if (which) __syncthreads();
 #pragma unroll
@@ -259,7 +275,7 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
         float t = merge[i];
 #pragma unroll
         for (int c = 1; c < COPIES; ++c) t += merge[c * COLS + i];
-        part[i] = t;
+        put(i, t);
       }
     }
   }
@@ -431,16 +447,6 @@ __global__ __launch_bounds__(kLNThreads) void ln_columns_kernel(const LNArgs A) 
   }
 }
 
-// the total of float i of the blocks of partials, to where it belongs
-template <int WDT, int LANES, int V> __device__ __forceinline__ void store_column(const LNArgs &A, int64_t i, float t) {
-  const bool beta = i >= A.cols;
-  const uint32_t j = (uint32_t)(beta ? i - A.cols : i);
-  const uint32_t u = j / (LANES * V), k = j / LANES % V, l = j % LANES;
-  const int64_t col = ((int64_t)u * LANES + l) * V + k;
-  void *out = beta ? A.dbeta : A.dgamma;
-  if (out && col < A.D) ((typename El<WDT>::bits *)out)[col] = (typename El<WDT>::bits)narrow<WDT>(t);
-}
-
 // dgamma and dbeta: the partials' sums, in a fixed order.  A block takes 16
 // floats of a block of partials (of 2 * cols), as 4 vectors; its 256 groups of
 // 4 threads take every 256th block of partials each, so that a thousand of
@@ -551,7 +557,7 @@ template <int DT, int WDT, int LANES, int NV> hipError_t launch_backward_rows(co
                                                    : ln_backward_kernel<DT, WDT, LANES, NV, false>;
     hipLaunchKernelGGL(kernel, dim3(a.nparts), dim3(T), 0, st, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.nparts == 1) return e;
   }
   return launch_reduce<WDT, LANES, kVec<DT>>(a, st);
 }

@@ -106,7 +106,10 @@ _LONG = 16384  # rows of up to 64 KiB need no workspace
 @functools.lru_cache(maxsize=256)
 def _forward_workspace_bytes(rows: int, d: int, code: int) -> int:
     shape = array("q", (1, rows, d))
-    return max(16, _lib.layer_norm_forward_workspace_bytes(shape.buffer_info()[0], code))
+    n = _lib.layer_norm_forward_workspace_bytes(shape.buffer_info()[0], code)
+    if n >> 63:
+        raise SeamBlendError(-2, "layer_norm_forward_workspace_bytes")
+    return max(16, n)
 
 
 def _forward(x, gamma, beta, eps, out):

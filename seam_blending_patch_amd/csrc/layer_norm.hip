@@ -70,9 +70,9 @@ template <int LANES, int NV> constexpr int kRowsTogether = NV == 1 && LANES <= 6
 // 1024 has one row (4096 x 16384 73 -> 78).
 template <int LANES, int ELEMENTS> constexpr bool kWeightsEarly = ELEMENTS <= 24 && LANES <= 256;
 
-// Forward.  Bound by the copy of the rows: 65536 x 2048 fp16, 537 MB in 100 us
-// (5.4 TB/s, a large copy's rate 5.2), 20280 x 12 heads of 128 bf16 out of a
-// packed projection, 125 MB in 23.8 us (5.2 TB/s), 20280 x 1536 bf16 in 20.5 us
+// Forward.  Bound by the copy of the rows: 65536 x 2048 fp16, 537 MB in 97 us
+// (5.5 TB/s, a large copy's rate 5.2), 20280 x 12 heads of 128 bf16 out of a
+// packed projection, 125 MB in 23.3 us (5.3 TB/s), 20280 x 1536 bf16 in 20.5 us
 // (within the last-level cache).  A wave to a row up to 256 vectors: no barrier.
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs A) {
@@ -156,9 +156,9 @@ template <int WDT, int LANES, int V> __device__ __forceinline__ void store_colum
 // rows, a thread the same columns of each, so dgamma and dbeta add up in
 // registers; at the end the block's rows are merged and written as one block of
 // partials.  The next row's vectors are requested before this row's are used.
-// Bound by the three rows it moves: 65536 x 2048 fp16, 805 MB in 148 us (5.4
-// TB/s, a large copy's rate 5.2) and 5 us for the reduction; 20280 x 1536 bf16,
-// 187 MB in 37.8 and 4.3 us.  (LNLayout has the layouts measured.)
+// Bound by the three rows it moves: 65536 x 2048 fp16, 805 MB in 144-150 us
+// (5.4-5.6 TB/s, a large copy's rate 5.2) and 5 us for the reduction; 20280 x
+// 1536 bf16, 187 MB in 36-38 and 4.9 us.  (LNLayout has the layouts measured.)
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const LNArgs A) {
   constexpr int V = kVec<DT>, T = kRowThreads<LANES>, GROUPS = T / LANES, COLS = LANES * NV * V;

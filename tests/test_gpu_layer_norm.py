@@ -69,7 +69,7 @@ def test_widths(sb, d, dtype):
     check(sb, x, dy, *weights(d, wt, d + 2), what=f"d={d}")
 
 
-@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 63, 64, 65, 257, 1031, 4099])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 16, 17, 63, 64, 65, 128, 129, 257, 1031, 4099])
 @pytest.mark.parametrize("d", [48, 320, 1280])
 def test_row_counts(sb, rows, d):
     check(sb, draw((rows, d), BF16, rows), draw((rows, d), BF16, rows + 1), *weights(d, F32, 5), what=f"rows={rows}")

@@ -155,10 +155,12 @@ template <int WDT, int LANES, int V> __device__ __forceinline__ void store_colum
 // dx and the columns' sums in one pass over x and dy.  A block keeps taking
 // rows, a thread the same columns of each, so dgamma and dbeta add up in
 // registers; at the end the block's rows are merged and written as one block of
-// partials.  The next row's vectors are requested before this row's are used.
-// Bound by the three rows it moves: 65536 x 2048 fp16, 805 MB in 144-150 us
-// (5.4-5.6 TB/s, a large copy's rate 5.2) and 5 us for the reduction; 20280 x
-// 1536 bf16, 187 MB in 36-38 and 4.9 us.  (LNLayout has the layouts measured.)
+// partials.  (Requesting the next row before this one is used costs more in
+// registers than it hides: 32768 x 4096 bf16 147 -> 173 us, 8192 x 16384 189 ->
+// 228, spilled.)
+// Bound by the three rows it moves: 65536 x 2048 fp16, 805 MB in 144-151 us
+// (5.3-5.6 TB/s, a large copy's rate 5.2) and 5 us for the reduction; 20280 x
+// 1536 bf16, 187 MB in 34.6 and 4.5 us.  (LNLayout has the layouts measured.)
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const LNArgs A) {
   constexpr int V = kVec<DT>, T = kRowThreads<LANES>, GROUPS = T / LANES, COLS = LANES * NV * V;
@@ -177,20 +179,16 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
       dg[u][k] = db[u][k] = 0.f;
     }
   });
-  Vec<16> xr[NV], gr[NV];
-  auto request = [&](int64_t row) {
-    // after the last row that one again, unused
-    const uint32_t at = (uint32_t)min(row, A.rows - 1);
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < A.rows; r0 += step) {
+    const int64_t row = r0 + group;
+    const uint32_t at = (uint32_t)min(row, A.rows - 1); // every lane takes part in the sums
     const int64_t xo = row_offset(at, A.inner, A.sx), go = row_offset(at, A.inner, A.sdy);
+    Vec<16> xr[NV], gr[NV];
     each<NV>([&](auto u) {
       xr[u] = request_row<DT, cover<NV, TAIL>(u)>(A.x, xo, (u * LANES + lane) * V, A.D);
       gr[u] = request_row<DT, cover<NV, TAIL>(u)>(A.dy, go, (u * LANES + lane) * V, A.D);
     });
-  };
-  const int64_t step = (int64_t)gridDim.x * GROUPS;
-  request((int64_t)blockIdx.x * GROUPS + group);
-  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < A.rows; r0 += step) {
-    const int64_t row = r0 + group;
     float x[NV][V], g[NV][V];
     each<NV>([&](auto u) {
       settle_row<DT, cover<NV, TAIL>(u)>(xr[u], (u * LANES + lane) * V, A.D);
@@ -198,7 +196,6 @@ __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const L
       unpack<DT, 16>(xr[u], x[u]);
       unpack<DT, 16>(gr[u], g[u]);
     });
-    request(row + step);
     if (row >= A.rows) { // an absent row adds nothing
 #pragma unroll
       for (int u = 0; u < NV; ++u)
@@ -576,7 +573,8 @@ template <int DT, int WDT> hipError_t launch_backward(const LNArgs &a, hipStream
   case 64 * 16 + 4: return launch_backward_rows<DT, WDT, 64, 4>(a, st);
   case 128 * 16 + 3: return launch_backward_rows<DT, WDT, 128, 3>(a, st);
   case 128 * 16 + 4: return launch_backward_rows<DT, WDT, 128, 4>(a, st);
-  case 512 * 16 + 2: return launch_backward_rows<DT, WDT, 512, 2>(a, st);
+  case 256 * 16 + 3: return launch_backward_rows<DT, WDT, 256, 3>(a, st);
+  case 256 * 16 + 4: return launch_backward_rows<DT, WDT, 256, 4>(a, st);
   case 1024 * 16 + 2: return launch_backward_rows<DT, WDT, 1024, 2>(a, st);
   }
   if (a.rows > 0) {

@@ -46,19 +46,19 @@ constexpr int kChunkVectors = 4; // vectors of a chunk on each of kLNThreads thr
 // vectors on each of LANES threads, as many rows to a block as it has room for
 // (lanes 0: the row is too long for registers and is split into chunks).
 // A wave to a row as long as the sums of its columns fit its registers: it
-// needs no barrier.  Measured in us, kernel and reduction (copy rate: 156 us for
-// each of these but the last, 37):
-//   65536 x 2048 fp16:  64 x 4 163    128 x 2 193    256 x 1 218
-//   32768 x 4096 bf16: 128 x 4 160    256 x 2 191
-//   16384 x 8192 bf16: 512 x 2 199    256 x 4 217
-//   243360 x 128 bf16, 16 x 1: 4 blocks a CU 42, 2 blocks 49, 6 blocks 43
+// needs no barrier; then the fewest waves.  Measured in us, kernel and reduction
+// (copy rate: 156 us for each of these but the last, 37):
+//   65536 x 2048 fp16:   64 x 4 157 (1, 3, 4 blocks a CU 175, 163, 158)
+//   32768 x 4096 bf16:  128 x 4 156
+//   16384 x 8192 bf16:  256 x 4 171   512 x 2 209
+//   8192 x 16384 bf16: 1024 x 2 183   512 x 4 178 (fp32, twice the bytes: 298, 313)
+//   243360 x 128 bf16:   16 x 1 41 (3, 6, 8 blocks a CU 43, 41, 44)
 struct LNLayout {
   int lanes, nv;
   int threads() const { return lanes > kLNThreads ? lanes : kLNThreads; }
   int rows() const { return threads() / lanes; } // of a block, at a time
-  // few blocks: each adds a row of partials to be written and read again (the
-  // first row above at 3 blocks 169, at 4 173); more of them only where a
-  // thread has little in flight
+  // few blocks: each adds a row of partials to be written and read again; more
+  // of them only where a thread has little in flight
   int blocks_per_cu() const { return nv == 1 ? 4 : lanes > kLNThreads ? 1 : 2; }
 };
 inline LNLayout backward_layout(int64_t nv) {
@@ -69,7 +69,7 @@ inline LNLayout backward_layout(int64_t nv) {
   }
   if (nv <= 256) return LNLayout{64, (int)(nv + 63) / 64};
   if (nv <= 512) return LNLayout{128, nv <= 384 ? 3 : 4};
-  if (nv <= 1024) return LNLayout{512, 2};
+  if (nv <= 1024) return LNLayout{256, nv <= 768 ? 3 : 4};
   if (nv <= kBackwardVectors) return LNLayout{1024, 2};
   return LNLayout{0, 0};
 }

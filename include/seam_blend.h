@@ -359,7 +359,9 @@ int grad_norm(const void *const *grads, const int64_t *numels, const int *dtypes
  * SB_F32), which is the gradient itself or shares no memory with any gradient
  * (checked against its own).  In place nothing is written when c is 1.  A norm
  * that is NaN or infinite scales by NaN or 0, as the formula says; the host is
- * not told (no synchronisation).  max_norm >= 0.
+ * not told (no synchronisation).  c is formed from the 64-bit norm, so finite
+ * gradients whose norm is past fp32 (it is written as infinite) are scaled as
+ * well.  max_norm >= 0.
  */
 int grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *numels, const int *dtypes,
                    const int *out_dtypes, int64_t n, float max_norm, float eps, float *norm, void *workspace,

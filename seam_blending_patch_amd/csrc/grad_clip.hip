@@ -6,7 +6,8 @@
 // its chunk.  No atomics, so the same inputs give the same bits.
 //
 // Squares are formed and summed in 64 bits: they neither overflow nor vanish
-// for any 32-bit gradient.
+// for any 32-bit gradient.  The factor is rounded to fp32 before it scales,
+// unless it is below fp32's normal numbers, which would cost it bits.
 
 #include "sb_row.h"
 #include "sb_transformer.h"
@@ -134,6 +135,27 @@ __device__ __forceinline__ void chunk_of(int types, const void *in, void *out, i
   }
 }
 
+// A chunk scaled in 64 bits, an element a thread at a time: for factors that
+// fp32 holds with fewer bits or not at all (norms 2^126 times the bound), while
+// the products may be ordinary numbers.
+template <int DT, int ODT>
+__device__ __forceinline__ void chunk_scale_f64(const void *in, void *out, int64_t e0, int64_t e1, double by) {
+  for (int64_t e = e0 + threadIdx.x; e < e1; e += kClipThreads) {
+    const float f = widen<DT>(((const typename El<DT>::bits *)in)[e]);
+    ((typename El<ODT>::bits *)out)[e] = (typename El<ODT>::bits)narrow<ODT>((float)(f * by));
+  }
+}
+
+__device__ __forceinline__ void chunk_of_f64(int types, const void *in, void *out, int64_t e0, int64_t e1, double by) {
+  switch (types) {
+  case DT_F32 | DT_F32 << 2: chunk_scale_f64<DT_F32, DT_F32>(in, out, e0, e1, by); break;
+  case DT_F16 | DT_F16 << 2: chunk_scale_f64<DT_F16, DT_F16>(in, out, e0, e1, by); break;
+  case DT_F16 | DT_F32 << 2: chunk_scale_f64<DT_F16, DT_F32>(in, out, e0, e1, by); break;
+  case DT_BF16 | DT_F32 << 2: chunk_scale_f64<DT_BF16, DT_F32>(in, out, e0, e1, by); break;
+  default: chunk_scale_f64<DT_BF16, DT_BF16>(in, out, e0, e1, by); break;
+  }
+}
+
 __global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipArgs A) {
   double s = 0.0;
   for (int i = threadIdx.x; i < A.npartials; i += kClipThreads) s += A.partials[i];
@@ -145,7 +167,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(const ClipArgs A) {
   const int t = find_tensor(A, blockIdx.x);
   if (c == 1.0f && A.in[t] == A.out[t]) return; // in place and nothing to scale
   const int64_t e0 = (int64_t)(blockIdx.x - A.begin[t]) * A.chunk, e1 = min(e0 + A.chunk, A.n[t]);
-  if (A.nt) chunk_of<true>(A.types[t], A.in[t], A.out[t], e0, e1, c);
+  if (by > 0.0 && by < 0x1p-126) chunk_of_f64(A.types[t], A.in[t], A.out[t], e0, e1, by);
+  else if (A.nt) chunk_of<true>(A.types[t], A.in[t], A.out[t], e0, e1, c);
   else chunk_of<false>(A.types[t], A.in[t], A.out[t], e0, e1, c);
 }
 

@@ -30,10 +30,14 @@ struct Strided {
     ext[k] = extent;
     str[k] = stride;
   }
-  // elements from the first to the last of the axes from `level` on
+  // elements from the first to the last of the axes from `level` on; kMaxSpan
+  // where they are that many or more (an extent times a stride passes 64 bits)
   int64_t span(int level = 0) const {
     int64_t s = run;
-    for (int k = level; k < n; ++k) s += (ext[k] - 1) * str[k];
+    for (int k = level; k < n; ++k) {
+      if (ext[k] > 1 && str[k] > (kMaxSpan - s) / (ext[k] - 1)) return kMaxSpan;
+      s += (ext[k] - 1) * str[k];
+    }
     return s;
   }
   // no element is reached by two indices

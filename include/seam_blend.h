@@ -326,7 +326,7 @@ int layer_norm_backward(const void *dy, const int64_t dy_stride[2], const void *
  *                interleaves are refused.
  *   freqs        device pointer to rot_dim / 2 doubles: radians per position.
  *   positions    device pointer to 4- or 8-byte signed integers, strides
- *                {axis, B, T} in elements (0 broadcasts).
+ *                {axis, B, T} in elements, 0..2^40 (0 broadcasts).
  *   sections     n_sections (1..4) pair counts that add up to rot_dim / 2:
  *                consecutive pairs turn by the positions of axis 0, 1, ...
  * The angle is formed and reduced in 64 bits, cosine and sine in fp32, one

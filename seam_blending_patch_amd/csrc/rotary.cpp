@@ -79,6 +79,12 @@ extern "C" int rotary_apply(const void *q, const int64_t q_stride[3], void *q_ou
   for (int k2 = 0; k2 < 3; ++k2)
     if (position_stride[k2] < 0 || position_stride[k2] >= sb::kMaxStride)
       return failf(SB_EGEOM, "strides of positions must be in 0..2^40 elements");
+  sb::Strided sp;
+  sp.run = 1;
+  sp.add(n_sections, position_stride[0]);
+  sp.add(B, position_stride[1]);
+  sp.add(T, position_stride[2]);
+  if (sp.span() >= sb::kMaxSpan) return failf(SB_EGEOM, "positions span 2^52 elements or more");
 
   const void *in[2] = {q, k};
   void *out[2] = {q_out, k_out};

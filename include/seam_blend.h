@@ -356,8 +356,9 @@ int grad_norm(const void *const *grads, const int64_t *numels, const int *dtypes
 /*
  * grad_norm, and every gradient times c = min(1, max_norm / (norm + eps)): in
  * place where outs is NULL, else into outs[k] of out_dtypes[k] (dtypes[k], or
- * SB_F32), which is the gradient itself or shares no memory with any gradient
- * (checked against its own).  In place nothing is written when c is 1.  A norm
+ * SB_F32), which is the gradient itself or shares no memory with any gradient.
+ * No two tensors that are written share memory (both checked; SB_EARG); what is
+ * only read may.  In place nothing is written when c is 1.  A norm
  * that is NaN or infinite scales by NaN or 0, as the formula says; the host is
  * not told (no synchronisation).  c is formed from the 64-bit norm, so finite
  * gradients whose norm is past fp32 (it is written as infinite) are scaled as

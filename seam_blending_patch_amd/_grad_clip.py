@@ -126,7 +126,8 @@ def grad_norm_clip(grads: Sequence[torch.Tensor], max_norm: float, eps: float = 
     """Scales the gradients by ``min(1, max_norm / (norm + eps))``, norm the
     2-norm over all of them, in place or into ``out`` (tensors of the same shapes
     and strides, of the gradients' dtypes or float32: the 32-bit gradients an
-    optimizer takes).  Returns the norm before clipping, a float32 scalar on the
+    optimizer takes).  A tensor that is written may share memory with no other
+    tensor of the call (refused).  Returns the norm before clipping, a float32 scalar on the
     GPU.  Nothing is waited for: a norm that is NaN or infinite shows in it and,
     as the formula says, in the gradients."""
     norm, _, index, function, name, args, keep = _clip(grads, max_norm, eps, out)

@@ -8,6 +8,8 @@
 
 #include <algorithm>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "sb_host.h"
 #include "sb_transformer.h"
@@ -44,6 +46,52 @@ int plan_clip(const int64_t *numels, int64_t n, ClipPlan &p) {
   return SB_OK;
 }
 
+// A tensor's bytes, and its place in the list.
+struct Run {
+  uintptr_t begin, end;
+  int64_t k;
+};
+
+// What is written shares no byte with anything else that the call reads or
+// writes: blocks scale and read in any order.  (An output over its own gradient
+// is the caller's check.)
+int check_written(const void *const *grads, void *const *outs, const int64_t *numels, const int *dtypes,
+                  const int *out_dtypes, int64_t n) {
+  auto run = [&](int64_t k, bool out) {
+    const uintptr_t p = out ? (uintptr_t)outs[k] : (uintptr_t)grads[k];
+    return Run{p, p + (uintptr_t)(numels[k] * sb::elem_bytes(out ? out_dtypes[k] : dtypes[k])), k};
+  };
+  const std::unique_ptr<Run[]> held(new (std::nothrow) Run[n > 0 ? n : 1]);
+  if (!held) return failf(SB_EGEOM, "no host memory for the table of %lld tensors", (long long)n);
+  Run *const first = held.get(), *last = first;
+  bool ascending = true; // views of a bucket mostly are
+  for (int64_t k = 0; k < n; ++k) {
+    if (numels[k] == 0) continue;
+    *last = run(k, outs != nullptr);
+    ascending = ascending && (last == first || last[-1].end <= last->begin);
+    ++last;
+  }
+  if (!ascending) {
+    std::sort(first, last, [](const Run &a, const Run &b) { return a.begin < b.begin; });
+    for (const Run *r = first + 1; r < last; ++r)
+      if (r->begin < r[-1].end) {
+        const char *what = outs ? "output" : "gradient";
+        return failf(SB_EARG, "%s %lld shares memory with %s %lld, and both are written", what, (long long)r->k, what,
+                     (long long)r[-1].k);
+      }
+  }
+  if (!outs) return SB_OK;
+  for (int64_t k = 0; k < n; ++k) {
+    if (numels[k] == 0) continue;
+    const Run g = run(k, false);
+    const Run *r = std::upper_bound(first, last, g.begin, [](uintptr_t p, const Run &a) { return p < a.end; });
+    for (; r < last && r->begin < g.end; ++r)
+      if (r->k != k)
+        return failf(SB_EARG, "output %lld shares memory with gradient %lld", (long long)r->k, (long long)k);
+  }
+  return SB_OK;
+}
+
 int clip_call(const void *const *grads, void *const *outs, const int64_t *numels, const int *dtypes,
               const int *out_dtypes, int64_t n, bool scale, float max_norm, float eps, float *norm, void *workspace,
               size_t workspace_bytes, void *stream) {
@@ -70,6 +118,7 @@ int clip_call(const void *const *grads, void *const *outs, const int64_t *numels
     if (!(g == o && dtypes[k] == out_dtypes[k]) && g < o + on && o < g + gn)
       return failf(SB_EARG, "output %lld overlaps its gradient without being it", (long long)k);
   }
+  if (scale && (rc = check_written(grads, outs, numels, dtypes, out_dtypes, n))) return rc;
   if (!workspace || !sb::aligned(workspace, 16)) return failf(SB_EARG, "workspace must be 16-byte aligned device memory");
   const size_t need = (size_t)std::max<int64_t>(p.chunks, 2) * sizeof(double);
   if (workspace_bytes < need)

@@ -74,3 +74,21 @@ def test_factors_below_the_normal_numbers_and_not_finite_gradients(sb, bad):
         assert torch.isposinf(norm) and torch.isnan(outs[0][7])
         outs[0][7] = 0
         assert not outs[0].any()
+
+
+def test_tensors_that_share_memory_are_refused_and_stay(sb):
+    bucket = torch.randn(100, generator=torch.Generator().manual_seed(1)).cuda()
+    before, other = bucket.clone(), torch.zeros(60, device="cuda")
+    grads = [bucket[:60], bucket[56:]]
+    for call in (lambda: sb.grad_norm_clip(grads, 1e-3), lambda: sb.GradNormClip(grads, 1e-3)(),
+                 lambda: sb.grad_norm_clip([other, bucket[:60]], 1e-3, out=[bucket[40:], other])):
+        with pytest.raises(sb.SeamBlendError) as e:
+            call()
+        assert e.value.code == -1 and "shares memory" in str(e.value)
+    assert torch.equal(bucket, before) and not other.any()
+    # read alone, or written elsewhere, they may
+    want = ref.clip([ref.f64(g) for g in grads], 1e-3, EPS)
+    norm, outs = clipped(sb, grads, 1e-3, [F32, F32])
+    assert abs(norm.item() - want[0]) <= want[1] and torch.equal(sb.grad_norm(grads), norm)
+    for o, w, t in zip(outs, want[2], want[3]):
+        ref.assert_near(o, w, t, "shared")

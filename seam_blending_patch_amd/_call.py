@@ -5,6 +5,7 @@ from __future__ import annotations
 import functools
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _check
 
@@ -32,3 +33,10 @@ def call(function, name: str, index: int, args):
             rc = function(*args, _raw_stream(index))
     if rc:
         _check(rc, name)
+
+
+def written(*tensors):
+    """Counts a caller's tensors (those that are not None) as written, as torch
+    does for its own operations: a backward pass that saved one is refused
+    instead of computed from what the call left in it."""
+    increment_version([t for t in tensors if t is not None])

@@ -7,6 +7,7 @@ from array import array
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _DTYPE, _lib, SeamBlendError
 from ._call import call, like
@@ -48,10 +49,12 @@ def _table(tensors: Sequence[torch.Tensor], name: str, index: int):
     return ptrs, codes, whole
 
 
-def _repeated(ptrs: array, numels: array) -> bool:
-    """Whether a tensor with elements is written to twice."""
-    return len(set(ptrs)) != len(ptrs) and len(set(p for p, n in zip(ptrs, numels) if n)) != sum(
-        1 for n in numels if n)
+def _refuse_repeated(keep):
+    """Raises where a tensor with elements is written to twice."""
+    ptrs, _, numels, outs, *_ = keep
+    written = [p for p, n in zip(ptrs if outs is None else outs, numels) if n]
+    if len(set(written)) != len(written):
+        raise ValueError("a tensor to be written is given twice")
 
 
 def _at(a: array) -> int:
@@ -79,8 +82,6 @@ def _clip(grads, max_norm, eps, out):
             raise ValueError("each output must have its gradient's shape and strides")
         if out_codes != codes and any(a != b and b != 0 for a, b in zip(codes, out_codes)):
             raise ValueError("each output must be of its gradient's dtype or float32")
-    if max_norm is not None and _repeated(ptrs if outs is None else outs, numels):
-        raise ValueError("a tensor to be written is given twice")
     need = _lib.grad_norm_workspace_bytes(_at(numels), n)
     if need == 0:
         raise SeamBlendError(-1, "grad_norm_workspace_bytes")
@@ -106,10 +107,14 @@ class GradNormClip:
         grads = list(grads)
         self.norm, self.out, index, self._function, self._name, self._args, keep = _clip(grads, max_norm, eps, out)
         self.device = torch.device("cuda", index)
+        if max_norm is not None:
+            _refuse_repeated(keep)
         self._keep = (grads, keep)
+        self._written = [self.norm] if max_norm is None else [self.norm, *self.out]
 
     def __call__(self) -> torch.Tensor:
         call(self._function, self._name, self.device.index, self._args)
+        increment_version(self._written)  # as torch counts its own writes
         return self.norm
 
 
@@ -130,6 +135,11 @@ def grad_norm_clip(grads: Sequence[torch.Tensor], max_norm: float, eps: float = 
     tensor of the call (refused).  Returns the norm before clipping, a float32 scalar on the
     GPU.  Nothing is waited for: a norm that is NaN or infinite shows in it and,
     as the formula says, in the gradients."""
-    norm, _, index, function, name, args, keep = _clip(grads, max_norm, eps, out)
-    call(function, name, index, args)
+    norm, out, index, function, name, args, keep = _clip(grads, max_norm, eps, out)
+    try:
+        call(function, name, index, args)
+    except SeamBlendError:
+        _refuse_repeated(keep)  # the library's answer to it is that they share memory
+        raise
+    increment_version(out)  # as torch counts its own writes
     return norm

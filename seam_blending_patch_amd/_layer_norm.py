@@ -11,7 +11,7 @@ import torch
 from torch import Tensor, empty_like
 
 from . import _DTYPE, _lib, SeamBlendError
-from ._call import call, like
+from ._call import call, like, written
 
 _ptr = ctypes.c_void_p  # of shapes and strides too: places in one array.array
 _lib.layer_norm_forward.argtypes = [_ptr, _ptr, _ptr, ctypes.c_float, _ptr, _ptr, ctypes.c_int, ctypes.c_int, _ptr,
@@ -147,6 +147,7 @@ class LayerNorm:
 
     def __call__(self) -> torch.Tensor:
         call(_lib.layer_norm_forward, "layer_norm_forward", self.device.index, self._args)
+        written(self.out)
         return self.out
 
 
@@ -156,10 +157,13 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     ``(x - mean) / sqrt(var + eps) * gamma + beta``, statistics in fp32, rounded
     once.  The last axis must be contiguous; the others may be strided (views
     of a packed projection) as long as they merge into two.  gamma / beta: [D]
-    of x's dtype or float32, or None.  ``out`` may be ``x``."""
-    out, index, args, geometry = _forward(x, gamma, beta, eps, out)
+    of x's dtype or float32, or None.  ``out`` may be ``x``.  The result carries
+    no autograd history: its gradient is layer_norm_backward."""
+    y, index, args, geometry = _forward(x, gamma, beta, eps, out)
     call(_lib.layer_norm_forward, "layer_norm_forward", index, args)
-    return out
+    if out is not None:
+        written(out)
+    return y
 
 
 @functools.lru_cache(maxsize=256)
@@ -233,6 +237,7 @@ class LayerNormBackward:
 
     def __call__(self) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
         call(_lib.layer_norm_backward, "layer_norm_backward", self.device.index, self._args)
+        written(*self.out)
         return self.out
 
 
@@ -246,7 +251,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
     (of gamma's dtype; float32 without gamma) are formed; by default where gamma
     or one of them is given, None in their place otherwise.  They are written,
     not added to.  ``dx`` may be ``dy`` or ``x``.  ``workspace``: optional uint8
-    GPU tensor of at least layer_norm_backward_workspace_bytes(x) bytes."""
+    GPU tensor of at least layer_norm_backward_workspace_bytes(x) bytes.  The
+    results carry no autograd history."""
     out, index, args, keep = _backward(dy, x, gamma, eps, dx, dgamma, dbeta, weight_grads, workspace)
     call(_lib.layer_norm_backward, "layer_norm_backward", index, args)
+    if dx is not None or dgamma is not None or dbeta is not None:
+        written(dx, dgamma, dbeta)
     return out

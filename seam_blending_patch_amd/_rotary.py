@@ -11,7 +11,7 @@ import torch
 from torch import Tensor, empty_like
 
 from . import _DTYPE, _lib
-from ._call import call
+from ._call import call, written
 
 _i64 = ctypes.c_int64
 _ptr = ctypes.c_void_p  # of shapes, strides and sections too: places in one array.array
@@ -159,6 +159,7 @@ class Rotary:
 
     def __call__(self) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
         call(_lib.rotary_apply, "rotary_apply", self.device.index, self._args)
+        written(*(self.out if isinstance(self.out, tuple) else (self.out,)))
         return self.out
 
 
@@ -173,10 +174,13 @@ def rotary(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, k: Opt
     ``scale``; the rest is copied.  positions: int64 or int32 [T] or [B, T];
     with ``sections`` (pair counts) a leading axis holds the positions each
     section turns by.  ``out`` / ``k_out`` may be ``q`` / ``k``.  Returns the
-    turned q, or (q, k)."""
-    out, index, args, table = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, False)
+    turned q, or (q, k), without autograd history: the gradient is
+    rotary_backward."""
+    turned, index, args, table = _rotation(q, positions, freqs, k, interleaved, sections, scale, out, k_out, False)
     call(_lib.rotary_apply, "rotary_apply", index, args)
-    return out
+    if out is not None or k_out is not None:
+        written(out, k_out)
+    return turned
 
 
 def rotary_backward(dq: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
@@ -185,6 +189,8 @@ def rotary_backward(dq: torch.Tensor, positions: torch.Tensor, freqs: torch.Tens
                     out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
     """Gradient of rotary: the gradients of its outputs (dq, and k's as ``k``)
     turned back.  Arguments as rotary's."""
-    out, index, args, table = _rotation(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, True)
+    turned, index, args, table = _rotation(dq, positions, freqs, k, interleaved, sections, scale, out, k_out, True)
     call(_lib.rotary_apply, "rotary_apply", index, args)
-    return out
+    if out is not None or k_out is not None:
+        written(out, k_out)
+    return turned

@@ -7,8 +7,10 @@
 // transpose (the gradient) turns by -a.
 //
 // The angle is formed in 64 bits as turns and reduced by its nearest whole
-// number before it is rounded to fp32, so that a position of a million costs
-// no accuracy; cosine and sine are then fp32 functions of at most half a turn.
+// number, so that a position of a million costs no accuracy; cosine and sine are
+// then fp32 functions of at most half a turn, rounded to fp32, and the little
+// that this rounding left out (up to 2^-26 turns, more than an fp32 cosine's own
+// error) turns them on by its own first order.
 
 #include "sb_row.h"
 #include "sb_transformer.h"
@@ -28,9 +30,11 @@ __device__ __forceinline__ float2 cos_sin(const RotaryArgs &A, int pair, uint32_
   for (int a = 0; a + 1 < kRotaryMaxAxes; ++a) axis += a + 1 < A.axes && pair >= A.ends[a];
   constexpr double kTurns = 0.15915494309189533577; // 1 / (2 pi)
   const double turns = (double)read_position(A, axis, b, t) * (A.freqs[pair] * kTurns);
+  const double part = turns - rint(turns);
+  const float near = (float)part, rest = 6.28318531f * (float)(part - (double)near);
   float s, c;
-  sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-  return make_float2(c * A.scale, s * A.scale_sin);
+  sincospif(2.0f * near, &s, &c);
+  return make_float2(fmaf(-s, rest, c) * A.scale, fmaf(c, rest, s) * A.scale_sin);
 }
 
 // field by field, so that it is selects among scalar registers and no load at

@@ -38,7 +38,10 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[st
       "by_parts"  pairs that turn more than high_turns times over
                   original_length are kept, those below low_turns slowed by
                   factor, those between mixed linearly in their turns; the
-                  factor for ``scale`` is 0.1 ln(factor) + 1.
+                  factor for ``scale`` is 0.1 ln(factor) + 1 (1 for a factor
+                  up to 1).  Programs differ here: some mix linearly in the
+                  pair's index, between two rounded ones, some scale by 1.  Give
+                  weights tuned with such a program its own frequencies and scale.
     """
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and at least 2")

@@ -35,10 +35,11 @@ int plan_clip(const int64_t *numels, int64_t n, ClipPlan &p) {
     total += numels[k];
   }
   // Chunks of 8192 elements, longer where that would be more than 4096 of
-  // them.  First pass and second, us: 4.7 M fp32 elements at 4096 a chunk 8.0 +
-  // 4.4, at 8192 6.7 + 3.8, at 16384 10.4 + 3.9; 251 M bf16 ones into fp32 at
-  // most 2048, 4096 and 8192 chunks 87 + 311, 85 + 298 and 86 + 294, 22.6 M fp32
-  // ones 37 + 63, 34 + 66 and 33 + 72 (every block adds up all chunks' sums).
+  // them.  First pass and second, us: 4.7 M fp32 elements that stay at 4096 a
+  // chunk 6.4 + 4.6, at 8192 6.2 + 3.7, at 16384 6.4 + 3.3, and 22.6 M fp32 ones
+  // into others 23 + 36, 23 + 33 and 24 + 32; 251 M bf16 ones into fp32 at most
+  // 2048, 4096 and 8192 chunks 90 + 312, 86 + 299 and 85 + 318, 47 M 17 + 46,
+  // 18 + 51 and 17 + 56 (every block adds up all chunks' sums).
   constexpr int64_t step = sb::kClipThreads * 8;
   p.chunk = std::max<int64_t>(8192, (total / 4096 + step - 1) / step * step);
   p.chunks = 0;
@@ -126,8 +127,12 @@ int clip_call(const void *const *grads, void *const *outs, const int64_t *numels
 
   // Outputs past the caches where gradients and outputs are more than the
   // last-level one holds: the gradients stay in it, and the next call's first
-  // pass does not wait for the outputs to leave it.  (22.6 M fp32 gradients
-  // into another 90 MB: 49 + 72 -> 34 + 67 us.)
+  // pass does not wait for the outputs to leave it.  Below that, an update that
+  // reads the outputs next finds them there.  us with the hint and without, the
+  // clip alone and (with such an update behind it): fp32 into fp32, 181 MB moved
+  // 51 / 58 (105 / 102), 240 MB 67 / 79 (135 / 138), 300 MB 85 / 103 (165 / 180),
+  // 1 GB 300 / 307 (576 / 585); bf16 into fp32, 181 MB 52 / 61 (121 / 115), 240 MB
+  // 64 / 75 (153 / 165), 300 MB 77 / 101 (187 / 214), 1 GB 279 / 281 (638 / 643).
   int64_t moved = 0;
   for (int64_t k = 0; k < n; ++k)
     moved += numels[k] * (sb::elem_bytes(dtypes[k]) + (outs ? sb::elem_bytes(out_dtypes[k]) : 0));

@@ -95,7 +95,7 @@ __device__ __forceinline__ void chunk_scale(const void *in, void *out, int64_t e
 
 // 16-bit gradients into fp32 ones, 4 elements a thread: a wave's stores are one
 // run of 1 KiB.  (With 8 elements a thread, in two stores 32 bytes apart from
-// lane to lane, 251 M bf16 elements took 428 us past the caches; these 298.)
+// lane to lane, 251 M bf16 elements took 428 us past the caches; these 299.)
 template <int DT, bool NT>
 __device__ __forceinline__ void chunk_widen(const void *in, void *out, int64_t e0, int64_t e1, float c) {
   constexpr int STEP = kClipThreads * 4, BATCH = 2 * kClipBatch;

@@ -70,9 +70,15 @@ int check_types(int dtype, int wdtype, const void *const *weights, int n) {
   return SB_OK;
 }
 
-// Stores pass the caches where the output alone fills the last-level one:
-// 65536 x 2048 fp16 forward 99.4 -> 97.5 us, backward 155.5 -> 151.  Below that
-// the next operator finds the rows there.
+// Stores pass the caches where the output alone fills the last-level one; below
+// that, an operator that reads the rows next finds them there.  us with the hint
+// and without, a call alone and (with such a reader behind it), rows of 2048 fp16:
+//   output    forward                       backward
+//    64 MB    25.4 /  32.2 ( 56 /  51)       47.5 /  48.9 ( 73 /  73)
+//   128 MB    50.9 /  53.8 (100 / 101)       83.0 /  85.4 (137 / 134)
+//   256 MB    94.9 /  99.0 (190 / 188)      156   / 159   (257 / 249)
+//   512 MB   184   / 191   (364 / 363)      303   / 309   (489 / 484)
+//     1 GB   365   / 375   (715 / 718)      605   / 621   (966 / 967)
 bool past_caches(const sb::LNArgs &a, int dtype) {
   return a.rows * (int64_t)a.D * sb::elem_bytes(dtype) >= sb::kLastLevelBytes;
 }

@@ -70,9 +70,9 @@ template <int LANES, int NV> constexpr int kRowsTogether = NV == 1 && LANES <= 6
 // 1024 has one row (4096 x 16384 73 -> 78).
 template <int LANES, int ELEMENTS> constexpr bool kWeightsEarly = ELEMENTS <= 24 && LANES <= 256;
 
-// Forward.  Bound by the copy of the rows: 65536 x 2048 fp16, 537 MB in 97 us
+// Forward.  Bound by the copy of the rows: 65536 x 2048 fp16, 537 MB in 98 us
 // (5.5 TB/s, a large copy's rate 5.2), 20280 x 12 heads of 128 bf16 out of a
-// packed projection, 125 MB in 23.3 us (5.3 TB/s), 20280 x 1536 bf16 in 20.5 us
+// packed projection, 125 MB in 23.4 us (5.3 TB/s), 20280 x 1536 bf16 in 20.5 us
 // (within the last-level cache).  A wave to a row up to 256 vectors: no barrier.
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_row_kernel(const LNArgs A) {
@@ -160,7 +160,7 @@ template <int WDT, int LANES, int V> __device__ __forceinline__ void store_colum
 // 228, spilled.)
 // Bound by the three rows it moves: 65536 x 2048 fp16, 805 MB in 144-151 us
 // (5.3-5.6 TB/s, a large copy's rate 5.2) and 5 us for the reduction; 20280 x
-// 1536 bf16, 187 MB in 34.6 and 4.5 us.  (LNLayout has the layouts measured.)
+// 1536 bf16, 187 MB in 34.7 and 4.8 us.  (LNLayout has the layouts measured.)
 template <int DT, int WDT, int LANES, int NV, bool TAIL, bool NT = false>
 __global__ __launch_bounds__(kRowThreads<LANES>) void ln_backward_kernel(const LNArgs A) {
   constexpr int V = kVec<DT>, T = kRowThreads<LANES>, GROUPS = T / LANES, COLS = LANES * NV * V;

@@ -52,12 +52,13 @@ __device__ __forceinline__ RotaryTensor tensor_of(const RotaryArgs &A, bool key)
 // requested before that.
 //
 // Bound by the copy of the heads: 20280 tokens of 24 x 128 bf16, interleaved,
-// 250 MB in 45.8 us (5.45 TB/s, the rate of a large copy), 16384 tokens of 40 x
-// 128 in halves 335 MB in 58 us.  Measured against it: whole tokens to a block
-// 61 us for the first of these (a third of the threads idle), an angle for
-// every head's step of its own 109 us; 2 and 4 steps a thread 44.3 and 46.2 us
-// for the first but 62 and 67 us for the second.  With one head to a key, 64
-// pairs of angles to every 256 bytes, the angles show (3.4 TB/s).
+// 250 MB in 46.5 to 51 us (4.9 to 5.4 TB/s, the rate of a large copy), 16384
+// tokens of 40 x 128 in halves 335 MB in 58 to 62 us.  Measured against it:
+// whole tokens to a block 61 us for the first of these (a third of the threads
+// idle), an angle for every head's step of its own 109 us; 2 and 4 steps a
+// thread 44.3 and 46.2 us for the first but 62 and 67 us for the second.  With
+// one head to a key, 64 pairs of angles to every 256 bytes, the angles show:
+// 65536 tokens, 67 MB, in 19.8 us (3.4 TB/s; 19.4 if their rounding stayed).
 template <int DT, bool INTER>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs A) {
   constexpr int V = kVec<DT>;

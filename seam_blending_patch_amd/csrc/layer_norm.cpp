@@ -97,6 +97,7 @@ int64_t split_bytes(int64_t rows, int64_t d, int dtype, int64_t most) {
 // split_bytes.
 struct BackwardPlan {
   int64_t nparts, cols, part_bytes, rowstat_bytes;
+  int64_t blocks; // of a call that forms no weight gradients, and so no partials
 };
 
 int check_workspace(const void *workspace, size_t bytes, int64_t need) {
@@ -114,16 +115,18 @@ BackwardPlan plan_backward(int64_t rows, int64_t d, int dtype) {
   if (lay.lanes) {
     p.cols = (int64_t)lay.lanes * lay.nv * v;
     const int64_t blocks = (int64_t)sb_cu_count() * lay.blocks_per_cu();
-    // A single block, whose sums need no second launch, for what it can take in
-    // four turns: 8 and 16 rows of 2048 bf16 7.8 and 11.3 us in one kernel, 8.8
-    // and 8.9 in two, of which the second costs the host 4 us more; 32 rows
-    // 15 against 9.4.
+    // Where there are weights' gradients to sum, a single block, whose sums need
+    // no second launch, for what it can take in four turns: 8 and 16 rows of 2048
+    // bf16 7.8 and 11.3 us in one kernel, 8.8 and 8.9 in two, of which the second
+    // costs the host 4 us more; 32 rows 15 against 9.4.
     const int64_t turns = (rows + lay.rows() - 1) / lay.rows();
-    p.nparts = turns <= 4 ? 1 : std::min(turns, blocks);
+    p.blocks = std::min(turns, blocks);
+    p.nparts = turns <= 4 ? 1 : p.blocks;
   } else {
     const int64_t per = sb::kLNThreads * v;
     p.cols = (d + per - 1) / per * per;
     p.nparts = std::max<int64_t>(1, std::min<int64_t>(rows, 4 * sb_cu_count() / std::max<int64_t>(1, p.cols / per)));
+    p.blocks = p.nparts;
   }
   p.rowstat_bytes = split_bytes(rows, d, dtype, sb::kBackwardVectors);
   p.part_bytes = p.nparts * 2 * p.cols * (int64_t)sizeof(float);
@@ -216,7 +219,7 @@ extern "C" int layer_norm_backward(const void *dy, const int64_t dy_stride[2], c
   a.part = wanted ? (float *)workspace : nullptr;
   a.rowstat = (float *)((char *)workspace + p.part_bytes);
   a.chunks = a.rowstat + a.rows * 8;
-  a.nparts = a.rows > 0 ? (int32_t)p.nparts : 0;
+  a.nparts = a.rows > 0 ? (int32_t)(wanted ? p.nparts : p.blocks) : 0;
   a.cols = (int32_t)p.cols;
   const hipError_t e = sb_launch_layer_norm_backward(a, dtype, weight_dtype, (hipStream_t)stream);
   if (e != hipSuccess) return failf(SB_ELAUNCH, "layer norm launch failed: %s", hipGetErrorString(e));

@@ -34,7 +34,7 @@ struct LNArgs {
   // backward
   float *part;        // weight-gradient partials [blocks][2][columns] (nullptr: none wanted)
   void *dgamma, *dbeta;
-  int32_t nparts, cols; // blocks of partials; floats of each (the columns, rounded up to the block's)
+  int32_t nparts, cols; // blocks (of partials); floats of each (the columns, rounded up to the block's)
 };
 
 constexpr int kLNThreads = 256; // threads of a block of rows, of a chunk or of columns

@@ -116,12 +116,15 @@ BackwardPlan plan_backward(int64_t rows, int64_t d, int dtype) {
     p.cols = (int64_t)lay.lanes * lay.nv * v;
     const int64_t blocks = (int64_t)sb_cu_count() * lay.blocks_per_cu();
     // Where there are weights' gradients to sum, a single block, whose sums need
-    // no second launch, for what it can take in four turns: 8 and 16 rows of 2048
-    // bf16 7.8 and 11.3 us in one kernel, 8.8 and 8.9 in two, of which the second
-    // costs the host 4 us more; 32 rows 15 against 9.4.
+    // no second launch, for what it can take in four turns and 2048 vectors: that
+    // launch costs the host 3 to 4 us of a call of 11.  Kernels in us, one block
+    // and several with the second launch, bf16: 16 rows of 768 7.8 / 6.7, 8 and
+    // 16 of 2048 8.5 / 8.2 and 11.6 / 8.2, 8 of 4096 15 / 10.1, 2 of 8192 12.7 /
+    // 10.8; past the rule 3 of 8192 14.7 / 10.8, 2 and 4 of 16384 21.5 / 14.7 and
+    // 27.3 / 14.7, 32 of 2048 15 / 9.4.
     const int64_t turns = (rows + lay.rows() - 1) / lay.rows();
     p.blocks = std::min(turns, blocks);
-    p.nparts = turns <= 4 ? 1 : p.blocks;
+    p.nparts = turns == 1 || (turns <= 4 && turns * nv <= 2048) ? 1 : p.blocks;
   } else {
     const int64_t per = sb::kLNThreads * v;
     p.cols = (d + per - 1) / per * per;

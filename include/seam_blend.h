@@ -368,6 +368,65 @@ int grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *n
                    const int *out_dtypes, int64_t n, float max_norm, float eps, float *norm, void *workspace,
                    size_t workspace_bytes, void *stream);
 
+/*
+ * Attention of query heads over key and value heads:
+ *   S = scale q k^T, out = softmax(S) v, lse = log sum exp S,
+ * over the keys that a query sees.
+ *   shape        {B, Lq, Lk, query heads, key heads, D}: D in 1..256; query heads
+ *                h share key head h / (query heads / key heads); at most 2^12 query
+ *                heads; Lq and Lk times the query heads of a key head, and B times
+ *                the key heads, below 2^30.
+ *   q, out       device tensors [B, Lq, query heads, D];  k, v [B, Lk, key heads, D].
+ *   *_stride     {B, T, head} strides in elements, 0..2^40; D is contiguous.  Views of
+ *                a packed projection and caches of any layout need no copy.
+ *   scale        positive (1e-30..2e38).
+ *   query_lengths, key_lengths  device pointers to B 4-byte integers, or NULL: sample
+ *                b has that many (clamped to 0..Lq, 0..Lk).  What lies behind is
+ *                not read, may hold anything, and its rows of out are zeros
+ *                with lse -inf.
+ *   causal       != 0: query i sees keys up to i + (key length - query length): the
+ *                last query sees the last key.  (A NaN or infinity in a key or value
+ *                that causal order alone hides may reach rows near it.)
+ *   lse          device pointer to [B, query heads, Lq] floats, or NULL.
+ *   out          each element held once; shares none with q, k, v (checked; SB_EARG).
+ *   workspace    caller-owned device scratch of attention_forward_workspace_bytes()
+ *                bytes, 16-byte aligned; not looked at where that is 0.  Contents
+ *                need not be initialised.
+ * A query that sees no key has a row of zeros and lse -inf.  Scores, softmax
+ * statistics and sums are fp32; probabilities (times a power of two) are rounded to
+ * dtype for the product with v, and out once.  Any element alignment is taken;
+ * 16-byte aligned rows are fastest.  Deterministic.
+ */
+int attention_forward(const void *q, const int64_t q_stride[3], const void *k, const int64_t k_stride[3],
+                      const void *v, const int64_t v_stride[3], const int64_t shape[6], int dtype, float scale,
+                      int causal, const int32_t *query_lengths, const int32_t *key_lengths, void *out,
+                      const int64_t out_stride[3], float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace (bytes) attention_forward / attention_backward need on the
+ * current device; (size_t)-1 with an error message for invalid arguments. */
+size_t attention_forward_workspace_bytes(const int64_t shape[6], int dtype);
+size_t attention_backward_workspace_bytes(const int64_t shape[6], int dtype);
+
+/*
+ * Gradient of attention_forward.  The probabilities are formed again from q, k
+ * and lse, nothing else of the scores' size is kept or stored:
+ *   P = exp(S - lse), dS = P (dout v^T - rowsum(dout out)),
+ *   dq = scale dS k, dk = scale dS^T q, dv = P^T dout.
+ *   out, lse     the forward call's results (lse is needed);  dout like out.
+ *   dq, dk, dv   like q, k, v; written, not added to; every element held once; share
+ *                none with each other or an input (checked; SB_EARG).  Zeros where a
+ *                length, or causal order, leaves nothing.
+ * Other arguments as attention_forward's.  P and dS are rounded to dtype for the
+ * products they enter (in fp16 what is below 6e-8 vanishes: scale the loss).  The
+ * heads that share a key head are added up in fp32, in a fixed order: deterministic.
+ */
+int attention_backward(const void *dout, const int64_t dout_stride[3], const void *q, const int64_t q_stride[3],
+                       const void *k, const int64_t k_stride[3], const void *v, const int64_t v_stride[3],
+                       const void *out, const int64_t out_stride[3], const float *lse, const int64_t shape[6],
+                       int dtype, float scale, int causal, const int32_t *query_lengths, const int32_t *key_lengths,
+                       void *dq, const int64_t dq_stride[3], void *dk, const int64_t dk_stride[3], void *dv,
+                       const int64_t dv_stride[3], void *workspace, size_t workspace_bytes, void *stream);
+
 /* Thread-local message describing the last non-zero return on this thread. */
 const char *seamblend_last_error(void);
 

@@ -24,6 +24,7 @@ __all__ = ["vae_tile_layout", "LAYOUT_RULES", "vae_tile_ramp_blend", "RampBlend"
            "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_bytes", "LayerNorm",
            "LayerNormBackward", "rotary", "rotary_backward", "rotary_frequencies", "Rotary",
            "grad_norm", "grad_norm_clip", "GradNormClip",
+           "attention", "attention_backward", "attention_workspace_bytes", "Attention", "AttentionBackward",
            "SeamBlendError", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libseamblend.so")
@@ -408,3 +409,5 @@ from ._layer_norm import (LayerNorm, LayerNormBackward, layer_norm, layer_norm_b
                         layer_norm_backward_workspace_bytes)
 from ._rotary import Rotary, rotary, rotary_backward, rotary_frequencies  # noqa: E402
 from ._grad_clip import GradNormClip, grad_norm, grad_norm_clip  # noqa: E402
+from ._attention import (Attention, AttentionBackward, attention, attention_backward,  # noqa: E402
+                         attention_workspace_bytes)

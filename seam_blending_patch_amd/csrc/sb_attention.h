@@ -1,0 +1,58 @@
+// sb_attention.h -- launch arguments of the attention kernels, shared by the
+// host entry points and the gfx950 kernels.
+#pragma once
+
+#include "sb_internal.h"
+
+namespace sb {
+
+// A tensor of heads [B, T, heads, D]: strides in elements, D contiguous.
+struct AttnHeads {
+  const void *p;
+  int64_t b, t, h;
+};
+
+// The query heads that share a key head are one list of rows, row q * group + g
+// for query q and head g of the group: whatever the group, a tile of rows reads
+// a tile of keys once, rows follow the queries (causal order cuts off an end of
+// them), and the gradients of a shared key head add up inside one loop.
+struct AttnArgs {
+  AttnHeads q, k, v, out, dout, dq, dk, dv; // out and the gradients are written (out only forward)
+  float *lse;             // [B, heads of q, Lq] natural logarithms (nullptr: not wanted, forward)
+  float *delta;           // [B, heads of q, Lq] row sums of dout * out (backward)
+  float *part, *part_lse; // partial results of the splits, [splits][units][rows or keys][D] (part_lse: no D)
+  const int32_t *q_len, *k_len; // of each sample, or nullptr
+  int32_t B, Lq, Lk, Hk, group, D;
+  int32_t rows;           // Lq * group
+  int32_t causal;
+  int32_t tiles, splits;  // of a unit (sample and key head)
+  int32_t span;           // keys (rows, for key gradients) of a split, whole tiles
+  FastDiv div_group, div_tiles, div_splits, div_Hk;
+  uint32_t unit0;         // first unit of this launch
+  uint32_t blocks;
+  float scale, scale2;    // of the scores, and that times log2(e)
+};
+
+constexpr int kAttnWaves = 4;     // waves of a block where there are rows for them
+constexpr int64_t kAttnWidth = 256; // longest head
+
+inline int attn_padded(int64_t d) { // head lengths that kernels are built for
+  return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : d <= 128 ? 128 : d <= 160 ? 160 : d <= 192 ? 192 : 256;
+}
+
+// keys of a block of the key gradients: 32 a wave, or a pair of waves where a
+// head's two halves go to two of them
+__host__ __device__ constexpr bool attn_paired(int elem_bytes, int padded) { return padded * elem_bytes > (elem_bytes == 2 ? 384 : 640); }
+
+} // namespace sb
+
+// waves: 1 or kAttnWaves, each with 32 rows of a tile (32 keys, for key gradients)
+hipError_t sb_launch_attention(const sb::AttnArgs &a, int dtype, int waves, hipStream_t st);
+hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, hipStream_t st);
+hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, hipStream_t st);
+// joins the splits of the forward pass, or adds up those of a gradient: `count`
+// rows of D of the partial results at a.part, to out (a.out's layout with
+// `heads` of a group)
+hipError_t sb_launch_attention_join(const sb::AttnArgs &a, int dtype, hipStream_t st);
+hipError_t sb_launch_attention_sum(const sb::AttnArgs &a, const sb::AttnHeads &out, const float *part, int64_t len,
+                                   int group, int dtype, hipStream_t st);

@@ -427,6 +427,81 @@ int attention_backward(const void *dout, const int64_t dout_stride[3], const voi
                        void *dq, const int64_t dq_stride[3], void *dk, const int64_t dk_stride[3], void *dv,
                        const int64_t dv_stride[3], void *workspace, size_t workspace_bytes, void *stream);
 
+/* what follows a group norm */
+#define SB_ACT_NONE 0
+#define SB_ACT_SILU 1 /* z / (1 + exp(-z)) */
+
+/* Device workspace (bytes) group_norm_forward and group_norm_backward need on
+ * the current device; (size_t)-1 with an error message for invalid arguments. */
+size_t group_norm_workspace_bytes(const int64_t shape[3], int64_t groups, int dtype);
+
+/*
+ * Group norm of channels-last activations, with the activation behind it: over
+ * the positions and channels of each group of each sample
+ *   m = mean x, v = mean (x - m)^2, r = 1 / sqrt(v + eps), h = (x - m) r,
+ *   out = act(h gamma_c + beta_c).
+ *   shape        {N, S, C}: samples (N * groups < 2^24), positions of a sample (all
+ *                spatial axes, < 2^31), channels (up to 2^16, a multiple of groups).
+ *   *_stride     {sample, position} strides in elements, 0..2^40; the C channels of a
+ *                position are contiguous.  These are also the tokens of attention.
+ *   gamma, beta  device pointers to [C] of weight_dtype, or NULL (1 and 0).
+ *   dtype        of x and out; weight_dtype: dtype, or SB_F32.
+ *   out          each element held once; x itself (same pointer and strides), or
+ *                sharing no element with it (checked; SB_EARG).
+ *   stats        device pointer to [N][groups][3] floats, or NULL: receives m as the
+ *                unevaluated sum of its first two, and r, for the gradient.
+ *   workspace    caller-owned device scratch, 16-byte aligned, contents need not be
+ *                initialised.
+ * Any element alignment is taken; 16-byte aligned positions are fastest.
+ * Statistics are fp32 about each group's first value and merged by Chan's formula
+ * (the merge over blocks in 64 bits), so a mean that is large against the spread
+ * costs no accuracy; one rounding to dtype.  Deterministic.  No positions: no-op.
+ */
+int group_norm_forward(const void *x, const int64_t x_stride[2], const int64_t shape[3], int64_t groups, float eps,
+                       const void *gamma, const void *beta, int activation, int dtype, int weight_dtype, void *out,
+                       const int64_t out_stride[2], float *stats, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * Gradient of group_norm_forward: with z = h gamma + beta, g = dy act'(z) and
+ * a = gamma g,
+ *   dx = r (a - mean(a) - h mean(a h))  (means over a group's positions and channels),
+ *   dgamma = sum g h, dbeta = sum g     (over samples and positions).
+ *   stats        what the forward call wrote; gamma, beta as there.
+ *   dx           may be dy or x themselves, else shares no element with them.
+ *   dgamma, dbeta  device pointers to [C] of weight_dtype, or NULL where not wanted;
+ *                written, not added to (zeros without positions).
+ * Sums are fp32 by block and 64-bit over blocks, in a fixed order.
+ */
+int group_norm_backward(const void *dy, const int64_t dy_stride[2], const void *x, const int64_t x_stride[2],
+                        const int64_t shape[3], int64_t groups, const float *stats, const void *gamma,
+                        const void *beta, int activation, int dtype, int weight_dtype, void *dx,
+                        const int64_t dx_stride[2], void *dgamma, void *dbeta, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * Dropout from a counter-based generator; the mask is never stored:
+ *   out = [residual +] (word(i) < floor(p 2^32) ? 0 : x / (1 - p)),
+ * for element i of x in row-major order, word(i) = word i % 4 of Philox4x32 with
+ * ten rounds at counter {i / 4, site, offset's low, high half}, key {seed's low,
+ * high half}.  The same call on a gradient, without residual, is its backward pass.
+ *   shape        {outer, inner, D}: outer * inner rows (< 2^31) of D contiguous
+ *                elements, at most 2^34 in all.
+ *   *_stride     {outer, inner} strides in elements, 0..2^40.
+ *   p            in [0, 1): the share that is dropped.
+ *   state        device pointer to two 8-byte integers, seed and offset, read when
+ *                the kernel runs: a captured graph that adds to the offset draws
+ *                another mask on every replay.
+ *   site         tells the dropouts of one step apart.
+ *   residual     device pointer like x, or NULL.
+ *   out          each element held once; x or residual itself (same pointer and
+ *                strides), or sharing no element with them (checked; SB_EARG).
+ * fp32 arithmetic, one rounding to dtype.  No elements: no-op.
+ */
+int dropout_apply(const void *x, const int64_t x_stride[2], const int64_t shape[3], int dtype, double p,
+                  const int64_t *state, uint32_t site, const void *residual, const int64_t residual_stride[2],
+                  void *out, const int64_t out_stride[2], void *stream);
+
 /* Thread-local message describing the last non-zero return on this thread. */
 const char *seamblend_last_error(void);
 

@@ -25,6 +25,8 @@ __all__ = ["vae_tile_layout", "LAYOUT_RULES", "vae_tile_ramp_blend", "RampBlend"
            "LayerNormBackward", "rotary", "rotary_backward", "rotary_frequencies", "Rotary",
            "grad_norm", "grad_norm_clip", "GradNormClip",
            "attention", "attention_backward", "attention_workspace_bytes", "Attention", "AttentionBackward",
+           "group_norm", "group_norm_backward", "group_norm_workspace_bytes", "GroupNorm", "GroupNormBackward",
+           "dropout", "dropout_backward", "Dropout",
            "SeamBlendError", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libseamblend.so")
@@ -411,3 +413,6 @@ from ._rotary import Rotary, rotary, rotary_backward, rotary_frequencies  # noqa
 from ._grad_clip import GradNormClip, grad_norm, grad_norm_clip  # noqa: E402
 from ._attention import (Attention, AttentionBackward, attention, attention_backward,  # noqa: E402
                          attention_workspace_bytes)
+from ._group_norm import (GroupNorm, GroupNormBackward, group_norm, group_norm_backward,  # noqa: E402
+                          group_norm_workspace_bytes)
+from ._dropout import Dropout, dropout, dropout_backward  # noqa: E402

@@ -20,7 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libseamblend.so")
 SOURCES = ["abi.cpp", "layout.cpp", "ramp.cpp", "blend_stitch.hip", "groupnorm.hip", "ramp_blend.hip",
            "layer_norm.cpp", "layer_norm.hip", "rotary.cpp", "rotary.hip", "grad_clip.cpp", "grad_clip.hip",
-           "attention.cpp", "attention.hip", "attention_backward.hip"]
+           "attention.cpp", "attention.hip", "attention_backward.hip", "channels_norm.cpp", "channels_norm.hip",
+           "dropout.cpp", "dropout.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=off",

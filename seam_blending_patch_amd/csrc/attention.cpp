@@ -111,12 +111,14 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // the other side in splits where that alone does not fill the chip.
 struct Plan {
   int waves;
+  int wave_rows; // of dq's pipelined kernel (0: not that one)
   int64_t tiles, splits, span;
 };
 
 Plan cut(int64_t units, int64_t own, int64_t per_block, int64_t along, int waves, int64_t want, int64_t least) {
   Plan p;
   p.waves = waves;
+  p.wave_rows = 0;
   p.tiles = (own + per_block - 1) / per_block;
   const int64_t blocks = std::max<int64_t>(1, units * p.tiles);
   const int64_t most = std::min<int64_t>(kMaxSplits, (along + least - 1) / least);
@@ -126,16 +128,34 @@ Plan cut(int64_t units, int64_t own, int64_t per_block, int64_t along, int waves
   return p;
 }
 
-Plan plan_rows(const sb::AttnArgs &a, int) {
+bool whole_chunks(const sb::AttnArgs &a, int dtype) { return a.D % (16 / sb::elem_bytes(dtype)) == 0; }
+
+Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward) {
   const int64_t cus = sb_cu_count(), units = (int64_t)a.B * a.Hk;
+  const int eb = sb::elem_bytes(dtype), padded = sb::attn_padded(a.D), wide = 2 * sb::kAttnWaves;
+  const bool whole = whole_chunks(a, dtype);
   if (a.rows <= 32) return cut(units, a.rows, 32, a.Lk, 1, 8 * cus, 128);
-  return cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, 2 * cus, 256);
+  if (forward && whole && sb::attn_wide(eb, padded) && units * ((a.rows + 32 * wide - 1) / (32 * wide)) >= 2 * cus)
+    return cut(units, a.rows, 32 * wide, a.Lk, wide, 1, a.Lk + 1);
+  Plan p;
+  if (!forward && whole && sb::attn_pipelined(eb, padded)) {
+    const int64_t rows = 64 * sb::kAttnWaves;
+    if (sb::attn_columns(padded) > 1 && units * ((a.rows + rows - 1) / rows) >= cus) {
+      p = cut(units, a.rows, rows, a.Lk, sb::kAttnWaves, 1, a.Lk + 1);
+      p.wave_rows = 64;
+      return p;
+    }
+    p = cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, cus, 512);
+    p.wave_rows = 32;
+    return p;
+  }
+  return cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, cus, 512);
 }
 
 Plan plan_keys(const sb::AttnArgs &a, int dtype) {
   const int64_t cus = sb_cu_count(), units = (int64_t)a.B * a.Hk;
   const bool paired = sb::attn_paired(sb::elem_bytes(dtype), sb::attn_padded(a.D));
-  return cut(units, a.Lk, 32 * sb::kAttnWaves / (paired ? 2 : 1), a.rows, sb::kAttnWaves, 2 * cus, 256);
+  return cut(units, a.Lk, 32 * sb::kAttnWaves / (paired ? 2 : 1), a.rows, sb::kAttnWaves, cus, 512);
 }
 
 int64_t rows_part(const sb::AttnArgs &a, const Plan &p) { // floats of the splits' rows
@@ -150,11 +170,11 @@ int64_t keys_part(const sb::AttnArgs &a, const Plan &p) {
 int64_t delta_floats(const sb::AttnArgs &a) { return up((int64_t)a.B * a.Hk * a.rows, 4); }
 
 int64_t forward_floats(const sb::AttnArgs &a, int dtype) {
-  const Plan p = plan_rows(a, dtype);
+  const Plan p = plan_rows(a, dtype, true);
   return rows_part(a, p) + rows_part_lse(a, p);
 }
 int64_t backward_floats(const sb::AttnArgs &a, int dtype) {
-  return delta_floats(a) + std::max(rows_part(a, plan_rows(a, dtype)), keys_part(a, plan_keys(a, dtype)));
+  return delta_floats(a) + std::max(rows_part(a, plan_rows(a, dtype, false)), keys_part(a, plan_keys(a, dtype)));
 }
 
 int check_workspace(const void *workspace, size_t bytes, int64_t need) {
@@ -170,12 +190,13 @@ template <class F> hipError_t over_units(sb::AttnArgs a, const Plan &p, F launch
   a.tiles = (int32_t)p.tiles;
   a.splits = (int32_t)p.splits;
   a.span = (int32_t)p.span;
-  a.div_tiles = sb::make_fastdiv((uint32_t)p.tiles);
+  a.div_set = sb::make_fastdiv((uint32_t)(8 * p.tiles * p.splits));
   a.div_splits = sb::make_fastdiv((uint32_t)p.splits);
   const int64_t units = (int64_t)a.B * a.Hk, each = p.tiles * p.splits, most = std::max<int64_t>(1, sb::kMaxBlocksX / each);
   for (int64_t u = 0; u < units; u += most) {
     a.unit0 = (uint32_t)u;
-    a.blocks = (uint32_t)(std::min(most, units - u) * each);
+    a.units = (uint32_t)std::min(most, units - u);
+    a.blocks = (uint32_t)(a.units * each);
     const hipError_t e = launch(a);
     if (e != hipSuccess) return e;
   }
@@ -223,7 +244,7 @@ extern "C" int attention_forward(const void *q, const int64_t q_stride[3], const
   if ((rc = check_workspace(workspace, workspace_bytes, forward_floats(a, dtype) * (int64_t)sizeof(float)))) return rc;
   a.causal = causal != 0;
   a.lse = lse;
-  const Plan p = plan_rows(a, dtype);
+  const Plan p = plan_rows(a, dtype, true);
   const hipStream_t st = (hipStream_t)stream;
   if (p.splits > 1) {
     a.part = (float *)workspace;
@@ -278,22 +299,19 @@ extern "C" int attention_backward(const void *dout, const int64_t dout_stride[3]
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (a.Lq > 0) {
-    const Plan p = plan_rows(a, dtype);
+    const Plan p = plan_rows(a, dtype, false);
     a.part = p.splits > 1 ? part : nullptr;
-    e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, st); });
+    e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, p.wave_rows, st); });
     a.splits = (int32_t)p.splits;
-    if (e == hipSuccess && p.splits > 1) e = sb_launch_attention_sum(a, a.dq, part, a.rows, a.group, dtype, st);
+    if (e == hipSuccess && p.splits > 1) e = sb_launch_attention_sum(a, &a.dq, 1, a.rows, a.group, dtype, st);
   }
   if (e == hipSuccess && a.Lk > 0) {
     const Plan p = plan_keys(a, dtype);
     a.part = p.splits > 1 ? part : nullptr;
-    e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dkv(b, dtype, st); });
+    e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dkv(b, dtype, whole_chunks(a, dtype), st); });
     a.splits = (int32_t)p.splits;
-    if (p.splits > 1) {
-      if (e == hipSuccess) e = sb_launch_attention_sum(a, a.dk, part, a.Lk, 1, dtype, st);
-      if (e == hipSuccess)
-        e = sb_launch_attention_sum(a, a.dv, part + p.splits * a.B * a.Hk * (int64_t)a.Lk * a.D, a.Lk, 1, dtype, st);
-    }
+    const sb::AttnHeads to_[2] = {a.dk, a.dv};
+    if (e == hipSuccess && p.splits > 1) e = sb_launch_attention_sum(a, to_, 2, a.Lk, 1, dtype, st);
   }
   return launched(e);
 }

@@ -5,162 +5,335 @@
 namespace sb {
 namespace {
 
-// Forward.  A wave has 32 rows (query, head of the group), a lane one of them:
-// S^T = K Q^T puts a row's scores into one lane and its partner in the other
-// half, so a row's maximum and sum need one exchange, a row's factors are
-// scalars of a lane, and P^T feeds O^T += V^T P^T as it lies.
-template <int DT, int DP, int NW>
-__global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs a) {
-  constexpr int kThreads = 64 * NW;
-  constexpr int KT = NW > 1 && Tile<DT, DP, 32>::SC <= 16 ? 64 : 32, NS = KT / 32; // keys of a tile
-  using T = Tile<DT, DP, KT>;
-  using St = Stage<DT, DP, KT, kThreads>;
-  constexpr bool kAhead = St::N <= 8;     // the next tile is requested while this one is used
-  constexpr int kBufs = kAhead ? 2 : 1, NB = DP / 32, PW = DT == DT_F32 ? 16 : 8;
-  __shared__ alignas(16) char lds[kBufs][2][T::kBytes];
+// Waves of a SIMD that the registers are shared out for: two that take turns at
+// the matrix cores and at the softmax are worth more than any register (128 wide,
+// 20280 rows and keys of 12 heads bf16: 5.94 ms for one, 2.96 for two); longer
+// heads would spill.
+constexpr int forward_waves(int dt, int dp, int nw) {
+  if (dt == DT_F32) return dp <= 32 ? 3 : dp <= 96 || (dp == 128 && nw > 1) ? 2 : 1;
+  return dp <= 64 ? 3 : dp <= 160 || (dp == 192 && nw > 1) ? 2 : 1;
+}
 
-  const Work w = work_of(a);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, n = lane & 31;
-  const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
-  const int off = klen - qlen, live_rows = qlen * a.group;
-  const int r0 = w.tile * 32 * NW, wr0 = r0 + wave * 32, row = wr0 + n;
-  const bool live = row < live_rows;
-  // keys that a row sees: the first seen(row)
-  const auto seen = [&](int r) {
+// What a block of NW waves has to do, and a wave and a lane of it: a wave has 32
+// rows (query, head of the group), a lane one of them.
+template <int NW> struct Rows {
+  Work w;
+  int lane, h, row;        // row: of the unit, this lane's
+  int klen, off, live_rows;
+  int sees, sure;          // keys that the row sees: the first `sees`; that all rows of the wave see
+  int begin, end, wend;    // keys of the block; the end of the wave's
+  bool live;
+  __device__ __forceinline__ int seen(const AttnArgs &a, int r) const {
     return a.causal ? min(max((int)fdiv((uint32_t)r, a.div_group) + off + 1, 0), klen) : klen;
-  };
-  const int sees = live ? seen(row) : klen;          // (rows past the end compute something that is not kept)
-  const int sure = seen(min(wr0, max(live_rows - 1, 0))); // keys that all rows of the wave see
-  const int last = min(r0 + 32 * NW, live_rows) - 1, wlast = min(wr0 + 32, live_rows) - 1;
-  const int begin = w.split * a.span;
-  const int end = last < r0 ? 0 : min(seen(last), begin + a.span);
-  const int wend = wlast < wr0 ? 0 : min(seen(wlast), end);
+  }
+  __device__ __forceinline__ Rows(const AttnArgs &a) : w(work_of<true>(a)) {
+    lane = threadIdx.x & 63;
+    h = lane >> 5;
+    klen = length_of(a.k_len, w.b, a.Lk);
+    const int qlen = length_of(a.q_len, w.b, a.Lq), r0 = w.tile * 32 * NW, wr0 = r0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32;
+    off = klen - qlen;
+    live_rows = qlen * a.group;
+    row = wr0 + (lane & 31);
+    live = row < live_rows;
+    sees = live ? seen(a, row) : klen; // (rows past the end compute something that is not kept)
+    sure = seen(a, min(wr0, max(live_rows - 1, 0)));
+    const int last = min(r0 + 32 * NW, live_rows) - 1, wlast = min(wr0 + 32, live_rows) - 1;
+    begin = w.split * a.span;
+    end = last < r0 ? 0 : min(seen(a, last), begin + a.span);
+    wend = wlast < wr0 ? 0 : min(seen(a, wlast), end);
+  }
+};
 
+// A wave's rows on their way: S^T = K Q^T puts a row's scores into one lane and
+// its partner in the other half, so a row's maximum and sum need one exchange, a
+// row's factors are scalars of a lane, and P^T feeds O^T += V^T P^T as it lies.
+template <int DT, int DP, int KT> struct Softmax {
+  using T = Tile<DT, DP, KT>;
+  static constexpr int NS = KT / 32, NB = DP / 32, PW = DT == DT_F32 ? 16 : 8;
   u32x4 qf[T::kFrags];
-  {
-    const int64_t at = live ? row_at(a.q, a, w.b, w.hk, row) : 0;
-#pragma unroll
-    for (int u = 0; u < T::kFrags; ++u) qf[u] = load_chunk<DT>(a.q.p, at, 2 * u + h, a.D, live);
-  }
   f32x16 o[NB];
-#pragma unroll
-  for (int db = 0; db < NB; ++db) o[db] = f32x16{0};
-  float m = -kInf, l = 0.0f; // m: of the scores before scaling; l: of this lane's half of the keys
-  const float slack = 8.0f / a.scale2;
+  float m, l; // m: of the scores before scaling; l: of this lane's half of the keys
+  float s[NS][16];
+  uint32_t p[NS][PW];
 
-  const int64_t k_base = w.b * a.k.b + w.hk * a.k.h, v_base = w.b * a.v.b + w.hk * a.v.h;
-  const auto k_at = [&](int r) { return k_base + r * a.k.t; };
-  const auto v_at = [&](int r) { return v_base + r * a.v.t; };
-  St sk, sv;
-  if (kAhead && begin < end) {
-    sk.load(a.k.p, begin, klen, a.D, k_at);
-    sv.load(a.v.p, begin, klen, a.D, v_at);
-    sk.store(lds[0][0]);
-    sv.store(lds[0][1]);
-    __syncthreads();
+  template <int NW> __device__ __forceinline__ void start(const AttnArgs &a, const Rows<NW> &r) {
+    const int64_t at = r.live ? row_at(a.q, a, r.w.b, r.w.hk, r.row) : 0;
+#pragma unroll
+    for (int u = 0; u < T::kFrags; ++u) qf[u] = load_chunk<DT>(a.q.p, at, 2 * u + r.h, a.D, r.live);
+#pragma unroll
+    for (int db = 0; db < NB; ++db) o[db] = f32x16{0};
+    m = -kInf;
+    l = 0.0f;
   }
-  for (int k0 = begin, cur = 0; k0 < end; k0 += KT) {
-    if constexpr (kAhead) {
-      if (k0 + KT < end) {
-        sk.load(a.k.p, k0 + KT, klen, a.D, k_at);
-        sv.load(a.v.p, k0 + KT, klen, a.D, v_at);
-      }
-    } else {
-      __syncthreads();
-      sk.load(a.k.p, k0, klen, a.D, k_at);
-      sk.store(lds[0][0]);
-      sv.load(a.v.p, k0, klen, a.D, v_at);
-      sv.store(lds[0][1]);
-      __syncthreads();
-    }
-    const char *kt = lds[cur][0], *vt = lds[cur][1];
-    if (k0 < wend) {
-      float s[NS][16];
+  // Steps of the products: first those of P with the values (kMix of them), then
+  // those of the keys with Q.
+  static constexpr int kMix = DT == DT_F32 ? 0 : 2 * NS * NB, kScores = NS * T::kFrags, kAhead = 6;
+  __device__ __forceinline__ u32x4 score_read(const char *lds, int kt, int i) const {
+    return T::row_fragment(lds, kt, 32 * (i % NS), i / NS);
+  }
+  __device__ __forceinline__ void score_use(f32x16 (&c)[NS], int i, u32x4 f) const {
+    c[i % NS] = mma<DT>(f, qf[i / NS], c[i % NS]);
+  }
+  __device__ __forceinline__ u32x4 mix_read(const char *lds, int vt, int i) const {
+    return T::column_fragment(lds, vt, 32 * (i / NB / 2), i % NB, i / NB % 2);
+  }
+  __device__ __forceinline__ void mix_use(int i, u32x4 f) {
+    const uint32_t *q = p[i / NB / 2] + 4 * (i / NB % 2);
+    o[i % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, o[i % NB]);
+  }
+  __device__ __forceinline__ void scores(const char *lds, int kt) {
+    f32x16 c[NS];
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        f32x16 c = {0};
-#pragma unroll
-        for (int u = 0; u < T::kFrags; ++u) c = mma<DT>(T::row_fragment(kt, 32 * j + n, u, h), qf[u], c);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[j][i] = c[i];
-      }
-      if (k0 + KT > sure) {
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[j][i] = k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) < sees ? s[j][i] : -kInf;
-      }
-      float mx = s[0][0];
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
-      mx = half_max(mx);
-      // The running maximum only has to keep exp2 in range: it moves when some
-      // row's has grown by 2^8 or more (P is then at most 2^8, which 16 bits
-      // hold as exactly as 1), which spares most tiles the turn over O.
-      if (__any(mx > m + slack)) {
-        const float up = fmaxf(m, mx), by = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f((m - up) * a.scale2);
-        m = up;
-        l *= by;
-#pragma unroll
-        for (int db = 0; db < NB; ++db) o[db] = o[db] * by;
-      }
-      const float base = m == -kInf ? 0.0f : -m * a.scale2;
-      uint32_t p[NS][PW];
-#pragma unroll
-      for (int j = 0; j < NS; ++j) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], a.scale2, base));
-          l += s[j][i];
-        }
-        pack_operand<DT>(s[j], p[j]);
-      }
+    for (int j = 0; j < NS; ++j) c[j] = f32x16{0};
+    in_order<kScores, kAhead>([&](int i) { return score_read(lds, kt, i); },
+                              [&](int i, u32x4 f) { score_use(c, i, f); });
+    keep(c);
+  }
+  __device__ __forceinline__ void mix(const char *lds, int vt) {
+    if constexpr (DT == DT_F32) {
 #pragma unroll
       for (int db = 0; db < NB; ++db)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) o[db] = T::column_product(vt, 32 * j, db, p[j], o[db], lane);
+        for (int j = 0; j < NS; ++j) o[db] = T::column_product(lds, vt, 32 * j, db, p[j], o[db]);
+    } else {
+      in_order<kMix, kAhead>([&](int i) { return mix_read(lds, vt, i); }, [&](int i, u32x4 f) { mix_use(i, f); });
+    }
+  }
+  // the values of one tile and the scores of the next, without a break
+  __device__ __forceinline__ void mix_then_scores(const char *lds, int vt, int kt) {
+    f32x16 c[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) c[j] = f32x16{0};
+    in_order<kMix + kScores, kAhead>(
+        [&](int i) { return i < kMix ? mix_read(lds, vt, i) : score_read(lds, kt, i - kMix); },
+        [&](int i, u32x4 f) {
+          if (i < kMix) mix_use(i, f);
+          else score_use(c, i - kMix, f);
+        });
+    keep(c);
+  }
+  __device__ __forceinline__ void keep(const f32x16 (&c)[NS]) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[j][i] = c[j][i];
+  }
+  // left: how many of the tile's keys the row sees, less 4 h
+  __device__ __forceinline__ void hide(int left) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[j][i] = 32 * j + 8 * (i >> 2) + (i & 3) < left ? s[j][i] : -kInf;
+  }
+  __device__ __forceinline__ void soften(float scale2, float slack) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
+    mx = half_max(mx);
+    // The running maximum only has to keep exp2 in range: it moves when some row's
+    // has grown by 2^8 or more (P is then at most 2^8, which 16 bits hold as exactly
+    // as 1), which spares most tiles the turn over O.
+    if (__any(mx > m + slack)) {
+      const float up = fmaxf(m, mx), by = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f((m - up) * scale2);
+      m = up;
+      l *= by;
+#pragma unroll
+      for (int db = 0; db < NB; ++db) o[db] = o[db] * by;
+    }
+    const float base = m == -kInf ? 0.0f : -m * scale2;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], scale2, base));
+        l += s[j][i];
+      }
+      pack_operand<DT>(s[j], p[j]);
+    }
+  }
+  template <int NW> __device__ __forceinline__ void finish(const AttnArgs &a, const Rows<NW> &r) {
+    if (r.row >= a.rows) return;
+    l = half_sum(l);
+    const bool some = r.live && !(l == 0.0f); // (a NaN goes on)
+    const float by = some ? 1.0f / l : 0.0f;
+    const float lse = some ? m * a.scale + logf(l) : -kInf;
+    if (a.part_lse) {
+      const int64_t at = ((int64_t)r.w.split * a.B * a.Hk + r.w.unit) * a.rows + r.row;
+      if (r.h == 0) a.part_lse[at] = lse;
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+        store_column<DT_F32>(a.part, at * a.D, db, r.h, a.D, some ? o[db] : f32x16{0}, by);
+    } else {
+      if (a.lse && r.h == 0) a.lse[stat_at(a, r.w.b, r.w.hk, r.row)] = lse;
+      const int64_t at = row_at(a.out, a, r.w.b, r.w.hk, r.row);
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+        store_column<DT>((void *)a.out.p, at, db, r.h, a.D, some ? o[db] : f32x16{0}, by);
+    }
+  }
+};
+
+template <int DT, int DP, int NW>
+__global__ __launch_bounds__(64 * NW, forward_waves(DT, DP, NW)) void attention_kernel(const AttnArgs a) {
+  constexpr int kThreads = 64 * NW;
+  constexpr int KT = NW > 1 && Tile<DT, DP, 32>::SC <= 16 ? 64 : 32; // keys of a tile
+  using T = Tile<DT, DP, KT>;
+  using St = Stage<DT, DP, KT, kThreads>;
+  constexpr bool kAhead = St::N <= 8; // the next tile is requested while this one is used
+  constexpr int kBufs = kAhead ? 2 : 1;
+  __shared__ alignas(1024) char lds[kBufs * 2 * T::kBytes]; // of each buffer keys, then values
+
+  const Rows<NW> r(a);
+  Softmax<DT, DP, KT> x;
+  x.start(a, r);
+  const float slack = 8.0f / a.scale2;
+  const int64_t k_base = r.w.b * a.k.b + r.w.hk * a.k.h, v_base = r.w.b * a.v.b + r.w.hk * a.v.h;
+  const auto k_at = [&](int k) { return k_base + k * a.k.t; };
+  const auto v_at = [&](int k) { return v_base + k * a.v.t; };
+  const int row_lane = T::row_place(r.lane), col_lane = T::column_place(r.lane);
+  St sk, sv;
+  if (kAhead && r.begin < r.end) {
+    sk.load(a.k.p, r.begin, r.klen, a.D, k_at);
+    sv.load(a.v.p, r.begin, r.klen, a.D, v_at);
+    sk.store(lds);
+    sv.store(lds + T::kBytes);
+    __syncthreads();
+  }
+  for (int k0 = r.begin, cur = 0; k0 < r.end; k0 += KT) {
+    if constexpr (kAhead) {
+      if (k0 + KT < r.end) {
+        sk.load(a.k.p, k0 + KT, r.klen, a.D, k_at);
+        sv.load(a.v.p, k0 + KT, r.klen, a.D, v_at);
+      }
+    } else {
+      __syncthreads();
+      stage_tile<DT, DP, KT, kThreads>(lds, a.k.p, k0, r.klen, a.D, k_at);
+      stage_tile<DT, DP, KT, kThreads>(lds + T::kBytes, a.v.p, k0, r.klen, a.D, v_at);
+      __syncthreads();
+    }
+    if (k0 < r.wend) {
+      // (the wave that has products goes first, the other has a softmax to do meanwhile)
+      __builtin_amdgcn_s_setprio(1);
+      x.scores(lds, row_lane + cur);
+      __builtin_amdgcn_s_setprio(0);
+      if (k0 + KT > r.sure) x.hide(r.sees - k0 - 4 * r.h);
+      x.soften(a.scale2, slack);
+      __builtin_amdgcn_s_setprio(1);
+      x.mix(lds, col_lane + cur + T::kBytes);
+      __builtin_amdgcn_s_setprio(0);
     }
     if constexpr (kAhead) {
-      cur ^= 1;
-      if (k0 + KT < end) {
-        sk.store(lds[cur][0]);
-        sv.store(lds[cur][1]);
+      cur ^= 2 * T::kBytes;
+      if (k0 + KT < r.end) {
+        sk.store(lds + cur);
+        sv.store(lds + cur + T::kBytes);
       }
       __syncthreads();
     }
   }
-
-  if (row >= a.rows) return;
-  l = half_sum(l);
-  const bool some = live && !(l == 0.0f); // (a NaN goes on)
-  const float by = some ? 1.0f / l : 0.0f;
-  const float lse = some ? m * a.scale + logf(l) : -kInf;
-  if (a.part_lse) {
-    const int64_t at = ((int64_t)w.split * a.B * a.Hk + w.unit) * a.rows + row;
-    if (h == 0) a.part_lse[at] = lse;
-#pragma unroll
-    for (int db = 0; db < NB; ++db)
-      store_column<DT_F32>(a.part, at * a.D, db, h, a.D, some ? o[db] : f32x16{0}, by);
-  } else {
-    if (a.lse && h == 0) a.lse[stat_at(a, w.b, w.hk, row)] = lse;
-    const int64_t at = row_at(a.out, a, w.b, w.hk, row);
-#pragma unroll
-    for (int db = 0; db < NB; ++db)
-      store_column<DT>((void *)a.out.p, at, db, h, a.D, some ? o[db] : f32x16{0}, by);
-  }
+  x.finish(a, r);
 }
 
-// A wave joins the splits of a row: out = sum_s exp(lse_s - lse) out_s.  At most
-// 64 splits: a lane has the weight of one.
-constexpr int kJoinRows = 4; // rows of a block
-template <int DT> __global__ __launch_bounds__(64 * kJoinRows) void join_kernel(const AttnArgs a, int64_t count) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * kJoinRows + (threadIdx.x >> 6);
-  if (at >= count) return;
-  const float lse = lane < a.splits ? a.part_lse[lane * count + at] : -kInf;
+// A barrier for LDS alone: what is on its way from memory stays on its way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Many rows: blocks of 8 waves in two sets, one wave of each to a SIMD, half a
+// turn apart: while one set has its products (of the last tile's values, of the
+// next tile's keys) the other has its softmax, so the matrix cores and the vector
+// unit are at work together instead of in turn.  Phases are kept apart by
+// barriers; in phase 2 t (the second set: 2 t + 1) a wave multiplies tile t's keys,
+// in the next it softens them, in the one after that it multiplies its values.
+// Keys t + 2 and values t + 1 are stored while tile t is softened, in one of three
+// buffers: its last reader was done two phases before, its first comes two after.
+template <int DT, int DP>
+__global__ __launch_bounds__(128 * kAttnWaves) void attention_wide_kernel(const AttnArgs a) {
+  constexpr int NW = 2 * kAttnWaves, kThreads = 64 * NW;
+  constexpr int KT = Tile<DT, DP, 32>::SC <= 16 ? 64 : 32; // keys of a tile
+  using T = Tile<DT, DP, KT>;
+  using St = RowStage<DT, DP, KT, kThreads>;
+  __shared__ alignas(1024) char lds[3 * 2 * T::kBytes]; // of each buffer keys, then values
+
+  const Rows<NW> r(a);
+  Softmax<DT, DP, KT> x;
+  x.start(a, r);
+  const float slack = 8.0f / a.scale2;
+  const int64_t k_base = r.w.b * a.k.b + r.w.hk * a.k.h, v_base = r.w.b * a.v.b + r.w.hk * a.v.h;
+  const int row_lane = T::row_place(r.lane), col_lane = T::column_place(r.lane);
+  const int tiles = r.end > r.begin ? (r.end - r.begin + KT - 1) / KT : 0;
+  if (tiles) {
+    clear_tiles<kThreads>(lds, sizeof lds, a.D < DP);
+    St sk, sv;
+    sk.start(a.k.p, k_base, a.k.t, r.begin, a.D);
+    sv.start(a.v.p, v_base, a.v.t, r.begin, a.D);
+    sk.load(r.begin, r.klen);
+    sv.load(r.begin, r.klen);
+    sk.store(lds);
+    sv.store(lds + T::kBytes);
+    if (tiles > 1) {
+      sk.load(r.begin + KT, r.klen);
+      sv.load(r.begin + KT, r.klen);
+      sk.store(lds + 2 * T::kBytes);
+    }
+    if (tiles > 2) sk.load(r.begin + 2 * KT, r.klen);
+    __syncthreads();
+    const bool second = __builtin_amdgcn_readfirstlane(threadIdx.x) >= kThreads / 2;
+    if (second) lds_barrier();
+    if (r.begin < r.wend) x.scores(lds, row_lane);
+    // byte offsets of the buffers of tiles t, t + 1 and t + 2
+    int b0 = 0, b1 = 2 * T::kBytes, b2 = 4 * T::kBytes;
+    for (int t = 0, k0 = r.begin; t < tiles; ++t, k0 += KT) {
+      lds_barrier();
+      if (k0 < r.wend) {
+        if (k0 + KT > r.sure) x.hide(r.sees - k0 - 4 * r.h);
+        x.soften(a.scale2, slack);
+      }
+      if (t + 2 < tiles) {
+        sk.store(lds + b2);
+        if (t + 3 < tiles) sk.load(k0 + 3 * KT, r.klen);
+      }
+      if (t + 1 < tiles) {
+        sv.store(lds + b1 + T::kBytes);
+        if (t + 2 < tiles) sv.load(k0 + 2 * KT, r.klen);
+      }
+      lds_barrier();
+      // (behind the last tile the scores are those of what the buffer holds, and not used)
+      if (k0 < r.wend) x.mix_then_scores(lds, col_lane + b0 + T::kBytes, row_lane + b1);
+      const int b = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = b;
+    }
+    if (!second) lds_barrier();
+  }
+  x.finish(a, r);
+}
+
+// Joins the splits of a row: out = sum_s exp(lse_s - lse) out_s.  At most 64
+// splits: a lane has the weight of one.  WAVES waves to a row, each with some of
+// the splits, 8 of which it requests together.
+constexpr int kJoinRows = 4; // waves of a block
+template <int DT, int WAVES> __global__ __launch_bounds__(64 * kJoinRows) void join_kernel(const AttnArgs a, int64_t count) {
+  __shared__ f32x4v lds[kJoinRows][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = wave % WAVES;
+  const int64_t at = (int64_t)blockIdx.x * (kJoinRows / WAVES) + wave / WAVES;
+  const bool any = at < count;
+  const float lse = any && lane < a.splits ? a.part_lse[lane * count + at] : -kInf;
+  const int d = lane * 4, n = any ? a.D - d : 0;
+  Vec<16> v[8]; // (the first are on their way while the weights are formed)
+  const auto request = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = s0 + j * WAVES;
+      v[j] = load_part<DT_F32>(a.part, (s * count + at) * a.D + d, s < a.splits ? n : 0);
+    }
+  };
+  request(part);
   float most = lse;
 #pragma unroll
   for (int k = 32; k; k >>= 1) most = fmaxf(most, __shfl_xor(most, k));
@@ -169,14 +342,23 @@ template <int DT> __global__ __launch_bounds__(64 * kJoinRows) void join_kernel(
   const bool some = !(total == 0.0f);
   const float mine = some ? weight / total : 0.0f;
   f32x4v acc = {0, 0, 0, 0};
-  const int d = lane * 4, n = a.D - d;
-  for (int s = 0; s < a.splits; ++s) {
-    const float by = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), s));
-    if (by == 0.0f || n <= 0) continue;
-    const Vec<16> v = load_part<DT_F32>(a.part, (s * count + at) * a.D + d, n);
+  for (int s0 = part; s0 < a.splits; s0 += 8 * WAVES) {
+    if (s0 != part) request(s0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += by * __uint_as_float(v.w[i]);
+    for (int j = 0; j < 8; ++j) {
+      const float by = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), min(s0 + j * WAVES, 63)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(by, __uint_as_float(v[j].w[i]), acc[i]);
+    }
   }
+  if constexpr (WAVES > 1) {
+    lds[wave][lane] = acc;
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) acc += lds[wave + w][lane];
+  }
+  if (!any) return;
   const uint32_t unit = (uint32_t)(at / a.rows);
   const int row = (int)(at - (int64_t)unit * a.rows), b = (int)fdiv(unit, a.div_Hk), hk = (int)(unit - b * a.div_Hk.d);
   if (a.lse && lane == 0) a.lse[stat_at(a, b, hk, row)] = some ? most + logf(total) : -kInf;
@@ -184,31 +366,44 @@ template <int DT> __global__ __launch_bounds__(64 * kJoinRows) void join_kernel(
   store_four<DT>((void *)a.out.p, to + d, n, acc);
 }
 
-// A gradient's splits added up in their order: rows [units][len][D] of the
-// partial results to head hk * group + g of sample b, position r / group
-template <int DT>
-__global__ __launch_bounds__(64 * kJoinRows) void sum_kernel(const AttnHeads out, const float *part, int splits, int D,
-                                                             int64_t count, int64_t len, FastDiv div_group,
-                                                             FastDiv div_Hk) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * kJoinRows + (threadIdx.x >> 6);
-  if (at >= count) return;
-  const int d = lane * 4, n = D - d;
+// Gradients' splits added up in their order: 4 elements to a thread.
+struct SumArgs {
+  AttnHeads out[2];
+  const float *part;
+  int splits, D;
+  int64_t rows, len;      // of all units, of one
+  FastDiv div_quads;      // 4-element steps of a row
+  FastDiv div_group, div_Hk;
+};
+constexpr int kSumThreads = 256;
+template <int DT> __global__ __launch_bounds__(kSumThreads) void sum_kernel(const SumArgs a) {
+  const uint32_t row = blockIdx.x * (kSumThreads / a.div_quads.d) + fdiv(threadIdx.x, a.div_quads);
+  const int d = (int)(threadIdx.x % a.div_quads.d) * 4, n = a.D - d;
+  if (threadIdx.x >= kSumThreads / a.div_quads.d * a.div_quads.d || row >= a.rows) return;
   f32x4v acc = {0, 0, 0, 0};
-  for (int s = 0; s < splits; ++s) {
-    const Vec<16> v = load_part<DT_F32>(part, (s * count + at) * D + d, n);
+  const float *part = a.part + (int64_t)blockIdx.y * a.splits * a.rows * a.D;
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    Vec<16> v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += __uint_as_float(v.w[i]);
+    for (int j = 0; j < 8; ++j)
+      v[j] = load_part<DT_F32>(part, ((s0 + j) * a.rows + row) * a.D + d, s0 + j < a.splits ? n : 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += __uint_as_float(v[j].w[i]);
   }
-  const uint32_t unit = (uint32_t)(at / len), r = (uint32_t)(at - (int64_t)unit * len);
-  const uint32_t b = fdiv(unit, div_Hk), hk = unit - b * div_Hk.d, q = fdiv(r, div_group), g = r - q * div_group.d;
-  store_four<DT>((void *)out.p, b * out.b + q * out.t + (int64_t)(hk * div_group.d + g) * out.h + d, n, acc);
+  const uint32_t unit = (uint32_t)(row / a.len), r = (uint32_t)(row - (int64_t)unit * a.len);
+  const uint32_t b = fdiv(unit, a.div_Hk), hk = unit - b * a.div_Hk.d, q = fdiv(r, a.div_group), g = r - q * a.div_group.d;
+  const AttnHeads &out = a.out[blockIdx.y];
+  store_four<DT>((void *)out.p, b * out.b + q * out.t + (int64_t)(hk * a.div_group.d + g) * out.h + d, n, acc);
 }
 
 template <int DT, int DP> void launch(const AttnArgs &a, int waves, hipStream_t st) {
   if (waves == 1) hipLaunchKernelGGL((attention_kernel<DT, DP, 1>), dim3(a.blocks), dim3(64), 0, st, a);
-  else
+  else if (waves == kAttnWaves || !attn_wide(Elem<DT>::bytes, DP))
     hipLaunchKernelGGL((attention_kernel<DT, DP, kAttnWaves>), dim3(a.blocks), dim3(64 * kAttnWaves), 0, st, a);
+  else if constexpr (attn_wide(Elem<DT>::bytes, DP))
+    hipLaunchKernelGGL((attention_wide_kernel<DT, DP>), dim3(a.blocks), dim3(128 * kAttnWaves), 0, st, a);
 }
 template <int DT> hipError_t launch(const AttnArgs &a, int waves, hipStream_t st) {
   switch (attn_padded(a.D)) {
@@ -234,23 +429,39 @@ hipError_t sb_launch_attention(const sb::AttnArgs &a, int dtype, int waves, hipS
 
 hipError_t sb_launch_attention_join(const sb::AttnArgs &a, int dtype, hipStream_t st) {
   const int64_t count = (int64_t)a.B * a.Hk * a.rows;
-  const dim3 grid((unsigned)((count + sb::kJoinRows - 1) / sb::kJoinRows)), block(64 * sb::kJoinRows);
-  if (dtype == sb::DT_F32) hipLaunchKernelGGL((sb::join_kernel<sb::DT_F32>), grid, block, 0, st, a, count);
-  else if (dtype == sb::DT_F16) hipLaunchKernelGGL((sb::join_kernel<sb::DT_F16>), grid, block, 0, st, a, count);
-  else hipLaunchKernelGGL((sb::join_kernel<sb::DT_BF16>), grid, block, 0, st, a, count);
+  const int waves = a.splits > 8 ? sb::kJoinRows : 1; // (rows whose splits a wave requests at once need no other)
+  const int64_t each = sb::kJoinRows / waves;
+  const dim3 grid((unsigned)((count + each - 1) / each)), block(64 * sb::kJoinRows);
+#define SB_JOIN(W)                                                                                                     \
+  if (dtype == sb::DT_F32) hipLaunchKernelGGL((sb::join_kernel<sb::DT_F32, W>), grid, block, 0, st, a, count);         \
+  else if (dtype == sb::DT_F16) hipLaunchKernelGGL((sb::join_kernel<sb::DT_F16, W>), grid, block, 0, st, a, count);    \
+  else hipLaunchKernelGGL((sb::join_kernel<sb::DT_BF16, W>), grid, block, 0, st, a, count)
+  if (waves == 1) {
+    SB_JOIN(1);
+  } else {
+    SB_JOIN(sb::kJoinRows);
+  }
+#undef SB_JOIN
   return hipGetLastError();
 }
 
-hipError_t sb_launch_attention_sum(const sb::AttnArgs &a, const sb::AttnHeads &out, const float *part, int64_t len,
-                                   int group, int dtype, hipStream_t st) {
-  const int64_t count = (int64_t)a.B * a.Hk * len;
-  const dim3 grid((unsigned)((count + sb::kJoinRows - 1) / sb::kJoinRows)), block(64 * sb::kJoinRows);
-  const sb::FastDiv dg = sb::make_fastdiv((uint32_t)group);
-#define SB_SUM(DT) \
-  hipLaunchKernelGGL((sb::sum_kernel<DT>), grid, block, 0, st, out, part, a.splits, a.D, count, len, dg, a.div_Hk)
-  if (dtype == sb::DT_F32) SB_SUM(sb::DT_F32);
-  else if (dtype == sb::DT_F16) SB_SUM(sb::DT_F16);
-  else SB_SUM(sb::DT_BF16);
-#undef SB_SUM
+hipError_t sb_launch_attention_sum(const sb::AttnArgs &a, const sb::AttnHeads *out, int n, int64_t len, int group,
+                                   int dtype, hipStream_t st) {
+  sb::SumArgs s;
+  s.out[0] = out[0];
+  s.out[1] = out[n - 1];
+  s.part = a.part;
+  s.splits = a.splits;
+  s.D = a.D;
+  s.len = len;
+  s.rows = (int64_t)a.B * a.Hk * len;
+  s.div_quads = sb::make_fastdiv((uint32_t)((a.D + 3) / 4));
+  s.div_group = sb::make_fastdiv((uint32_t)group);
+  s.div_Hk = a.div_Hk;
+  const int64_t each = sb::kSumThreads / s.div_quads.d;
+  const dim3 grid((unsigned)((s.rows + each - 1) / each), (unsigned)n), block(sb::kSumThreads);
+  if (dtype == sb::DT_F32) hipLaunchKernelGGL((sb::sum_kernel<sb::DT_F32>), grid, block, 0, st, s);
+  else if (dtype == sb::DT_F16) hipLaunchKernelGGL((sb::sum_kernel<sb::DT_F16>), grid, block, 0, st, s);
+  else hipLaunchKernelGGL((sb::sum_kernel<sb::DT_BF16>), grid, block, 0, st, s);
   return hipGetLastError();
 }

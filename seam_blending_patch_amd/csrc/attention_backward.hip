@@ -19,9 +19,9 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
   using St = Stage<DT, DP, KT, kThreads>;
   constexpr bool kAhead = St::N <= 8 && T::kFrags * 4 <= 64; // the next tile is requested while this one is used
   constexpr int kBufs = kAhead ? 2 : 1, NB = DP / 32, PW = DT == DT_F32 ? 16 : 8;
-  __shared__ alignas(16) char lds[kBufs][2][T::kBytes];
+  __shared__ alignas(1024) char lds[kBufs * 2 * T::kBytes]; // of each buffer keys, then values
 
-  const Work w = work_of(a);
+  const Work w = work_of<true>(a);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, n = lane & 31;
   const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
   const int off = klen - qlen, live_rows = qlen * a.group;
@@ -68,12 +68,13 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
   const int64_t k_base = w.b * a.k.b + w.hk * a.k.h, v_base = w.b * a.v.b + w.hk * a.v.h;
   const auto k_at = [&](int r) { return k_base + r * a.k.t; };
   const auto v_at = [&](int r) { return v_base + r * a.v.t; };
+  const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
   St sk, sv;
   if (kAhead && begin < end) {
     sk.load(a.k.p, begin, klen, a.D, k_at);
     sv.load(a.v.p, begin, klen, a.D, v_at);
-    sk.store(lds[0][0]);
-    sv.store(lds[0][1]);
+    sk.store(lds);
+    sv.store(lds + T::kBytes);
     __syncthreads();
   }
   for (int k0 = begin, cur = 0; k0 < end; k0 += KT) {
@@ -84,19 +85,17 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
       }
     } else {
       __syncthreads();
-      sk.load(a.k.p, k0, klen, a.D, k_at);
-      sk.store(lds[0][0]);
-      sv.load(a.v.p, k0, klen, a.D, v_at);
-      sv.store(lds[0][1]);
+      stage_tile<DT, DP, KT, kThreads>(lds, a.k.p, k0, klen, a.D, k_at);
+      stage_tile<DT, DP, KT, kThreads>(lds + T::kBytes, a.v.p, k0, klen, a.D, v_at);
       __syncthreads();
     }
-    const char *kt = lds[cur][0], *vt = lds[cur][1];
+    const int kt = row_lane + cur, vt = kt + T::kBytes, kc = col_lane + cur;
     if (k0 < wend) {
       f32x16 s = {0}, dp = {0};
 #pragma unroll
       for (int u = 0; u < T::kFrags; ++u) {
-        s = mma<DT>(T::row_fragment(kt, n, u, h), qf[u], s);
-        dp = mma<DT>(T::row_fragment(vt, n, u, h), gf[u], dp);
+        s = mma<DT>(T::row_fragment(lds, kt, 0, u), qf[u], s);
+        dp = mma<DT>(T::row_fragment(lds, vt, 0, u), gf[u], dp);
       }
       float ds[16];
 #pragma unroll
@@ -109,13 +108,13 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
       uint32_t p[PW];
       pack_operand<DT>(ds, p);
 #pragma unroll
-      for (int db = 0; db < NB; ++db) dq[db] = T::column_product(kt, 0, db, p, dq[db], lane);
+      for (int db = 0; db < NB; ++db) dq[db] = T::column_product(lds, kc, 0, db, p, dq[db]);
     }
     if constexpr (kAhead) {
-      cur ^= 1;
+      cur ^= 2 * T::kBytes;
       if (k0 + KT < end) {
-        sk.store(lds[cur][0]);
-        sv.store(lds[cur][1]);
+        sk.store(lds + cur);
+        sv.store(lds + cur + T::kBytes);
       }
       __syncthreads();
     }
@@ -149,11 +148,11 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
   constexpr int kBufs = 4 * T::kBytes <= 65536 * (PAIR ? 1 : 2) ? 2 : 1;
   constexpr bool kAhead = kBufs == 2;
   constexpr int W = PAIR ? 2 : 1, NF = T::kFrags / W, NB = DP / 32 / W, PW = DT == DT_F32 ? 16 : 8;
-  __shared__ alignas(16) char lds[kBufs][2][T::kBytes];
+  __shared__ alignas(1024) char lds[kBufs * 2 * T::kBytes]; // of each buffer q, then dout
   __shared__ alignas(16) float stats[kBufs][2][RT]; // log sums (base 2) and deltas
   __shared__ float halves[PAIR ? kAttnWaves : 1][PAIR ? 32 : 1][64];
 
-  const Work w = work_of(a);
+  const Work w = work_of<false>(a);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, n = lane & 31;
   const int part = PAIR ? wave & 1 : 0;
   const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
@@ -179,6 +178,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
 
   const auto q_at = [&](int r) { return row_at(a.q, a, w.b, w.hk, r); };
   const auto g_at = [&](int r) { return row_at(a.dout, a, w.b, w.hk, r); };
+  const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
   St sq, sg;
   float stat[2];
   const auto load_stats = [&](int r) { // of row r + thread
@@ -202,8 +202,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
     sq.load(a.q.p, begin, live_rows, a.D, q_at);
     sg.load(a.dout.p, begin, live_rows, a.D, g_at);
     load_stats(begin);
-    sq.store(lds[0][0]);
-    sg.store(lds[0][1]);
+    sq.store(lds);
+    sg.store(lds + T::kBytes);
     store_stats(0);
     __syncthreads();
   }
@@ -217,20 +217,18 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
     } else {
       __syncthreads();
       load_stats(r0);
-      sq.load(a.q.p, r0, live_rows, a.D, q_at);
-      sq.store(lds[0][0]);
-      sg.load(a.dout.p, r0, live_rows, a.D, g_at);
-      sg.store(lds[0][1]);
+      stage_tile<DT, DP, RT, kThreads>(lds, a.q.p, r0, live_rows, a.D, q_at);
+      stage_tile<DT, DP, RT, kThreads>(lds + T::kBytes, a.dout.p, r0, live_rows, a.D, g_at);
       store_stats(0);
       __syncthreads();
     }
-    const char *qt = lds[cur][0], *gt = lds[cur][1];
+    const int qt = row_lane + cur, gt = qt + T::kBytes, qc = col_lane + cur, gc = qc + T::kBytes;
     if (PAIR || r0 + RT > wfrom) {
       f32x16 s = {0}, dp = {0};
 #pragma unroll
       for (int u = 0; u < NF; ++u) {
-        s = mma<DT>(T::row_fragment(qt, n, u + part * NF, h), kf[u], s);
-        dp = mma<DT>(T::row_fragment(gt, n, u + part * NF, h), vf[u], dp);
+        s = mma<DT>(T::row_fragment(lds, qt, 0, u + part * NF), kf[u], s);
+        dp = mma<DT>(T::row_fragment(lds, gt, 0, u + part * NF), vf[u], dp);
       }
       if constexpr (PAIR) { // (the barrier before the next tile keeps these until they are read)
 #pragma unroll
@@ -248,8 +246,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
       float p[16], ds[16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 lse2 = *reinterpret_cast<const float4 *>(&stats[cur][0][8 * j + 4 * h]);
-        const float4 delta = *reinterpret_cast<const float4 *>(&stats[cur][1][8 * j + 4 * h]);
+        const float4 lse2 = *reinterpret_cast<const float4 *>(&stats[cur != 0][0][8 * j + 4 * h]);
+        const float4 delta = *reinterpret_cast<const float4 *>(&stats[cur != 0][1][8 * j + 4 * h]);
         const float l4[4] = {lse2.x, lse2.y, lse2.z, lse2.w}, d4[4] = {delta.x, delta.y, delta.z, delta.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -270,16 +268,16 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
       pack_operand<DT>(ds, pd);
 #pragma unroll
       for (int db = 0; db < NB; ++db) {
-        dv[db] = T::column_product(gt, 0, db + part * NB, pp, dv[db], lane);
-        dk[db] = T::column_product(qt, 0, db + part * NB, pd, dk[db], lane);
+        dv[db] = T::column_product(lds, gc, 0, db + part * NB, pp, dv[db]);
+        dk[db] = T::column_product(lds, qc, 0, db + part * NB, pd, dk[db]);
       }
     }
     if constexpr (kAhead) {
-      cur ^= 1;
+      cur ^= 2 * T::kBytes;
       if (r0 + RT < end) {
-        sq.store(lds[cur][0]);
-        sg.store(lds[cur][1]);
-        store_stats(cur);
+        sq.store(lds + cur);
+        sg.store(lds + cur + T::kBytes);
+        store_stats(cur != 0);
       }
       __syncthreads();
     }
@@ -302,32 +300,423 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
   }
 }
 
-template <int DT, int DP> void launch_dq(const AttnArgs &a, int waves, hipStream_t st) {
-  if (waves == 1) hipLaunchKernelGGL((dq_kernel<DT, DP, 1>), dim3(a.blocks), dim3(64), 0, st, a);
-  else hipLaunchKernelGGL((dq_kernel<DT, DP, kAttnWaves>), dim3(a.blocks), dim3(64 * kAttnWaves), 0, st, a);
+// ---------------------------------------------------------------------------
+// The same two gradients for 16-bit heads of up to 192: every turn multiplies the
+// next tile's scores while it turns this tile's into probabilities, an element
+// beside each product, so that one wave keeps the matrix cores and the vector
+// unit at work together.  Three buffers: the turn of tile t reads tiles t and
+// t + 1 and stores tile t + 2.
+// ---------------------------------------------------------------------------
+constexpr int kProductsAhead = 6; // LDS reads this many products before their use
+
+// A barrier for LDS alone: what is on its way from memory stays on its way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
-template <int DT, int DP> void launch_dkv(const AttnArgs &a, int, hipStream_t st) {
-  hipLaunchKernelGGL((dkv_kernel<DT, DP, attn_paired(Elem<DT>::bytes, DP)>), dim3(a.blocks), dim3(64 * kAttnWaves), 0,
-                     st, a);
+
+// dq: a wave has R columns of 32 rows.
+template <int DT, int DP, int NW, int R>
+__global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a) {
+  constexpr int kThreads = 64 * NW, KT = 32, ROWS = 32 * R;
+  using T = Tile<DT, DP, KT>;
+  using St = RowStage<DT, DP, KT, kThreads>;
+  constexpr int NB = DP / 32, NF = T::kFrags;
+  __shared__ alignas(1024) char lds[3 * 2 * T::kBytes]; // of each buffer keys, then values
+
+  const Work w = work_of<true>(a);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, n = lane & 31;
+  const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
+  const int off = klen - qlen, live_rows = qlen * a.group;
+  const int r0 = w.tile * ROWS * NW, wr0 = r0 + wave * ROWS;
+  const auto seen = [&](int r) {
+    return a.causal ? min(max((int)fdiv((uint32_t)r, a.div_group) + off + 1, 0), klen) : klen;
+  };
+  const int sure = seen(min(wr0, max(live_rows - 1, 0)));
+  const int last = min(r0 + ROWS * NW, live_rows) - 1;
+  const int begin = w.split * a.span;
+  const int end = last < r0 ? 0 : min(seen(last), begin + a.span);
+
+  u32x4 qf[R][NF], gf[R][NF];
+  float delta[R], lse2[R];
+  int sees[R];
+#pragma unroll
+  for (int c = 0; c < R; ++c) {
+    const int row = wr0 + 32 * c + n;
+    const bool live = row < live_rows;
+    sees[c] = live ? seen(row) : klen;
+    const int64_t at = live ? row_at(a.q, a, w.b, w.hk, row) : 0, to = live ? row_at(a.out, a, w.b, w.hk, row) : 0,
+                  gt = live ? row_at(a.dout, a, w.b, w.hk, row) : 0;
+    float d = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NF; ++u) {
+      qf[c][u] = load_chunk<DT>(a.q.p, at, 2 * u + h, a.D, live);
+      gf[c][u] = load_chunk<DT>(a.dout.p, gt, 2 * u + h, a.D, live);
+      const u32x4 of = load_chunk<DT>(a.out.p, to, 2 * u + h, a.D, live);
+      float f[T::V], g[T::V];
+      unpack<DT, 16>(Vec<16>{of[0], of[1], of[2], of[3]}, f);
+      unpack<DT, 16>(Vec<16>{gf[c][u][0], gf[c][u][1], gf[c][u][2], gf[c][u][3]}, g);
+#pragma unroll
+      for (int i = 0; i < T::V; ++i) d = __builtin_fmaf(f[i], g[i], d);
+    }
+    delta[c] = half_sum(d);
+    lse2[c] = kInf; // (a row that sees no key, or is none: its probabilities are exp2(-inf))
+    if (live) {
+      const int64_t st = stat_at(a, w.b, w.hk, row);
+      const float lse = a.lse[st];
+      if (lse != -kInf) lse2[c] = lse * kLog2e;
+      if (w.split == 0 && h == 0) a.delta[st] = delta[c];
+    }
+  }
+  f32x16 dq[R][NB];
+#pragma unroll
+  for (int c = 0; c < R; ++c)
+#pragma unroll
+    for (int db = 0; db < NB; ++db) dq[c][db] = f32x16{0};
+
+  const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
+  const int tiles = end > begin ? (end - begin + KT - 1) / KT : 0;
+  if (tiles) {
+    clear_tiles<kThreads>(lds, sizeof lds, a.D < DP);
+    St sk, sv;
+    sk.start(a.k.p, w.b * a.k.b + w.hk * a.k.h, a.k.t, begin, a.D);
+    sv.start(a.v.p, w.b * a.v.b + w.hk * a.v.h, a.v.t, begin, a.D);
+    sk.load(begin, klen);
+    sv.load(begin, klen);
+    sk.store(lds);
+    sv.store(lds + T::kBytes);
+    if (tiles > 1) {
+      sk.load(begin + KT, klen);
+      sv.load(begin + KT, klen);
+      sk.store(lds + 2 * T::kBytes);
+      sv.store(lds + 3 * T::kBytes);
+    }
+    if (tiles > 2) {
+      sk.load(begin + 2 * KT, klen);
+      sv.load(begin + 2 * KT, klen);
+    }
+    __syncthreads();
+    f32x16 s[R], dp[R], s1[R], dp1[R];
+    // steps: for each fragment u the keys' and the values', times R columns
+    const auto read = [&](int buffer, int i) {
+      return T::row_fragment(lds, row_lane + buffer + (i & 1) * T::kBytes, 0, i >> 1);
+    };
+#pragma unroll
+    for (int c = 0; c < R; ++c) s[c] = dp[c] = f32x16{0};
+    in_order<2 * NF, kProductsAhead>([&](int i) { return read(0, i); }, [&](int i, u32x4 f) {
+#pragma unroll
+      for (int c = 0; c < R; ++c) {
+        if (i & 1) dp[c] = mma<DT>(f, gf[c][i >> 1], dp[c]);
+        else s[c] = mma<DT>(f, qf[c][i >> 1], s[c]);
+      }
+    });
+    int b0 = 0, b1 = 2 * T::kBytes, b2 = 4 * T::kBytes;
+    for (int t = 0, k0 = begin; t < tiles; ++t, k0 += KT) {
+      if (t + 2 < tiles) {
+        sk.store(lds + b2);
+        sv.store(lds + b2 + T::kBytes);
+        if (t + 3 < tiles) {
+          sk.load(k0 + 3 * KT, klen);
+          sv.load(k0 + 3 * KT, klen);
+        }
+      }
+      {
+        float ds[R][16];
+#pragma unroll
+        for (int c = 0; c < R; ++c) s1[c] = dp1[c] = f32x16{0};
+        // (behind the last tile: scores of what the buffer holds, not used)
+        uint32_t p[R][8];
+        in_order<2 * NF + 2 * NB, kProductsAhead>(
+            [&](int i) {
+              const int j = i - 2 * NF;
+              return j < 0 ? read(b1, i) : T::column_fragment(lds, col_lane + b0, 0, j % NB, j / NB);
+            },
+            [&](int i, u32x4 f) {
+              const int j = i - 2 * NF;
+#pragma unroll
+              for (int c = 0; c < R; ++c) {
+                if (j >= 0) {
+                  const uint32_t *q = p[c] + 4 * (j / NB);
+                  dq[c][j % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, dq[c][j % NB]);
+                  continue;
+                }
+                if (i & 1) dp1[c] = mma<DT>(f, gf[c][i >> 1], dp1[c]);
+                else s1[c] = mma<DT>(f, qf[c][i >> 1], s1[c]);
+#pragma unroll
+                for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e)
+                  ds[c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e], a.scale2, -lse2[c])) * (dp[c][e] - delta[c]);
+                if (j == -1) {
+                  if (k0 + KT > sure) {
+                    const int left = sees[c] - k0 - 4 * h;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) ds[c][x] = 8 * (x >> 2) + (x & 3) < left ? ds[c][x] : 0.0f;
+                  }
+                  pack_operand<DT>(ds[c], p[c]);
+                }
+              }
+            });
+#pragma unroll
+        for (int c = 0; c < R; ++c) {
+          s[c] = s1[c];
+          dp[c] = dp1[c];
+        }
+      }
+      lds_barrier();
+      const int b = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = b;
+    }
+  }
+
+#pragma unroll
+  for (int c = 0; c < R; ++c) {
+    const int row = wr0 + 32 * c + n;
+    if (row >= a.rows) continue;
+    const bool live = row < live_rows;
+    const float by = live ? a.scale : 0.0f;
+    if (a.part) {
+      const int64_t at = ((int64_t)w.split * a.B * a.Hk + w.unit) * a.rows + row;
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+        store_column<DT_F32>(a.part, at * a.D, db, h, a.D, live ? dq[c][db] : f32x16{0}, by);
+    } else {
+      const int64_t at = row_at(a.dq, a, w.b, w.hk, row);
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+        store_column<DT>((void *)a.dq.p, at, db, h, a.D, live ? dq[c][db] : f32x16{0}, by);
+    }
+  }
+}
+
+// dk and dv: a wave has 32 keys.
+template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv_pipelined_kernel(const AttnArgs a) {
+  constexpr int kThreads = 64 * kAttnWaves, RT = 32, KEYS = 32 * kAttnWaves;
+  using T = Tile<DT, DP, RT>;
+  using S = Share<DT, DP, RT, kThreads>;
+  constexpr int NF = T::kFrags, NB = DP / 32;
+  __shared__ alignas(1024) char lds[3 * 2 * T::kBytes]; // of each buffer q, then dout
+  __shared__ alignas(16) float stats[3][2][RT];         // log sums (base 2) and deltas
+
+  const Work w = work_of<false>(a);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, n = lane & 31;
+  const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
+  const int off = klen - qlen, live_rows = qlen * a.group;
+  const int k0 = w.tile * KEYS, wk0 = k0 + wave * 32, key = wk0 + n;
+  const bool live = key < klen;
+  // rows that see a key: from first(key) on
+  const auto first = [&](int k) { return a.causal ? max(k - off, 0) * a.group : 0; };
+  const int from = first(key), wsure = first(wk0 + 31);
+  const int begin = max(w.split * a.span, first(k0) / RT * RT);
+  const int end = k0 >= klen ? 0 : min(live_rows, w.split * a.span + a.span);
+
+  u32x4 kf[NF], vf[NF];
+#pragma unroll
+  for (int u = 0; u < NF; ++u) {
+    kf[u] = load_chunk<DT>(a.k.p, w.b * a.k.b + w.hk * a.k.h + (live ? key : 0) * a.k.t, 2 * u + h, a.D, live);
+    vf[u] = load_chunk<DT>(a.v.p, w.b * a.v.b + w.hk * a.v.h + (live ? key : 0) * a.v.t, 2 * u + h, a.D, live);
+  }
+  f32x16 dk[NB], dv[NB];
+#pragma unroll
+  for (int db = 0; db < NB; ++db) dk[db] = dv[db] = f32x16{0};
+
+  u32x4 sq[S::N], sg[S::N];
+  float stat[2];
+  const bool any = S::chunk() * T::V < a.D && !(S::kIdle && S::row(0) >= RT);
+  const int e0 = any ? S::chunk() * T::V : 0;
+  // A tile's packed rows are the last one's moved on where whole queries fill it:
+  // then offsets are added to, not formed.
+  const bool regular = RT % a.group == 0;
+  const int64_t q_step = RT / a.group * a.q.t, g_step = RT / a.group * a.dout.t;
+  int64_t q_off[S::N], g_off[S::N], st_off;
+  const auto place = [&](int r) { // (rows past the end: the last one, whose probabilities are zeros then)
+#pragma unroll
+    for (int k = 0; k < S::N; ++k) {
+      const int x = min(r + S::row(k), live_rows - 1);
+      q_off[k] = row_at(a.q, a, w.b, w.hk, x) + e0;
+      g_off[k] = row_at(a.dout, a, w.b, w.hk, x) + e0;
+    }
+    st_off = stat_at(a, w.b, w.hk, min(r + (int)threadIdx.x % RT, live_rows - 1));
+  };
+  const auto load = [&](int r) { // the tile of rows r on, the one after the last loaded
+    typedef typename El<DT>::bits bits;
+    if (!regular || r + RT > live_rows) place(r);
+#pragma unroll
+    for (int k = 0; k < S::N; ++k) {
+      sq[k] = *reinterpret_cast<const typename El<DT>::vec *>((const bits *)a.q.p + q_off[k]);
+      sg[k] = *reinterpret_cast<const typename El<DT>::vec *>((const bits *)a.dout.p + g_off[k]);
+      q_off[k] += q_step;
+      g_off[k] += g_step;
+    }
+    stat[0] = a.lse[st_off]; // (looked at when it is stored, so that nothing waits for it here)
+    stat[1] = a.delta[st_off];
+    st_off += RT / a.group;
+  };
+  const auto store = [&](int buffer, int r) {
+    char *to = lds + buffer * 2 * T::kBytes;
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < S::N; ++k) {
+        *reinterpret_cast<u32x4 *>(to + T::place(S::row(k), S::chunk())) = sq[k];
+        *reinterpret_cast<u32x4 *>(to + T::kBytes + T::place(S::row(k), S::chunk())) = sg[k];
+      }
+    }
+    if (threadIdx.x < RT) {
+      // (no row, or one without keys: no probability)
+      stats[buffer][0][threadIdx.x] = r + (int)threadIdx.x >= live_rows || stat[0] == -kInf ? kInf : stat[0] * kLog2e;
+      stats[buffer][1][threadIdx.x] = stat[1];
+    }
+  };
+  const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
+  const int tiles = end > begin ? (end - begin + RT - 1) / RT : 0;
+  if (tiles) {
+    clear_tiles<kThreads>(lds, sizeof lds, a.D < DP);
+    place(begin);
+    load(begin);
+    store(0, begin);
+    if (tiles > 1) {
+      load(begin + RT);
+      store(1, begin + RT);
+    }
+    if (tiles > 2) load(begin + 2 * RT);
+    __syncthreads();
+    f32x16 s, dp, s1, dp1;
+    const auto read = [&](int buffer, int i) { // the rows' q and dout by turns
+      return T::row_fragment(lds, row_lane + buffer * 2 * T::kBytes + (i & 1) * T::kBytes, 0, i >> 1);
+    };
+    s = dp = f32x16{0};
+    in_order<2 * NF, kProductsAhead>([&](int i) { return read(0, i); }, [&](int i, u32x4 f) {
+      if (i & 1) dp = mma<DT>(f, vf[i >> 1], dp);
+      else s = mma<DT>(f, kf[i >> 1], s);
+    });
+    int b0 = 0, b1 = 1, b2 = 2;
+    for (int t = 0, r0 = begin; t < tiles; ++t, r0 += RT) {
+      if (t + 2 < tiles) {
+        store(b2, r0 + 2 * RT);
+        if (t + 3 < tiles) load(r0 + 3 * RT);
+      }
+      {
+        float p[16], ds[16];
+        f32x4v lse2[4], delta[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          lse2[j] = *reinterpret_cast<const f32x4v *>(&stats[b0][0][8 * j + 4 * h]);
+          delta[j] = *reinterpret_cast<const f32x4v *>(&stats[b0][1][8 * j + 4 * h]);
+        }
+        s1 = dp1 = f32x16{0};
+        // (behind the last tile: scores of what the buffer holds, not used)
+        uint32_t pp[8], pd[8];
+        in_order<2 * NF + 4 * NB, kProductsAhead>(
+            [&](int i) {
+              const int j = i - 2 * NF;
+              return j < 0 ? read(b1, i)
+                           : T::column_fragment(lds, col_lane + b0 * 2 * T::kBytes + (j < 2 * NB ? T::kBytes : 0), 0, j % NB,
+                                                j / NB % 2);
+            },
+            [&](int i, u32x4 f) {
+              const int j = i - 2 * NF;
+              if (j >= 0) {
+                const uint32_t *q = (j < 2 * NB ? pp : pd) + 4 * (j / NB % 2);
+                const u32x4 b = {q[0], q[1], q[2], q[3]};
+                if (j < 2 * NB) dv[j % NB] = mma<DT>(f, b, dv[j % NB]);
+                else dk[j % NB] = mma<DT>(f, b, dk[j % NB]);
+                return;
+              }
+              if (i & 1) dp1 = mma<DT>(f, vf[i >> 1], dp1);
+              else s1 = mma<DT>(f, kf[i >> 1], s1);
+#pragma unroll
+              for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e) {
+                p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.scale2, -lse2[e >> 2][e & 3]));
+                ds[e] = p[e] * (dp[e] - delta[e >> 2][e & 3]);
+              }
+              if (j == -1) {
+                if (r0 < wsure) { // causal: some row of the tile does not see some key of the wave
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) {
+                    const bool sees = r0 + 8 * (x >> 2) + 4 * h + (x & 3) >= from;
+                    p[x] = sees ? p[x] : 0.0f;
+                    ds[x] = sees ? ds[x] : 0.0f;
+                  }
+                }
+                pack_operand<DT>(p, pp);
+                pack_operand<DT>(ds, pd);
+              }
+            });
+        s = s1;
+        dp = dp1;
+      }
+      lds_barrier();
+      const int b = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = b;
+    }
+  }
+
+  if (key >= a.Lk) return;
+  const float by = live ? a.scale : 0.0f;
+  const int64_t units = (int64_t)a.B * a.Hk, at = ((int64_t)w.split * units + w.unit) * a.Lk + key;
+#pragma unroll
+  for (int db = 0; db < NB; ++db) {
+    const f32x16 k = live ? dk[db] : f32x16{0}, v = live ? dv[db] : f32x16{0};
+    if (a.part) {
+      store_column<DT_F32>(a.part, at * a.D, db, h, a.D, k, by);
+      store_column<DT_F32>(a.part, ((int64_t)a.splits * units * a.Lk + at) * a.D, db, h, a.D, v, 1.0f);
+    } else {
+      store_column<DT>((void *)a.dk.p, w.b * a.dk.b + w.hk * a.dk.h + key * a.dk.t, db, h, a.D, k, by);
+      store_column<DT>((void *)a.dv.p, w.b * a.dv.b + w.hk * a.dv.h + key * a.dv.t, db, h, a.D, v, 1.0f);
+    }
+  }
+}
+
+// wave_rows: 32 or 64 (where attn_columns allows it) rows of a wave, for whole
+// chunks; 0: the kernels that take any head
+template <int DT, int DP> void launch_dq(const AttnArgs &a, int waves, int wave_rows, hipStream_t st) {
+  const dim3 grid(a.blocks), block(64 * kAttnWaves);
+  if constexpr (attn_pipelined(Elem<DT>::bytes, DP)) {
+    if constexpr (attn_columns(DP) > 1) {
+      if (wave_rows == 64) {
+        hipLaunchKernelGGL((dq_pipelined_kernel<DT, DP, kAttnWaves, 2>), grid, block, 0, st, a);
+        return;
+      }
+    }
+    if (wave_rows) {
+      hipLaunchKernelGGL((dq_pipelined_kernel<DT, DP, kAttnWaves, 1>), grid, block, 0, st, a);
+      return;
+    }
+  }
+  if (waves == 1) hipLaunchKernelGGL((dq_kernel<DT, DP, 1>), grid, dim3(64), 0, st, a);
+  else hipLaunchKernelGGL((dq_kernel<DT, DP, kAttnWaves>), grid, block, 0, st, a);
+}
+template <int DT, int DP> void launch_dkv(const AttnArgs &a, int, int whole, hipStream_t st) {
+  const dim3 grid(a.blocks), block(64 * kAttnWaves);
+  if constexpr (attn_pipelined(Elem<DT>::bytes, DP)) {
+    if (whole) {
+      hipLaunchKernelGGL((dkv_pipelined_kernel<DT, DP>), grid, block, 0, st, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((dkv_kernel<DT, DP, attn_paired(Elem<DT>::bytes, DP)>), grid, block, 0, st, a);
 }
 
 #define SB_WIDTHS(F)                                                                                                   \
-  template <int DT> hipError_t F(const AttnArgs &a, int waves, hipStream_t st) {                                      \
+  template <int DT> hipError_t F(const AttnArgs &a, int waves, int rows, hipStream_t st) {                                     \
     switch (attn_padded(a.D)) {                                                                                        \
-    case 32: F<DT, 32>(a, waves, st); break;                                                                           \
-    case 64: F<DT, 64>(a, waves, st); break;                                                                           \
-    case 96: F<DT, 96>(a, waves, st); break;                                                                           \
-    case 128: F<DT, 128>(a, waves, st); break;                                                                         \
-    case 160: F<DT, 160>(a, waves, st); break;                                                                         \
-    case 192: F<DT, 192>(a, waves, st); break;                                                                         \
-    default: F<DT, 256>(a, waves, st);                                                                                 \
+    case 32: F<DT, 32>(a, waves, rows, st); break;                                                                           \
+    case 64: F<DT, 64>(a, waves, rows, st); break;                                                                           \
+    case 96: F<DT, 96>(a, waves, rows, st); break;                                                                           \
+    case 128: F<DT, 128>(a, waves, rows, st); break;                                                                         \
+    case 160: F<DT, 160>(a, waves, rows, st); break;                                                                         \
+    case 192: F<DT, 192>(a, waves, rows, st); break;                                                                         \
+    default: F<DT, 256>(a, waves, rows, st);                                                                                 \
     }                                                                                                                  \
     return hipGetLastError();                                                                                          \
   }                                                                                                                    \
-  hipError_t F(const AttnArgs &a, int dtype, int waves, hipStream_t st) {                                              \
-    if (dtype == DT_F32) return F<DT_F32>(a, waves, st);                                                               \
-    if (dtype == DT_F16) return F<DT_F16>(a, waves, st);                                                               \
-    return F<DT_BF16>(a, waves, st);                                                                                   \
+  hipError_t F(const AttnArgs &a, int dtype, int waves, int rows, hipStream_t st) {                                              \
+    if (dtype == DT_F32) return F<DT_F32>(a, waves, rows, st);                                                               \
+    if (dtype == DT_F16) return F<DT_F16>(a, waves, rows, st);                                                               \
+    return F<DT_BF16>(a, waves, rows, st);                                                                                   \
   }
 SB_WIDTHS(launch_dq)
 SB_WIDTHS(launch_dkv)
@@ -336,9 +725,9 @@ SB_WIDTHS(launch_dkv)
 } // namespace
 } // namespace sb
 
-hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, hipStream_t st) {
-  return sb::launch_dq(a, dtype, waves, st);
+hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int wave_rows, hipStream_t st) {
+  return sb::launch_dq(a, dtype, waves, wave_rows, st);
 }
-hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, hipStream_t st) {
-  return sb::launch_dkv(a, dtype, 0, st);
+hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, int whole, hipStream_t st) {
+  return sb::launch_dkv(a, dtype, sb::kAttnWaves, whole, st);
 }

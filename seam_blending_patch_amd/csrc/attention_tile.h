@@ -59,43 +59,74 @@ template <int DT, int DP, int ROWS> struct Tile {
   }
   static __device__ __forceinline__ int place(int r, int c) { return (r * SC + (c ^ mix(r))) * 16; }
 
-  static __device__ __forceinline__ u32x4 row_fragment(const char *tile, int r, int u, int h) {
-    return *reinterpret_cast<const u32x4 *>(tile + place(r, 2 * u + h));
+  // Places as a lane's own offset, in which only bits below a row's length still
+  // change, by exclusive or with what the loops count: no address arithmetic is
+  // left but that, and whole rows are constant offsets.  `tile` is an offset too.
+  //
+  // row fragment u of row r0 + lane % 32:
+  static __device__ __forceinline__ int row_place(int lane) { return place(lane & 31, lane >> 5); }
+  static __device__ __forceinline__ u32x4 row_fragment(const char *lds, int place, int r0, int u) {
+    return *reinterpret_cast<const u32x4 *>(lds + (place ^ (u << 5)) + r0 * (SC * 16));
+  }
+  // columns 32 db .. 32 db + 31 of the rows that column_product takes
+  static __device__ __forceinline__ int column_place(int lane) {
+    const int h = lane >> 5;
+    if constexpr (DT == DT_F32) return place(4 * h, (lane & 31) >> 2) + (lane & 3) * 4;
+    const int i = lane & 15; // of 16 lanes, which read the 4 columns i % 4 of row i / 4 and get column i of 4 rows
+    return place(4 * h + (i >> 2), ((lane >> 4) & 1) * 2 + ((i >> 1) & 1)) + (i & 1) * 8;
   }
 
-  // acc += (columns 32 db .. 32 db + 31 of rows r0 .. r0 + 31)^T times the 32 x 32
-  // operand `p` (16 result registers of a product; 16-bit: packed in pairs)
-  static __device__ __forceinline__ f32x16 column_product(const char *tile, int r0, int db, const uint32_t *p,
-                                                          f32x16 acc, int lane) {
-    const int h = lane >> 5;
+  // 16-bit: the fragment of those columns for terms 16 t .. 16 t + 15 of rows r0 on
+  static __device__ __forceinline__ u32x4 column_fragment(const char *lds, int place, int r0, int db, int t) {
+    u32x4 a;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = 16 * t + 8 * half;
+      const auto at = (__attribute__((address_space(3))) const char *)lds + (place ^ (mix(r) << 4) ^ (db << 6))
+                      + (r0 + r) * (SC * 16);
+      const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
+      const uint64_t w = __builtin_bit_cast(uint64_t, v);
+      a[2 * half] = (uint32_t)w;
+      a[2 * half + 1] = (uint32_t)(w >> 32);
+    }
+    return a;
+  }
+
+  // acc += (columns 32 db .. of rows r0 .. r0 + 31)^T times the 32 x 32 operand `p`
+  // (16 result registers of a product; 16-bit: packed in pairs)
+  static __device__ __forceinline__ f32x16 column_product(const char *lds, int place, int r0, int db,
+                                                          const uint32_t *p, f32x16 acc) {
     if constexpr (DT == DT_F32) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int r = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
-        const float a = *reinterpret_cast<const float *>(tile + place(r, 8 * db + ((lane & 31) >> 2)) + (lane & 3) * 4);
+        const int r = 8 * (i >> 2) + (i & 3);
+        const float a = *reinterpret_cast<const float *>(lds + (place ^ (mix(r) << 4) ^ (db << 7)) + (r0 + r) * (SC * 16));
         acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, __uint_as_float(p[i]), acc, 0, 0, 0);
       }
     } else {
-      // a transposing read gives lane i of 16 the 16 columns' i-th, of 4 rows
-      const int i = lane & 15, c = 4 * db + ((lane >> 4) & 1) * 2 + ((i >> 1) & 1);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        u32x4 a;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = r0 + 16 * t + 8 * half + 4 * h + (i >> 2);
-          const auto at = (__attribute__((address_space(3))) char *)tile + place(r, c) + (i & 1) * 8;
-          const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
-          const uint64_t w = __builtin_bit_cast(uint64_t, v);
-          a[2 * half] = (uint32_t)w;
-          a[2 * half + 1] = (uint32_t)(w >> 32);
-        }
-        acc = mma<DT>(a, u32x4{p[4 * t], p[4 * t + 1], p[4 * t + 2], p[4 * t + 3]}, acc);
-      }
+      for (int t = 0; t < 2; ++t)
+        acc = mma<DT>(column_fragment(lds, place, r0, db, t), u32x4{p[4 * t], p[4 * t + 1], p[4 * t + 2], p[4 * t + 3]},
+                      acc);
     }
     return acc;
   }
 };
+
+// Products whose fragments are read from LDS AHEAD of them: read(i) gives the
+// fragment of step i, use(i, fragment) its product.  The order is kept as written.
+template <int N, int AHEAD, class Read, class Use> __device__ __forceinline__ void in_order(Read read, Use use) {
+  u32x4 f[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD && i < N; ++i) f[i] = read(i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    use(i, f[i % AHEAD]);
+    if (i + AHEAD < N) f[i % AHEAD] = read(i + AHEAD);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
 
 // 16 result registers as the operand of the next product.  16-bit: rounded to
 // nearest, so that a product of probabilities (at most 1) or of their gradients
@@ -117,55 +148,126 @@ template <int DT> __device__ __forceinline__ u32x4 load_chunk(const void *p, int
   return u32x4{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
 
-// how the threads of a block share the chunks of a tile
-template <int DT, int DP, int ROWS, int THREADS> struct Stage {
+// How the threads of a block share the chunks of a tile: TURNS of them (all, or as
+// many as are to be in registers at a time) from turn k0 on.
+template <int DT, int DP, int ROWS, int THREADS> struct Share {
   using T = Tile<DT, DP, ROWS>;
   static constexpr int N = (ROWS * T::SC + THREADS - 1) / THREADS; // chunks of a thread
   static constexpr bool kIdle = ROWS * T::SC < THREADS;            // a small tile leaves some threads without one
   static_assert(kIdle || ROWS * T::SC % THREADS == 0, "whole turns");
-  u32x4 v[N];
   static __device__ __forceinline__ int row(int k) { return ((int)threadIdx.x + k * THREADS) / T::SC; }
   static __device__ __forceinline__ int chunk() { return (int)threadIdx.x % T::SC; } // the same of every row
+};
+template <int DT, int DP, int ROWS, int THREADS, int TURNS = Share<DT, DP, ROWS, THREADS>::N>
+struct Stage : Share<DT, DP, ROWS, THREADS> {
+  using S = Share<DT, DP, ROWS, THREADS>;
+  using T = typename S::T;
+  using S::chunk;
+  using S::row;
+  u32x4 v[TURNS];
   // rows r0 on, those below `end` present; at(r) is a row's first element
-  template <class At> __device__ __forceinline__ void load(const void *p, int r0, int end, int D, At at) {
+  template <class At> __device__ __forceinline__ void load(const void *p, int r0, int end, int D, At at, int k0 = 0) {
     const int e = chunk() * T::V;
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = u32x4{0, 0, 0, 0};
-    if (kIdle && row(0) >= ROWS) return;
+    for (int k = 0; k < TURNS; ++k) v[k] = u32x4{0, 0, 0, 0};
+    if (S::kIdle && row(0) >= ROWS) return;
     if (e + T::V <= D && r0 + ROWS <= end) { // nothing to leave out: requests without a branch between them
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        v[k] = *reinterpret_cast<const typename El<DT>::vec *>((const typename El<DT>::bits *)p + at(r0 + row(k)) + e);
+      for (int k = 0; k < TURNS; ++k)
+        v[k] = *reinterpret_cast<const typename El<DT>::vec *>((const typename El<DT>::bits *)p + at(r0 + row(k0 + k)) + e);
     } else if (e < D) {
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (r0 + row(k) < end) v[k] = load_chunk<DT>(p, at(r0 + row(k)), chunk(), D, true);
+      for (int k = 0; k < TURNS; ++k)
+        if (r0 + row(k0 + k) < end) v[k] = load_chunk<DT>(p, at(r0 + row(k0 + k)), chunk(), D, true);
     }
   }
-  __device__ __forceinline__ void store(char *tile) const {
-    if ((T::kChunks == T::SC || chunk() < T::kChunks) && !(kIdle && row(0) >= ROWS)) {
+  __device__ __forceinline__ void store(char *tile, int k0 = 0) const {
+    if ((T::kChunks == T::SC || chunk() < T::kChunks) && !(S::kIdle && row(0) >= ROWS)) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) *reinterpret_cast<u32x4 *>(tile + T::place(row(k), chunk())) = v[k];
+      for (int k = 0; k < TURNS; ++k) *reinterpret_cast<u32x4 *>(tile + T::place(row(k0 + k), chunk())) = v[k];
     }
   }
 };
+// Tiles of consecutive rows of whole chunks (D a multiple of one), one after the
+// other, at a stride: a thread's place moves by a tile, nothing is multiplied on
+// the way.  Rows past the end are zeros (what is requested in their place is the
+// last row); chunks past D are not stored: clear_tiles puts zeros there once.
+template <int DT, int DP, int ROWS, int THREADS> struct RowStage {
+  using S = Share<DT, DP, ROWS, THREADS>;
+  using T = typename S::T;
+  static constexpr int N = S::N;
+  typedef typename El<DT>::bits bits;
+  u32x4 v[N];
+  const bits *at;     // of this thread, in the next tile
+  int64_t stride;
+  bool any;           // the thread has a chunk of every row
+  __device__ __forceinline__ void start(const void *p, int64_t base, int64_t row_stride, int r0, int D) {
+    any = S::chunk() * T::V < D && !(S::kIdle && S::row(0) >= ROWS);
+    stride = row_stride;
+    at = (const bits *)p + base + (int64_t)(r0 + (any ? S::row(0) : 0)) * stride + (any ? S::chunk() * T::V : 0);
+  }
+  __device__ __forceinline__ void load(int r0, int end) { // rows r0 on, those below `end` (r0 is one) present
+    const int left = end - r0;
+    if (left >= ROWS) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        v[k] = *reinterpret_cast<const typename El<DT>::vec *>(at + k * (THREADS / T::SC) * stride);
+    } else {
+      const int mine = any ? S::row(0) : 0; // (at's row)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int r = mine + k * (THREADS / T::SC);
+        const u32x4 w = *reinterpret_cast<const typename El<DT>::vec *>(at + (int64_t)(min(r, left - 1) - mine) * stride);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k][i] = r < left ? w[i] : 0;
+      }
+    }
+    at += ROWS * stride;
+  }
+  __device__ __forceinline__ void store(char *lds) const {
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) *reinterpret_cast<u32x4 *>(lds + T::place(S::row(k), S::chunk())) = v[k];
+    }
+  }
+};
+// zeros in `bytes` of LDS where heads are shorter than what the kernel is built for
+template <int THREADS> __device__ __forceinline__ void clear_tiles(char *lds, int bytes, bool shorter) {
+  if (shorter) {
+    for (int i = threadIdx.x * 16; i < bytes; i += THREADS * 16) *reinterpret_cast<u32x4 *>(lds + i) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+  }
+}
 
-// a block's work: its unit (sample and key head), its tile of the unit's rows or
-// keys and its split of the other side.  Blocks go to the 8 XCDs in turn; each
-// of those takes a run of consecutive work, so that the blocks which read the
-// same keys (rows) share an L2.
+// a whole tile now, a few chunks of a thread at a time
+template <int DT, int DP, int ROWS, int THREADS, class At>
+__device__ __forceinline__ void stage_tile(char *tile, const void *p, int r0, int end, int D, At at) {
+  constexpr int N = Share<DT, DP, ROWS, THREADS>::N, TURNS = N < 8 ? N : 8;
+#pragma unroll 1
+  for (int k0 = 0; k0 < N; k0 += TURNS) {
+    Stage<DT, DP, ROWS, THREADS, TURNS> st;
+    st.load(p, r0, end, D, at, k0);
+    st.store(tile, k0);
+  }
+}
+
+// A block's work: its unit (sample and key head), its tile of the unit's rows or
+// keys and its split of the other side.  Blocks go to the 8 XCDs in turn: units in
+// sets of 8, a unit of them to each, so that the blocks that read the same keys
+// (rows) share an L2, and unlike lengths spread.  In a unit the tiles with most to
+// do come first (causal order leaves the last rows, or the first keys, the most).
 struct Work {
   uint32_t unit;
   int b, hk, tile, split;
 };
-__device__ __forceinline__ Work work_of(const AttnArgs &a) {
-  const uint32_t id = blockIdx.x, xcd = id & 7, per = a.blocks >> 3, more = a.blocks & 7;
-  const uint32_t w = xcd * per + min(xcd, more) + (id >> 3);
-  const uint32_t s = fdiv(w, a.div_tiles), u = fdiv(s, a.div_splits);
+template <bool LAST_FIRST> __device__ __forceinline__ Work work_of(const AttnArgs &a) {
+  const uint32_t set = fdiv(blockIdx.x, a.div_set), first = set * 8, in = blockIdx.x - set * a.div_set.d;
+  const uint32_t of = min(8u, a.units - first), rest = in / of;
   Work k;
-  k.tile = (int)(w - s * a.div_tiles.d);
-  k.split = (int)(s - u * a.div_splits.d);
-  k.unit = a.unit0 + u;
+  k.unit = a.unit0 + first + (in - rest * of);
+  k.tile = (int)fdiv(rest, a.div_splits);
+  k.split = (int)rest - k.tile * (int)a.div_splits.d;
+  if (LAST_FIRST) k.tile = a.tiles - 1 - k.tile;
   k.b = (int)fdiv(k.unit, a.div_Hk);
   k.hk = (int)(k.unit - (uint32_t)k.b * a.div_Hk.d);
   return k;

@@ -27,8 +27,8 @@ struct AttnArgs {
   int32_t causal;
   int32_t tiles, splits;  // of a unit (sample and key head)
   int32_t span;           // keys (rows, for key gradients) of a split, whole tiles
-  FastDiv div_group, div_tiles, div_splits, div_Hk;
-  uint32_t unit0;         // first unit of this launch
+  FastDiv div_group, div_set, div_splits, div_Hk; // (set: the blocks of 8 units)
+  uint32_t unit0, units;  // of this launch
   uint32_t blocks;
   float scale, scale2;    // of the scores, and that times log2(e)
 };
@@ -40,19 +40,35 @@ inline int attn_padded(int64_t d) { // head lengths that kernels are built for
   return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : d <= 128 ? 128 : d <= 160 ? 160 : d <= 192 ? 192 : 256;
 }
 
+// heads for which forward has blocks of twice as many waves too
+__host__ __device__ constexpr bool attn_wide(int elem_bytes, int padded) {
+  return elem_bytes == 2 && padded >= 96 && padded <= 192;
+}
+
+// heads for which the gradients' kernels form the next tile's scores while they
+// use this one's
+__host__ __device__ constexpr bool attn_pipelined(int elem_bytes, int padded) {
+  return elem_bytes == 2 && padded <= 192;
+}
+
+// columns of 32 rows of a wave of those for dq, at most (their registers)
+__host__ __device__ constexpr int attn_columns(int padded) { return padded <= 128 ? 2 : 1; }
+
 // keys of a block of the key gradients: 32 a wave, or a pair of waves where a
 // head's two halves go to two of them
 __host__ __device__ constexpr bool attn_paired(int elem_bytes, int padded) { return padded * elem_bytes > (elem_bytes == 2 ? 384 : 640); }
 
 } // namespace sb
 
-// waves: 1 or kAttnWaves, each with 32 rows of a tile (32 keys, for key gradients)
+// waves: 1, kAttnWaves or (forward, attn_wide) twice that, each with 32 rows of a
+// tile; wave_rows, whole: as launch_dq and launch_dkv say
 hipError_t sb_launch_attention(const sb::AttnArgs &a, int dtype, int waves, hipStream_t st);
-hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, hipStream_t st);
-hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, hipStream_t st);
-// joins the splits of the forward pass, or adds up those of a gradient: `count`
-// rows of D of the partial results at a.part, to out (a.out's layout with
-// `heads` of a group)
+hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int wave_rows, hipStream_t st);
+hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, int whole, hipStream_t st);
+// joins the splits of the forward pass
 hipError_t sb_launch_attention_join(const sb::AttnArgs &a, int dtype, hipStream_t st);
-hipError_t sb_launch_attention_sum(const sb::AttnArgs &a, const sb::AttnHeads &out, const float *part, int64_t len,
-                                   int group, int dtype, hipStream_t st);
+// adds up a.splits splits of n (1 or 2) gradients of the same shape: partial
+// results [n][splits][units][len][D] to out[k], rows r of a unit at position
+// r / group of head hk * group + r % group
+hipError_t sb_launch_attention_sum(const sb::AttnArgs &a, const sb::AttnHeads *out, int n, int64_t len, int group,
+                                   int dtype, hipStream_t st);

@@ -102,6 +102,46 @@ def test_many_rows_over_few_keys(sb, dtype, size, causal):
     check_backward(sb, q, k, v, g, f"{size} {dtype}", causal=causal)
 
 
+MANY = [
+    # samples and heads that fill the chip: the kernels for many rows
+    (16, 40, 50, 32, 32, 128), (16, 70, 33, 32, 32, 96), (8, 65, 130, 64, 64, 192), (16, 33, 64, 32, 32, 160),
+    (8, 90, 70, 96, 32, 104), (9, 300, 140, 32, 32, 64), (32, 50, 40, 24, 8, 128), (16, 257, 20, 16, 16, 32),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("size", MANY, ids=str)
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_rows(sb, dtype, size, causal):
+    q, k, v, g = draw(17, *size, dtype)
+    check_forward(sb, q, k, v, f"{size} {dtype}", causal=causal)
+    check_backward(sb, q, k, v, g, f"{size} {dtype}", causal=causal)
+
+
+@pytest.mark.parametrize("size", [(16, 40, 50, 32, 32, 128), (9, 300, 140, 32, 32, 64), (8, 90, 70, 96, 32, 104)], ids=str)
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_rows_of_unlike_lengths(sb, size, causal):
+    q, k, v, g = draw(18, *size, "bf16")
+    gen = torch.Generator().manual_seed(19)
+    ql = torch.randint(0, size[1] + 1, (size[0],), generator=gen).tolist()
+    kl = torch.randint(0, size[2] + 1, (size[0],), generator=gen).tolist()
+    ql[0], kl[0], kl[1] = 0, size[2], 0
+    kept = [t.clone() for t in (q, k, v, g)]
+    for b in range(size[0]):
+        q[b, ql[b]:] = g[b, ql[b]:] = float("nan")
+        k[b, kl[b]:] = v[b, kl[b]:] = float("inf")
+    how = dict(causal=causal, query_lengths=lens(ql), key_lengths=lens(kl))
+    scale = size[-1] ** -0.5
+    (out, lse), tol = ref.forward(*kept[:3], scale, causal, ql, kl)
+    got, got_lse = sb.attention(q, k, v, return_lse=True, **how)
+    assert_near(got, out, tol[0], "out")
+    assert_near(got_lse, lse, tol[1], "lse")
+    out, lse = torch.from_numpy(out).to(q.dtype).cuda(), torch.from_numpy(lse).float().cuda()
+    want, tol = ref.backward(kept[3], *kept[:3], out, lse, scale, causal, ql, kl)
+    for name, a, w, t in zip(("dq", "dk", "dv"), sb.attention_backward(g, q, k, v, out, lse, **how), want, tol):
+        assert_near(a, w, t, name)
+
+
 LENGTHS = [
     # batch of 4: query lengths, key lengths
     (None, [0, 1, 64, 150]), ([0, 1, 33, 90], None), ([90, 5, 64, 0], [150, 70, 0, 32]), ([90, 40, 1, 2], [20, 40, 9, 1]),
@@ -250,7 +290,7 @@ def test_gradient_against_differences(sb):
 
 @pytest.mark.parametrize("dtype", DT)
 def test_same_bits_every_time(sb, dtype):
-    for size in ((2, 1, 3000, 8, 2, 128), (1, 300, 260, 4, 2, 64)):
+    for size in ((2, 1, 3000, 8, 2, 128), (1, 300, 260, 4, 2, 64), (16, 60, 70, 32, 32, 128)):
         q, k, v, g = draw(13, *size, dtype)
         out, lse = sb.attention(q, k, v, return_lse=True)
         grads = sb.attention_backward(g, q, k, v, out, lse)

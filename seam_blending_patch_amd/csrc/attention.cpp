@@ -107,7 +107,8 @@ int check_distinct(const Heads &out) {
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// How a kernel's work is cut: blocks of `waves` waves with 32 rows (keys) each,
+// How a kernel's work is cut (causal gradients into more splits than blocks alone
+// would need, for the longest tiles are twice the mean): blocks of `waves` waves with 32 rows (keys) each,
 // the other side in splits where that alone does not fill the chip.
 struct Plan {
   int waves;
@@ -130,8 +131,8 @@ Plan cut(int64_t units, int64_t own, int64_t per_block, int64_t along, int waves
 
 bool whole_chunks(const sb::AttnArgs &a, int dtype) { return a.D % (16 / sb::elem_bytes(dtype)) == 0; }
 
-Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward) {
-  const int64_t cus = sb_cu_count(), units = (int64_t)a.B * a.Hk;
+Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward, bool causal) {
+  const int64_t cus = sb_cu_count(), want = !forward && causal ? 3 * cus : cus, units = (int64_t)a.B * a.Hk;
   const int eb = sb::elem_bytes(dtype), padded = sb::attn_padded(a.D), wide = 2 * sb::kAttnWaves;
   const bool whole = whole_chunks(a, dtype);
   if (a.rows <= 32) return cut(units, a.rows, 32, a.Lk, 1, 8 * cus, 128);
@@ -140,22 +141,23 @@ Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward) {
   Plan p;
   if (!forward && whole && sb::attn_pipelined(eb, padded)) {
     const int64_t rows = 64 * sb::kAttnWaves;
-    if (sb::attn_columns(padded) > 1 && units * ((a.rows + rows - 1) / rows) >= cus) {
+    if (sb::attn_columns(padded) > 1 && 2 * units * ((a.rows + rows - 1) / rows) >= 3 * cus) {
       p = cut(units, a.rows, rows, a.Lk, sb::kAttnWaves, 1, a.Lk + 1);
       p.wave_rows = 64;
       return p;
     }
-    p = cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, cus, 512);
+    p = cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, want, 512);
     p.wave_rows = 32;
     return p;
   }
-  return cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, cus, 512);
+  return cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, want, 512);
 }
 
-Plan plan_keys(const sb::AttnArgs &a, int dtype) {
+Plan plan_keys(const sb::AttnArgs &a, int dtype, bool causal) {
   const int64_t cus = sb_cu_count(), units = (int64_t)a.B * a.Hk;
   const bool paired = sb::attn_paired(sb::elem_bytes(dtype), sb::attn_padded(a.D));
-  return cut(units, a.Lk, 32 * sb::kAttnWaves / (paired ? 2 : 1), a.rows, sb::kAttnWaves, cus, 512);
+  return cut(units, a.Lk, 32 * sb::kAttnWaves / (paired ? 2 : 1), a.rows, sb::kAttnWaves, causal ? 3 * cus : cus,
+             causal ? 256 : 512);
 }
 
 int64_t rows_part(const sb::AttnArgs &a, const Plan &p) { // floats of the splits' rows
@@ -170,11 +172,13 @@ int64_t keys_part(const sb::AttnArgs &a, const Plan &p) {
 int64_t delta_floats(const sb::AttnArgs &a) { return up((int64_t)a.B * a.Hk * a.rows, 4); }
 
 int64_t forward_floats(const sb::AttnArgs &a, int dtype) {
-  const Plan p = plan_rows(a, dtype, true);
+  const Plan p = plan_rows(a, dtype, true, a.causal);
   return rows_part(a, p) + rows_part_lse(a, p);
 }
+// (the workspace's size does not go by causal order: the larger need)
 int64_t backward_floats(const sb::AttnArgs &a, int dtype) {
-  return delta_floats(a) + std::max(rows_part(a, plan_rows(a, dtype, false)), keys_part(a, plan_keys(a, dtype)));
+  return delta_floats(a) + std::max({rows_part(a, plan_rows(a, dtype, false, false)), rows_part(a, plan_rows(a, dtype, false, true)),
+                                     keys_part(a, plan_keys(a, dtype, false)), keys_part(a, plan_keys(a, dtype, true))});
 }
 
 int check_workspace(const void *workspace, size_t bytes, int64_t need) {
@@ -190,7 +194,8 @@ template <class F> hipError_t over_units(sb::AttnArgs a, const Plan &p, F launch
   a.tiles = (int32_t)p.tiles;
   a.splits = (int32_t)p.splits;
   a.span = (int32_t)p.span;
-  a.div_set = sb::make_fastdiv((uint32_t)(8 * p.tiles * p.splits));
+  a.set = a.q_len || a.k_len ? 1 : 8;
+  a.div_set = sb::make_fastdiv((uint32_t)(a.set * p.tiles * p.splits));
   a.div_splits = sb::make_fastdiv((uint32_t)p.splits);
   const int64_t units = (int64_t)a.B * a.Hk, each = p.tiles * p.splits, most = std::max<int64_t>(1, sb::kMaxBlocksX / each);
   for (int64_t u = 0; u < units; u += most) {
@@ -244,8 +249,14 @@ extern "C" int attention_forward(const void *q, const int64_t q_stride[3], const
   if ((rc = check_workspace(workspace, workspace_bytes, forward_floats(a, dtype) * (int64_t)sizeof(float)))) return rc;
   a.causal = causal != 0;
   a.lse = lse;
-  const Plan p = plan_rows(a, dtype, true);
+  const Plan p = plan_rows(a, dtype, true, a.causal);
   const hipStream_t st = (hipStream_t)stream;
+  // Causal tiles that are resident all at once, two blocks to a CU: the longest
+  // beside the shortest (2049 tokens, 16 heads of 80 in 4 groups of two samples
+  // fp32: 288 us, longest first 336).
+  const int64_t units = (int64_t)a.B * a.Hk, beside = sb_cu_count() / units;
+  if (a.causal && !a.q_len && !a.k_len && p.waves == sb::kAttnWaves && p.splits == 1 && units <= 8 && p.tiles > beside && 2 * p.tiles <= 5 * beside)
+    a.beside = (int32_t)beside;
   if (p.splits > 1) {
     a.part = (float *)workspace;
     a.part_lse = a.part + rows_part(a, p);
@@ -299,14 +310,14 @@ extern "C" int attention_backward(const void *dout, const int64_t dout_stride[3]
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (a.Lq > 0) {
-    const Plan p = plan_rows(a, dtype, false);
+    const Plan p = plan_rows(a, dtype, false, a.causal);
     a.part = p.splits > 1 ? part : nullptr;
     e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, p.wave_rows, st); });
     a.splits = (int32_t)p.splits;
     if (e == hipSuccess && p.splits > 1) e = sb_launch_attention_sum(a, &a.dq, 1, a.rows, a.group, dtype, st);
   }
   if (e == hipSuccess && a.Lk > 0) {
-    const Plan p = plan_keys(a, dtype);
+    const Plan p = plan_keys(a, dtype, a.causal);
     a.part = p.splits > 1 ? part : nullptr;
     e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dkv(b, dtype, whole_chunks(a, dtype), st); });
     a.splits = (int32_t)p.splits;

@@ -254,19 +254,23 @@ __device__ __forceinline__ void stage_tile(char *tile, const void *p, int r0, in
 // A block's work: its unit (sample and key head), its tile of the unit's rows or
 // keys and its split of the other side.  Blocks go to the 8 XCDs in turn: units in
 // sets of 8, a unit of them to each, so that the blocks that read the same keys
-// (rows) share an L2, and unlike lengths spread.  In a unit the tiles with most to
+// (rows) share an L2; one by one, their tiles over the XCDs, where lengths differ.  In a unit the tiles with most to
 // do come first (causal order leaves the last rows, or the first keys, the most).
 struct Work {
   uint32_t unit;
   int b, hk, tile, split;
 };
 template <bool LAST_FIRST> __device__ __forceinline__ Work work_of(const AttnArgs &a) {
-  const uint32_t set = fdiv(blockIdx.x, a.div_set), first = set * 8, in = blockIdx.x - set * a.div_set.d;
-  const uint32_t of = min(8u, a.units - first), rest = in / of;
+  const uint32_t set = fdiv(blockIdx.x, a.div_set), first = set * a.set, in = blockIdx.x - set * a.div_set.d;
+  const uint32_t of = min(a.set, a.units - first), rest = in / of;
   Work k;
   k.unit = a.unit0 + first + (in - rest * of);
   k.tile = (int)fdiv(rest, a.div_splits);
   k.split = (int)rest - k.tile * (int)a.div_splits.d;
+  if (a.beside && k.tile >= a.beside) { // the second blocks of the CUs get longer as the first get shorter
+    const int over = max(a.tiles - 2 * a.beside, 0); // (the shortest tiles of all, for whoever is done first)
+    k.tile = k.tile < 2 * a.beside ? a.tiles - 1 - over - (k.tile - a.beside) : a.tiles - over + (k.tile - 2 * a.beside);
+  }
   if (LAST_FIRST) k.tile = a.tiles - 1 - k.tile;
   k.b = (int)fdiv(k.unit, a.div_Hk);
   k.hk = (int)(k.unit - (uint32_t)k.b * a.div_Hk.d);

@@ -44,14 +44,39 @@ int read_shape(const int64_t *shape, int64_t groups, int dtype, sb::ChanArgs &a)
   a.RB = sb::kChanThreads / a.CV;
   a.div_CV = sb::make_fastdiv((uint32_t)a.CV);
   a.div_slabs = sb::make_fastdiv((uint32_t)a.slabs);
-  // enough blocks for the chip, each with a batch of every thread at least
-  const int64_t least = (int64_t)a.RB * sb::kChanBatch, want = 8 * (int64_t)sb_cu_count();
-  const int64_t most = std::max<int64_t>(1, want / std::max<int64_t>(1, N * a.slabs));
-  const int64_t chunks = std::max<int64_t>(1, std::min(most, (S + least - 1) / least));
-  a.chunk = (int32_t)std::min<int64_t>(up((S + chunks - 1) / chunks, a.RB), sb::kMaxExtent - 1);
-  a.chunks = a.chunk ? (int32_t)((S + a.chunk - 1) / a.chunk) : 0;
+  // Blocks of the pass that sums: two a CU where each thread has 4 positions at
+  // least, for each leaves partials that a merge reads (512 x 512 x 256 of two
+  // samples fp16 with 2, 4 and 8 a CU: 164, 172 and 174 us in all; 256 x 256 x 512
+  // bf16 backward 69, 76 and 93).
+  const int64_t least = (int64_t)a.RB * 4, cus = sb_cu_count();
+  const auto cut = [&](int64_t want, int32_t &chunk, int32_t &chunks) {
+    const int64_t most = std::max<int64_t>(1, want / std::max<int64_t>(1, N * a.slabs));
+    const int64_t n = std::max<int64_t>(1, std::min(most, (S + least - 1) / least));
+    chunk = (int32_t)std::min<int64_t>(up((S + n - 1) / n, a.RB), sb::kMaxExtent - 1);
+    chunks = chunk ? (int32_t)((S + chunk - 1) / chunk) : 0;
+  };
+  cut(2 * cus, a.chunk, a.chunks);
+  cut(16 * cus, a.apply_chunk, a.apply_chunks); // (leaves none)
   a.div_chunks = sb::make_fastdiv((uint32_t)std::max(a.chunks, 1));
+  a.far = N * S * C * sb::elem_bytes(dtype) >= (int64_t)256 << 20;
   return SB_OK;
+}
+
+// Groups for a block to hold: the fewest that fill whole vectors, where `vectors`
+// of each of `threads` threads have room for their positions.  Then the merge's partials are one chunk
+// of a sample (for the weights' gradients, which add up over samples).
+void hold(sb::ChanArgs &a, int dtype, int64_t threads, int64_t vectors) {
+  const int64_t v = 16 / sb::elem_bytes(dtype);
+  int64_t sg = 1;
+  while (sg <= v && sg * a.Cg % v != 0) ++sg;
+  if (sg > v || a.G % sg != 0) return;
+  const int64_t cv = sg * a.Cg / v;
+  if (cv > threads || (a.S + threads / cv - 1) / (threads / cv) > vectors) return; // (positions of a turn, turns)
+  a.sg = (int32_t)sg;
+  a.CS = (int32_t)(sg * a.Cg);
+  a.div_CVs = sb::make_fastdiv((uint32_t)cv);
+  a.chunks = 1;
+  a.chunk = a.S;
 }
 
 int read_positions(const char *name, const void *p, const int64_t *stride, const sb::ChanArgs &a, int dtype,
@@ -137,6 +162,7 @@ extern "C" int group_norm_forward(const void *x, const int64_t x_stride[2], cons
   a.eps = eps;
   a.part = (float *)workspace;
   a.stats = stats ? stats : a.part + part_floats(a);
+  hold(a, dtype, sb::kHeldThreads, sb::kHeldVectors);
   const hipError_t e = sb_launch_channels_norm(a, dtype, weight_dtype, (hipStream_t)stream);
   if (e != hipSuccess) return failf(SB_ELAUNCH, "group norm launch failed: %s", hipGetErrorString(e));
   return SB_OK;
@@ -176,6 +202,9 @@ extern "C" int group_norm_backward(const void *dy, const int64_t dy_stride[2], c
   a.stats = const_cast<float *>(stats); // only read
   a.part = (float *)workspace;
   a.coef = a.part + part_floats(a);
+  a.apply_chunk = a.chunk;
+  a.apply_chunks = a.chunks;
+  if (a.N) hold(a, dtype, sb::kHeldBackThreads, sb::kHeldBackVectors);
   const hipError_t e = sb_launch_channels_norm_backward(a, dtype, weight_dtype, (hipStream_t)stream);
   if (e != hipSuccess) return failf(SB_ELAUNCH, "group norm launch failed: %s", hipGetErrorString(e));
   return SB_OK;

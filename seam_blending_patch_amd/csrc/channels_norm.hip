@@ -19,7 +19,7 @@ struct Place {
   bool on;              // (the threads that are left over when a turn's positions do not fill the block are off)
 };
 __device__ __forceinline__ Place place_of(const ChanArgs &a) {
-  const uint32_t b = a.block0 + blockIdx.x, t = fdiv(b, a.div_slabs), slab = b - t * a.div_slabs.d;
+  const uint32_t at = a.block0 + blockIdx.x, b = a.last ? a.last - at : at, t = fdiv(b, a.div_slabs), slab = b - t * a.div_slabs.d;
   Place p;
   p.n = (int)fdiv(t, a.div_chunks);
   p.chunk = (int)(t - (uint32_t)p.n * a.div_chunks.d);
@@ -154,41 +154,66 @@ __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
   }
 }
 
-// a block's sum of one double each, in every thread
-__device__ __forceinline__ double block_sum(double v, double *lds) {
+// a block's sums of two doubles each, in every thread
+__device__ __forceinline__ void block_sums(double &u, double &v, double (*lds)[2]) {
 #pragma unroll
-  for (int k = 32; k; k >>= 1) v += __shfl_xor(v, k);
+  for (int k = 32; k; k >>= 1) {
+    u += __shfl_xor(u, k);
+    v += __shfl_xor(v, k);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    lds[threadIdx.x >> 6][0] = u;
+    lds[threadIdx.x >> 6][1] = v;
+  }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kChanThreads / 64; ++w) s += lds[w];
-  return s;
+  u = v = 0.0;
+  for (int w = 0; w < (int)blockDim.x / 64; ++w) {
+    u += lds[w][0];
+    v += lds[w][1];
+  }
 }
 
-// A group's chunks and channels merged: a block to a group.  64 bits: the sums
-// are short and cost nothing.
-template <int DT> __global__ __launch_bounds__(kChanThreads) void merge_kernel(const ChanArgs a) {
-  __shared__ double lds[kChanThreads / 64];
-  const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G, items = a.chunks * a.Cg;
+// Calls f(chunk, channel of the group, first, second) with a group's partials, 8 of
+// a thread on their way at a time.
+template <class F> __device__ __forceinline__ void over_partials(const ChanArgs &a, int n, int g, F f) {
   const float *part = a.part + (int64_t)n * a.chunks * 2 * a.C + g * a.Cg;
+  const int items = a.chunks * a.Cg;
+  for (int i0 = threadIdx.x; i0 < items; i0 += 8 * kMergeThreads) {
+    float u[8], v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = min(i0 + j * kMergeThreads, items - 1), chunk = (int)fdiv((uint32_t)i, a.div_Cg);
+      const float *at = part + (int64_t)chunk * 2 * a.C + (i - chunk * a.Cg);
+      u[j] = at[0];
+      v[j] = at[a.C];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kMergeThreads;
+      if (i < items) {
+        const int chunk = (int)fdiv((uint32_t)i, a.div_Cg);
+        f(chunk, i - chunk * a.Cg, u[j], v[j]);
+      }
+    }
+  }
+}
+
+// A group's chunks and channels merged: a block to a group.  In 64 bits the merge of
+// many sets may be taken by sums of squares: the means are of what is left of the
+// group's first value.
+template <int DT> __global__ __launch_bounds__(kMergeThreads) void merge_kernel(const ChanArgs a) {
+  __shared__ double lds[kMergeThreads / 64][2];
+  const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G;
   const double total = (double)a.S * a.Cg;
-  const auto count_of = [&](int chunk) { return (double)(min(a.S, (chunk + 1) * a.chunk) - chunk * a.chunk); };
-  double s = 0.0;
-  for (int i = threadIdx.x; i < items; i += kChanThreads) {
-    const int chunk = (int)fdiv((uint32_t)i, a.div_Cg), c = i - chunk * a.Cg;
-    s += count_of(chunk) * (double)part[(int64_t)chunk * 2 * a.C + c];
-  }
-  const double mean = block_sum(s, lds) / total;
-  s = 0.0;
-  for (int i = threadIdx.x; i < items; i += kChanThreads) {
-    const int chunk = (int)fdiv((uint32_t)i, a.div_Cg), c = i - chunk * a.Cg;
-    const double d = (double)part[(int64_t)chunk * 2 * a.C + c] - mean;
-    s += (double)part[((int64_t)chunk * 2 + 1) * a.C + c] + count_of(chunk) * d * d;
-  }
-  const double var = block_sum(s, lds) / total;
+  double s = 0.0, t = 0.0;
+  over_partials(a, n, g, [&](int chunk, int, float mean, float m2) {
+    const double count = min(a.S, (chunk + 1) * a.chunk) - chunk * a.chunk, m = mean;
+    s += count * m;
+    t += (double)m2 + count * m * m;
+  });
+  block_sums(s, t, lds);
   if (threadIdx.x == 0) {
+    const double mean = s / total, var = fmax(t / total - mean * mean, 0.0);
     float *to = a.stats + ((int64_t)n * a.G + g) * 3;
     to[0] = group_shift<DT>(a, n, g);
     to[1] = (float)mean;
@@ -220,7 +245,7 @@ template <int DT, int WT, Cover C> struct Channels {
   __device__ __forceinline__ float h(float x, int k) const { return ((x - K[k]) - m[k]) * r[k]; }
 };
 
-template <int DT, int WT, Cover C, bool SILU>
+template <int DT, int WT, Cover C, bool SILU, bool FAR>
 __global__ __launch_bounds__(kChanThreads) void apply_kernel(const ChanArgs a) {
   constexpr int V = kVec<DT>, R = kChanBatch;
   const Place p = place_of(a);
@@ -247,7 +272,7 @@ __global__ __launch_bounds__(kChanThreads) void apply_kernel(const ChanArgs a) {
           const float z = __builtin_fmaf(ch.h(f[k], k), ch.gamma[k], ch.beta[k]);
           f[k] = SILU ? z * logistic(z) : z;
         }
-        store_row<DT, C>(a.out, to + j * so, e, a.C, pack<DT, 16>(f));
+        store_row<DT, C, FAR>(a.out, to + j * so, e, a.C, pack<DT, 16>(f));
       }
   }
 }
@@ -340,22 +365,21 @@ __global__ __launch_bounds__(kChanThreads) void sums_kernel(const ChanArgs a) {
   }
 }
 
-// The sums over a group (first N G blocks: means of gamma g and gamma g h), and
-// over the samples by channel (a wave to a channel: dbeta and dgamma).
-template <int WT> __global__ __launch_bounds__(kChanThreads) void gather_kernel(const ChanArgs a) {
-  __shared__ double lds[kChanThreads / 64];
+// The sums over a group (first N G blocks: means of gamma g and gamma g h), and by
+// channel over the samples (a block to 64 channels: dbeta and dgamma).
+template <int WT> __global__ __launch_bounds__(kMergeThreads) void gather_kernel(const ChanArgs a) {
+  constexpr int W = kMergeThreads / 64;
+  __shared__ double lds[W][2];
+  __shared__ double sums[W][2][64];
   if ((int)blockIdx.x < a.N * a.G) {
-    const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G, items = a.chunks * a.Cg;
-    const float *part = a.part + (int64_t)n * a.chunks * 2 * a.C + g * a.Cg;
+    const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G;
     double s = 0.0, t = 0.0;
-    for (int i = threadIdx.x; i < items; i += kChanThreads) {
-      const int chunk = (int)fdiv((uint32_t)i, a.div_Cg), c = i - chunk * a.Cg;
+    over_partials(a, n, g, [&](int, int c, float sg, float sh) {
       const double gamma = a.gamma ? (double)value_at<WT>(a.gamma, g * a.Cg + c) : 1.0;
-      s += gamma * (double)part[(int64_t)chunk * 2 * a.C + c];
-      t += gamma * (double)part[((int64_t)chunk * 2 + 1) * a.C + c];
-    }
-    s = block_sum(s, lds);
-    t = block_sum(t, lds);
+      s += gamma * (double)sg;
+      t += gamma * (double)sh;
+    });
+    block_sums(s, t, lds);
     if (threadIdx.x == 0) {
       const double total = (double)a.S * a.Cg;
       a.coef[blockIdx.x * 2] = (float)(s / total);
@@ -363,27 +387,40 @@ template <int WT> __global__ __launch_bounds__(kChanThreads) void gather_kernel(
     }
     return;
   }
-  const int c = ((int)blockIdx.x - a.N * a.G) * (kChanThreads / 64) + (threadIdx.x >> 6);
-  if (c >= a.C) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = ((int)blockIdx.x - a.N * a.G) * 64 + lane;
+  const int rows = a.N * a.chunks;
   double s = 0.0, t = 0.0;
-  for (int i = threadIdx.x & 63; i < a.N * a.chunks; i += 64) {
-    s += (double)a.part[(int64_t)i * 2 * a.C + c];
-    t += (double)a.part[((int64_t)i * 2 + 1) * a.C + c];
-  }
+  if (c < a.C) {
+    for (int i0 = wave; i0 < rows; i0 += 8 * W) {
+      float u[8], v[8];
 #pragma unroll
-  for (int k = 32; k; k >>= 1) {
-    s += __shfl_xor(s, k);
-    t += __shfl_xor(t, k);
+      for (int j = 0; j < 8; ++j) {
+        const float *at = a.part + (int64_t)min(i0 + j * W, rows - 1) * 2 * a.C + c;
+        u[j] = at[0];
+        v[j] = at[a.C];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * W < rows) {
+          s += (double)u[j];
+          t += (double)v[j];
+        }
+    }
   }
-  if ((threadIdx.x & 63) == 0) {
+  sums[wave][0][lane] = s;
+  sums[wave][1][lane] = t;
+  __syncthreads();
+  if (wave < 2 && c < a.C) { // the first wave dbeta, the second dgamma
+    double sum = 0.0;
+    for (int w = 0; w < W; ++w) sum += sums[w][wave][lane];
     typedef typename El<WT>::bits bits;
-    if (a.dbeta) ((bits *)a.dbeta)[c] = (bits)narrow<WT>((float)s);
-    if (a.dgamma) ((bits *)a.dgamma)[c] = (bits)narrow<WT>((float)t);
+    void *to = wave ? a.dgamma : a.dbeta;
+    if (to) ((bits *)to)[c] = (bits)narrow<WT>((float)sum);
   }
 }
 
 // dx = r (gamma g - mean(gamma g) - h mean(gamma g h))
-template <int DT, int WT, Cover C, bool SILU>
+template <int DT, int WT, Cover C, bool SILU, bool FAR>
 __global__ __launch_bounds__(kChanThreads) void gradient_kernel(const ChanArgs a) {
   constexpr int V = kVec<DT>, R = kChanBatch / 2;
   const Place p = place_of(a);
@@ -420,8 +457,225 @@ __global__ __launch_bounds__(kChanThreads) void gradient_kernel(const ChanArgs a
 #pragma unroll
         for (int k = 0; k < V; ++k)
           g[k] = ch.r[k] * (__builtin_fmaf(g[k], ch.gamma[k], -mg[k]) - h[k] * mh[k]);
-        store_row<DT, C>(a.out, to + j * so, e, a.C, pack<DT, 16>(g));
+        store_row<DT, C, FAR>(a.out, to + j * so, e, a.C, pack<DT, 16>(g));
       }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// groups that a block holds in registers
+// ---------------------------------------------------------------------------
+// A block's channels c0 .. c0 + CS of sample n; a thread has vector column col of
+// positions r, r + RB, ...
+struct Held {
+  int n, c0, r, col, RB;
+  bool on;
+  template <int THREADS> static __device__ __forceinline__ Held of(const ChanArgs &a) {
+    const int per = a.G / a.sg, cv = (int)a.div_CVs.d;
+    Held p;
+    p.n = blockIdx.x / per;
+    p.c0 = (blockIdx.x - p.n * per) * a.CS;
+    p.RB = THREADS / cv;
+    p.r = (int)fdiv(threadIdx.x, a.div_CVs);
+    p.col = threadIdx.x - p.r * cv;
+    p.on = p.r < p.RB;
+    return p;
+  }
+};
+
+// The values of K sums by channel of every thread, added up over the block for each
+// of its groups (at most 8): within a wave without memory, then over the waves.
+template <int K, int V, int THREADS>
+__device__ __forceinline__ void group_sums(int sg, const int (&group)[V], const float (&v)[K][V], float (*lds)[8][THREADS / 64],
+                                           float (*out)[8]) {
+  constexpr int W = THREADS / 64;
+  for (int g = 0; g < sg; ++g) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < V; ++k) s += group[k] == g ? v[j][k] : 0.0f;
+      s = lanes_sum<64>(s);
+      if ((threadIdx.x & 63) == 0) lds[j][g][threadIdx.x >> 6] = s;
+    }
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < sg * K) {
+    const int j = threadIdx.x / sg, g = threadIdx.x - j * sg;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += lds[j][g][w];
+    out[j][g] = s;
+  }
+  __syncthreads();
+}
+
+// N weights from channel e on
+template <int WT, int N> __device__ __forceinline__ void weights_of(const void *p, int e, float fill, float (&f)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) f[k] = p ? value_at<WT>(p, e + k) : fill;
+}
+
+template <int DT, int WT, bool SILU> __global__ __launch_bounds__(kHeldThreads) void held_kernel(const ChanArgs a) {
+  constexpr int V = kVec<DT>, NV = kHeldVectors;
+  __shared__ float lds[2][8][kHeldThreads / 64], sums[3][2][8];
+  const Held p = Held::of<kHeldThreads>(a);
+  const int e = p.c0 + (p.on ? p.col * V : 0), row = p.on ? p.r : 0;
+  Vec<16> v[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) // (positions past the end: the last one, left out below)
+    v[j] = load_part<DT>(a.x, p.n * a.sx.n + (int64_t)min(row + j * p.RB, a.S - 1) * a.sx.s + e, V);
+  float gamma[V], beta[V];
+  weights_of<WT, V>(a.gamma, e, 1.0f, gamma);
+  weights_of<WT, V>(a.beta, e, 0.0f, beta);
+  int group[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) group[k] = p.on ? (int)fdiv((uint32_t)(p.col * V + k), a.div_Cg) : 0;
+  const int turns = p.on && p.r < a.S ? (a.S - p.r + p.RB - 1) / p.RB : 0;
+  const float inv = 1.0f / ((float)a.S * (float)a.Cg);
+  // sums about a first mean, then its rounding error taken out
+  float s[1][V], d2[2][V], mean[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) s[0][k] = d2[0][k] = d2[1][k] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (j >= turns) continue;
+    float f[V];
+    unpack<DT, 16>(v[j], f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) s[0][k] += f[k];
+  }
+  group_sums<1, V, kHeldThreads>(a.sg, group, s, lds, sums[0]);
+#pragma unroll
+  for (int k = 0; k < V; ++k) mean[k] = sums[0][0][group[k]] * inv;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (j >= turns) continue;
+    float f[V];
+    unpack<DT, 16>(v[j], f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float d = f[k] - mean[k];
+      d2[0][k] += d;
+      d2[1][k] = __builtin_fmaf(d, d, d2[1][k]);
+    }
+  }
+  group_sums<2, V, kHeldThreads>(a.sg, group, d2, lds, sums[1]);
+  if ((int)threadIdx.x < a.sg) { // this thread's group is its own number
+    const float e1 = sums[1][0][threadIdx.x] * inv, var = fmaxf(sums[1][1][threadIdx.x] * inv - e1 * e1, 0.0f);
+    const float r = 1.0f / sqrtf(var + a.eps);
+    sums[2][0][threadIdx.x] = e1;
+    sums[2][1][threadIdx.x] = r;
+    float *to = a.stats + ((int64_t)p.n * a.G + (int)fdiv((uint32_t)p.c0, a.div_Cg) + threadIdx.x) * 3;
+    to[0] = sums[0][0][threadIdx.x] * inv;
+    to[1] = e1;
+    to[2] = r;
+  }
+  __syncthreads();
+  float rest[V], r[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    rest[k] = sums[2][0][group[k]];
+    r[k] = sums[2][1][group[k]];
+  }
+  const int64_t to = p.n * a.sout.n + (int64_t)p.r * a.sout.s + e;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (j >= turns) continue;
+    float f[V];
+    unpack<DT, 16>(v[j], f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float z = __builtin_fmaf(((f[k] - mean[k]) - rest[k]) * r[k], gamma[k], beta[k]);
+      f[k] = SILU ? z * logistic(z) : z;
+    }
+    store_part<DT>(a.out, to + (int64_t)j * p.RB * a.sout.s, V, pack<DT, 16>(f));
+  }
+}
+
+template <int DT, int WT, bool SILU>
+__global__ __launch_bounds__(kHeldBackThreads) void held_gradient_kernel(const ChanArgs a) {
+  constexpr int V = kVec<DT>, NV = kHeldBackVectors, THREADS = kHeldBackThreads, STRIDE = THREADS * V;
+  __shared__ float part[2 * STRIDE]; // sums of g and of g h by channel and position of a turn
+  __shared__ float lds[2][8][THREADS / 64], sums[2][8];
+  const Held p = Held::of<THREADS>(a);
+  const int e = p.c0 + (p.on ? p.col * V : 0), row = p.on ? p.r : 0;
+  Vec<16> v[NV], w[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) { // (positions past the end: the last one, left out below)
+    const int64_t at = min(row + j * p.RB, a.S - 1);
+    v[j] = load_part<DT>(a.x, p.n * a.sx.n + at * a.sx.s + e, V);
+    w[j] = load_part<DT>(a.dy, p.n * a.sdy.n + at * a.sdy.s + e, V);
+  }
+  Channels<DT, WT, WHOLE> ch;
+  ch.load(a, p.n, e);
+  int group[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) group[k] = p.on ? (int)fdiv((uint32_t)(p.col * V + k), a.div_Cg) : 0;
+  const int turns = p.on && p.r < a.S ? (a.S - p.r + p.RB - 1) / p.RB : 0;
+  float by[2][V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) by[0][k] = by[1][k] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (j >= turns) continue;
+    float g[V], h[V];
+    gradient_of<DT, WT, WHOLE, SILU>(ch, v[j], w[j], g, h);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      by[0][k] += g[k];
+      by[1][k] = __builtin_fmaf(g[k], h[k], by[1][k]);
+    }
+  }
+  const bool wanted = a.dgamma || a.dbeta;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    if (wanted && p.on) {
+      part[(p.col * V + k) * p.RB + p.r] = by[0][k];
+      part[STRIDE + (p.col * V + k) * p.RB + p.r] = by[1][k];
+    }
+    by[0][k] *= ch.gamma[k];
+    by[1][k] *= ch.gamma[k];
+  }
+  group_sums<2, V, THREADS>(a.sg, group, by, lds, sums);
+  const float inv = 1.0f / ((float)a.S * (float)a.Cg);
+  float mg[V], mh[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    mg[k] = sums[0][group[k]] * inv;
+    mh[k] = sums[1][group[k]] * inv;
+  }
+  const int64_t to = p.n * a.sout.n + (int64_t)p.r * a.sout.s + e;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (j >= turns) continue;
+    float g[V], h[V];
+    gradient_of<DT, WT, WHOLE, SILU>(ch, v[j], w[j], g, h);
+#pragma unroll
+    for (int k = 0; k < V; ++k) g[k] = ch.r[k] * (__builtin_fmaf(g[k], ch.gamma[k], -mg[k]) - h[k] * mh[k]);
+    store_part<DT>(a.out, to + (int64_t)j * p.RB * a.sout.s, V, pack<DT, 16>(g));
+  }
+  if (!wanted) return;
+  // the weights' gradients by channel (a wave to one): of a single sample, or its part
+  const int lane = threadIdx.x & 63;
+  for (int c = threadIdx.x >> 6; c < a.CS; c += THREADS / 64) {
+    float s = 0.0f, t = 0.0f;
+    for (int i = lane; i < p.RB; i += 64) {
+      s += part[c * p.RB + i];
+      t += part[STRIDE + c * p.RB + i];
+    }
+    s = lanes_sum<64>(s);
+    t = lanes_sum<64>(t);
+    if (lane != 0) continue;
+    const int at = p.c0 + c;
+    if (a.N == 1) {
+      typedef typename El<WT>::bits bits;
+      if (a.dbeta) ((bits *)a.dbeta)[at] = (bits)narrow<WT>(s);
+      if (a.dgamma) ((bits *)a.dgamma)[at] = (bits)narrow<WT>(t);
+    } else {
+      a.part[(int64_t)p.n * 2 * a.C + at] = s;
+      a.part[(int64_t)p.n * 2 * a.C + a.C + at] = t;
+    }
   }
 }
 
@@ -433,28 +687,58 @@ template <class F> void over_blocks(ChanArgs a, F launch) {
     launch(a, dim3((unsigned)(blocks - b < kMaxBlocksX ? blocks - b : kMaxBlocksX)));
   }
 }
+// The pass that writes goes backwards, so that it begins with what the first pass
+// read last and the caches still hold.
+ChanArgs backwards(ChanArgs a) {
+  a.chunk = a.apply_chunk;
+  a.chunks = a.apply_chunks;
+  a.div_chunks = make_fastdiv((uint32_t)a.chunks);
+  a.last = (uint32_t)((int64_t)a.N * a.chunks * a.slabs - 1);
+  return a;
+}
 
 template <int DT, int WT, Cover C, bool SILU> hipError_t forward(const ChanArgs &a, hipStream_t st) {
   const dim3 block(kChanThreads);
+  if constexpr (C == WHOLE) {
+    if (a.sg) {
+      hipLaunchKernelGGL((held_kernel<DT, WT, SILU>), dim3((unsigned)(a.N * (a.G / a.sg))), dim3(kHeldThreads), 0, st, a);
+      return hipGetLastError();
+    }
+  }
   over_blocks(a, [&](const ChanArgs &b, dim3 grid) { hipLaunchKernelGGL((stats_kernel<DT, C>), grid, block, 0, st, b); });
-  hipLaunchKernelGGL((merge_kernel<DT>), dim3((unsigned)(a.N * a.G)), block, 0, st, a);
-  over_blocks(a, [&](const ChanArgs &b, dim3 grid) {
-    hipLaunchKernelGGL((apply_kernel<DT, WT, C, SILU>), grid, block, 0, st, b);
+  hipLaunchKernelGGL((merge_kernel<DT>), dim3((unsigned)(a.N * a.G)), dim3(kMergeThreads), 0, st, a);
+  over_blocks(backwards(a), [&](const ChanArgs &b, dim3 grid) {
+    if (a.far) hipLaunchKernelGGL((apply_kernel<DT, WT, C, SILU, true>), grid, block, 0, st, b);
+    else hipLaunchKernelGGL((apply_kernel<DT, WT, C, SILU, false>), grid, block, 0, st, b);
   });
   return hipGetLastError();
 }
 
 template <int DT, int WT, Cover C, bool SILU> hipError_t backward(const ChanArgs &a, hipStream_t st) {
   const dim3 block(kChanThreads);
-  const unsigned waves = kChanThreads / 64, columns = a.dgamma || a.dbeta ? (a.C + waves - 1) / waves : 0;
+  const unsigned columns = a.dgamma || a.dbeta ? (a.C + 63) / 64 : 0;
+  if constexpr (C == WHOLE) {
+    if (a.sg) {
+      hipLaunchKernelGGL((held_gradient_kernel<DT, WT, SILU>), dim3((unsigned)(a.N * (a.G / a.sg))),
+                         dim3(kHeldBackThreads), 0, st, a);
+      if (a.N > 1 && columns) {
+        ChanArgs b = a;
+        b.G = 0; // (no groups to gather: channels alone)
+        hipLaunchKernelGGL((gather_kernel<WT>), dim3(columns), dim3(kMergeThreads), 0, st, b);
+      }
+      return hipGetLastError();
+    }
+  }
   over_blocks(a, [&](const ChanArgs &b, dim3 grid) {
     hipLaunchKernelGGL((sums_kernel<DT, WT, C, SILU>), grid, block, 0, st, b);
   });
   if (a.N * a.G + columns)
-    hipLaunchKernelGGL((gather_kernel<WT>), dim3((unsigned)(a.N * a.G) + columns), block, 0, st, a);
-  over_blocks(a, [&](const ChanArgs &b, dim3 grid) {
-    hipLaunchKernelGGL((gradient_kernel<DT, WT, C, SILU>), grid, block, 0, st, b);
-  });
+    hipLaunchKernelGGL((gather_kernel<WT>), dim3((unsigned)(a.N * a.G) + columns), dim3(kMergeThreads), 0, st, a);
+  if (a.N)
+    over_blocks(backwards(a), [&](const ChanArgs &b, dim3 grid) {
+      if (a.far) hipLaunchKernelGGL((gradient_kernel<DT, WT, C, SILU, true>), grid, block, 0, st, b);
+      else hipLaunchKernelGGL((gradient_kernel<DT, WT, C, SILU, false>), grid, block, 0, st, b);
+    });
   return hipGetLastError();
 }
 

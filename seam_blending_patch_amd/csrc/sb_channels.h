@@ -15,7 +15,11 @@ struct SampleStride {
   int64_t n, s;
 };
 
-constexpr int kChanThreads = 256; // of every block
+constexpr int kChanThreads = 256; // of the blocks that go along the positions
+constexpr int kMergeThreads = 1024;
+// A group (or the few that fill whole vectors) that a block holds in registers needs
+// one launch and is read once: vectors of a thread, forward and backward.
+constexpr int kHeldThreads = 1024, kHeldVectors = 8, kHeldBackThreads = 512, kHeldBackVectors = 10;
 constexpr int kChanBatch = 8;     // positions of a thread in flight
 
 struct ChanArgs {
@@ -28,8 +32,13 @@ struct ChanArgs {
   int32_t NV, CV, RB;    // vectors of a position; of a block's columns; positions of a block at a time
   int32_t slabs;         // of CV vectors to a position
   int32_t chunks, chunk; // of a sample, positions of one
+  int32_t apply_chunks, apply_chunk; // of the pass that writes, which leaves no partials
+  uint32_t last;         // blocks go backwards from this one (0: forwards)
   int32_t silu;
+  int32_t far;           // the output is more than the caches hold
   float eps;
+  int32_t sg, CS;        // groups held by one block, channels of those (whole vectors); 0: the passes over blocks
+  FastDiv div_CVs;       // vectors of those channels
   float *stats;          // [N][G][3]: the mean in two parts, 1 / sigma
   float *part;           // forward [N][chunks][2][C]: means less the first part, sums of squares about them;
                          // backward: sums of g and of g h

@@ -118,6 +118,15 @@ def test_many_rows(sb, dtype, size, causal):
     check_backward(sb, q, k, v, g, f"{size} {dtype}", causal=causal)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("size", [(2, 1060, 1060, 16, 4, 32), (1, 2100, 2050, 4, 4, 64)], ids=str)
+def test_causal_tiles_that_share_compute_units(sb, dtype, size):
+    """more tiles than units' shares of the chip: the order that sets long ones beside short ones"""
+    q, k, v, g = draw(25, *size, dtype)
+    check_forward(sb, q, k, v, f"{size} {dtype}", causal=True)
+    check_backward(sb, q, k, v, g, f"{size} {dtype}", causal=True)
+
+
 @pytest.mark.parametrize("size", [(16, 40, 50, 32, 32, 128), (9, 300, 140, 32, 32, 64), (8, 90, 70, 96, 32, 104)], ids=str)
 @pytest.mark.parametrize("causal", [False, True])
 def test_many_rows_of_unlike_lengths(sb, size, causal):

@@ -56,6 +56,9 @@ SIZES = [
     ((1, 1, 1), 1), ((2, 1, 8), 4), ((1, 2, 64), 32), ((3, 33, 96), 32), ((1, 257, 320), 32), ((2, 64, 7), 7),
     ((1, 100, 13), 1), ((1, 1000, 4), 2), ((2, 50, 1280), 32), ((1, 9, 2049), 3), ((1, 20, 4100), 4), ((5, 17, 30), 10),
     ((1, 3001, 24), 8), ((2, 40, 2048), 16), ((130, 3, 16), 2),
+    # at and past what a block holds of a group, forward (8192 vectors) and backward (5120)
+    ((2, 1024, 320), 32), ((1, 4096, 64), 4), ((1, 4097, 64), 4), ((3, 1280, 128), 4), ((1, 1281, 128), 4), ((2, 1551, 96), 32),
+    ((1, 8192, 16), 2), ((1, 8193, 16), 2), ((1, 900, 40), 4), ((1, 5120, 24), 3), ((2, 12000, 8), 1), ((1, 3, 4096), 1),
 ]
 
 

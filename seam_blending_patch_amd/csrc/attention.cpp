@@ -131,11 +131,15 @@ Plan cut(int64_t units, int64_t own, int64_t per_block, int64_t along, int waves
 
 bool whole_chunks(const sb::AttnArgs &a, int dtype) { return a.D % (16 / sb::elem_bytes(dtype)) == 0; }
 
-Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward, bool causal) {
+Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward, bool causal, bool lengths) {
   const int64_t cus = sb_cu_count(), want = !forward && causal ? 3 * cus : cus, units = (int64_t)a.B * a.Hk;
   const int eb = sb::elem_bytes(dtype), padded = sb::attn_padded(a.D), wide = 2 * sb::kAttnWaves;
   const bool whole = whole_chunks(a, dtype);
-  if (a.rows <= 32) return cut(units, a.rows, 32, a.Lk, 1, 8 * cus, 128);
+  // Single tokens: a wave to a block, as many splits as keep the memory busy; twice
+  // as many where lengths leave some of them empty (8 tokens over 16384, 14044, ... 0
+  // keys, 32 heads of 128 in 8 groups bf16 61.9 us with 16 waves a CU, 69.0 with 8;
+  // 32 over 4096 keys each 118 and 108).
+  if (a.rows <= 32) return cut(units, a.rows, 32, a.Lk, 1, (lengths ? 16 : 8) * cus, 128);
   if (forward && whole && sb::attn_wide(eb, padded) && units * ((a.rows + 32 * wide - 1) / (32 * wide)) >= 2 * cus)
     return cut(units, a.rows, 32 * wide, a.Lk, wide, 1, a.Lk + 1);
   Plan p;
@@ -171,14 +175,22 @@ int64_t keys_part(const sb::AttnArgs &a, const Plan &p) {
 }
 int64_t delta_floats(const sb::AttnArgs &a) { return up((int64_t)a.B * a.Hk * a.rows, 4); }
 
+// (the workspace's size goes by the shape alone: the largest need)
 int64_t forward_floats(const sb::AttnArgs &a, int dtype) {
-  const Plan p = plan_rows(a, dtype, true, a.causal);
-  return rows_part(a, p) + rows_part_lse(a, p);
+  int64_t most = 0;
+  for (const bool lengths : {false, true}) {
+    const Plan p = plan_rows(a, dtype, true, false, lengths);
+    most = std::max(most, rows_part(a, p) + rows_part_lse(a, p));
+  }
+  return most;
 }
-// (the workspace's size does not go by causal order: the larger need)
 int64_t backward_floats(const sb::AttnArgs &a, int dtype) {
-  return delta_floats(a) + std::max({rows_part(a, plan_rows(a, dtype, false, false)), rows_part(a, plan_rows(a, dtype, false, true)),
-                                     keys_part(a, plan_keys(a, dtype, false)), keys_part(a, plan_keys(a, dtype, true))});
+  int64_t most = 0;
+  for (const bool causal : {false, true}) {
+    most = std::max(most, keys_part(a, plan_keys(a, dtype, causal)));
+    for (const bool lengths : {false, true}) most = std::max(most, rows_part(a, plan_rows(a, dtype, false, causal, lengths)));
+  }
+  return delta_floats(a) + most;
 }
 
 int check_workspace(const void *workspace, size_t bytes, int64_t need) {
@@ -194,8 +206,7 @@ template <class F> hipError_t over_units(sb::AttnArgs a, const Plan &p, F launch
   a.tiles = (int32_t)p.tiles;
   a.splits = (int32_t)p.splits;
   a.span = (int32_t)p.span;
-  a.set = a.q_len || a.k_len ? 1 : 8;
-  a.div_set = sb::make_fastdiv((uint32_t)(a.set * p.tiles * p.splits));
+  a.div_set = sb::make_fastdiv((uint32_t)(8 * p.tiles * p.splits));
   a.div_splits = sb::make_fastdiv((uint32_t)p.splits);
   const int64_t units = (int64_t)a.B * a.Hk, each = p.tiles * p.splits, most = std::max<int64_t>(1, sb::kMaxBlocksX / each);
   for (int64_t u = 0; u < units; u += most) {
@@ -249,7 +260,7 @@ extern "C" int attention_forward(const void *q, const int64_t q_stride[3], const
   if ((rc = check_workspace(workspace, workspace_bytes, forward_floats(a, dtype) * (int64_t)sizeof(float)))) return rc;
   a.causal = causal != 0;
   a.lse = lse;
-  const Plan p = plan_rows(a, dtype, true, a.causal);
+  const Plan p = plan_rows(a, dtype, true, a.causal, a.q_len || a.k_len);
   const hipStream_t st = (hipStream_t)stream;
   // Causal tiles that are resident all at once, two blocks to a CU: the longest
   // beside the shortest (2049 tokens, 16 heads of 80 in 4 groups of two samples
@@ -310,7 +321,7 @@ extern "C" int attention_backward(const void *dout, const int64_t dout_stride[3]
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (a.Lq > 0) {
-    const Plan p = plan_rows(a, dtype, false, a.causal);
+    const Plan p = plan_rows(a, dtype, false, a.causal, a.q_len || a.k_len);
     a.part = p.splits > 1 ? part : nullptr;
     e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, p.wave_rows, st); });
     a.splits = (int32_t)p.splits;

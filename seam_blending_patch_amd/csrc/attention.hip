@@ -81,23 +81,23 @@ template <int DT, int DP, int KT> struct Softmax {
     const uint32_t *q = p[i / NB / 2] + 4 * (i / NB % 2);
     o[i % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, o[i % NB]);
   }
+  // (left to the compiler's order: with several waves to a SIMD it is as good for heads
+  // of 128 and better for 64, 8192 tokens of 16 heads 318 us against 367)
   __device__ __forceinline__ void scores(const char *lds, int kt) {
     f32x16 c[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) c[j] = f32x16{0};
-    in_order<kScores, kAhead>([&](int i) { return score_read(lds, kt, i); },
-                              [&](int i, u32x4 f) { score_use(c, i, f); });
+    for (int j = 0; j < NS; ++j) {
+      c[j] = f32x16{0};
+#pragma unroll
+      for (int u = 0; u < T::kFrags; ++u) c[j] = mma<DT>(T::row_fragment(lds, kt, 32 * j, u), qf[u], c[j]);
+    }
     keep(c);
   }
   __device__ __forceinline__ void mix(const char *lds, int vt) {
-    if constexpr (DT == DT_F32) {
 #pragma unroll
-      for (int db = 0; db < NB; ++db)
+    for (int db = 0; db < NB; ++db)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) o[db] = T::column_product(lds, vt, 32 * j, db, p[j], o[db]);
-    } else {
-      in_order<kMix, kAhead>([&](int i) { return mix_read(lds, vt, i); }, [&](int i, u32x4 f) { mix_use(i, f); });
-    }
+      for (int j = 0; j < NS; ++j) o[db] = T::column_product(lds, vt, 32 * j, db, p[j], o[db]);
   }
   // the values of one tile and the scores of the next, without a break
   __device__ __forceinline__ void mix_then_scores(const char *lds, int vt, int kt) {

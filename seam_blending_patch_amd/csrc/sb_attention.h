@@ -27,8 +27,7 @@ struct AttnArgs {
   int32_t causal;
   int32_t tiles, splits;  // of a unit (sample and key head)
   int32_t span;           // keys (rows, for key gradients) of a split, whole tiles
-  FastDiv div_group, div_set, div_splits, div_Hk; // (set: the blocks of a set of units)
-  uint32_t set;           // units of a set
+  FastDiv div_group, div_set, div_splits, div_Hk; // (set: the blocks of 8 units)
   uint32_t unit0, units;  // of this launch
   uint32_t blocks;
   int32_t beside;         // tiles of a unit after which the next share their CUs (0: longest first throughout)

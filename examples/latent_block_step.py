@@ -4,8 +4,8 @@ The block predicts the noise in latents: layer norm, one projection to query,
 key and value heads, a norm over each query and key head (in place of the packed
 projection's views, no copy), rotary embedding by (frame, row, column), attention,
 projection.  Its gradients are clipped by their global norm into the 32-bit ones
-that the update takes.  Layer norm, rotary embedding and clipping are this
-library's; matrix products and the softmax are torch's.
+that the update takes.  Layer norm, rotary embedding, attention and clipping are
+this library's; matrix products are torch's.
 
     python examples/latent_block_step.py
 """
@@ -53,6 +53,30 @@ class Turn(torch.autograd.Function):
         return dq, dk, None, None, None
 
 
+class Mix(torch.autograd.Function):
+    """attention of [tokens, heads, D] with its gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v):
+        import seam_blending_patch_amd as sb
+        out, lse = sb.attention(q, k, v, return_lse=True)
+        ctx.save_for_backward(q, k, v, out, lse)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        import seam_blending_patch_amd as sb
+        return sb.attention_backward(dout.contiguous(), *ctx.saved_tensors)
+
+
+def plain_mix(q, k, v):
+    """the same by products and a softmax in at least 32 bits, head by head: [heads, tokens, d]"""
+    wide = torch.promote_types(q.dtype, torch.float32)
+    a, b, c = (t.transpose(0, 1).to(wide).contiguous() for t in (q, k, v))
+    scores = torch.bmm(a, b.transpose(1, 2).contiguous()) / q.shape[-1] ** 0.5
+    return torch.bmm(torch.softmax(scores, -1), c).transpose(0, 1).to(q.dtype)
+
+
 def weights(width: int, heads: int, dtype, device, seed: int = 0):
     """The block's parameters, in the order that block() takes them."""
     gen = torch.Generator().manual_seed(seed)
@@ -63,19 +87,17 @@ def weights(width: int, heads: int, dtype, device, seed: int = 0):
     return [w.to(dtype).to(device).requires_grad_() for w in made]
 
 
-def block(x, w, heads: int, positions, freqs, sections, norm=Norm.apply, turn=Turn.apply):
-    """[tokens, width] -> [tokens, width]"""
+def block(x, w, heads: int, positions, freqs, sections, norm=Norm.apply, turn=Turn.apply, mix=None):
+    """[tokens, width] -> [tokens, width]; mix: attention, by default the library's (on the CPU, where the
+    block is checked, the plain one)"""
     gamma, beta, w_qkv, q_gamma, q_beta, k_gamma, k_beta, w_out = w
     tokens, width = x.shape
     d = width // heads
     qkv = (norm(x, gamma, beta) @ w_qkv).view(tokens, 3, heads, d)
     q, k = norm(qkv[:, 0], q_gamma, q_beta), norm(qkv[:, 1], k_gamma, k_beta)
     q, k = turn(q, k, positions, freqs, sections)
-    # attention in at least 32 bits, head by head: [heads, tokens, d]
-    wide = torch.promote_types(x.dtype, torch.float32)
-    q, k, v = (t.transpose(0, 1).to(wide).contiguous() for t in (q, k, qkv[:, 2]))
-    scores = torch.bmm(q, k.transpose(1, 2).contiguous()) / d ** 0.5
-    mixed = torch.bmm(torch.softmax(scores, -1), v).transpose(0, 1).reshape(tokens, width).to(x.dtype)
+    mix = mix or (Mix.apply if x.is_cuda else plain_mix)
+    mixed = mix(q, k, qkv[:, 2]).reshape(tokens, width)
     return x + mixed @ w_out
 
 

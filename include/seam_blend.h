@@ -22,7 +22,9 @@
  *
  * Beside them, operators of the transformer over latent tokens that makes the
  * latents those tiles are decoded from: layer norm (forward and backward),
- * rotary position embedding, and the gradient norm with clipping.
+ * rotary position embedding, and the gradient norm with clipping; and of such
+ * transformers' and of VAEs' and U-Nets' blocks: attention and group norm of
+ * channels-last activations (forward and backward), and dropout.
  *
  * Conventions shared by every entry point
  *  - Pointers named "device" are HIP device pointers (any device memory the
@@ -440,8 +442,8 @@ size_t group_norm_workspace_bytes(const int64_t shape[3], int64_t groups, int dt
  * the positions and channels of each group of each sample
  *   m = mean x, v = mean (x - m)^2, r = 1 / sqrt(v + eps), h = (x - m) r,
  *   out = act(h gamma_c + beta_c).
- *   shape        {N, S, C}: samples (N * groups < 2^24), positions of a sample (all
- *                spatial axes, < 2^31), channels (up to 2^16, a multiple of groups).
+ *   shape        {N, S, C}: samples (N * groups up to 2^22 - 2^12), positions of a sample
+ *                (all spatial axes, < 2^30), channels (up to 2^16, a multiple of groups).
  *   *_stride     {sample, position} strides in elements, 0..2^40; the C channels of a
  *                position are contiguous.  These are also the tokens of attention.
  *   gamma, beta  device pointers to [C] of weight_dtype, or NULL (1 and 0).

@@ -1,7 +1,8 @@
 """MI355X (gfx950) tiled-VAE decode assembly: blend + crop + stitch of
 overlapping decoded tiles, and patch-split GroupNorm; and operators of the
 transformer over latent tokens: layer norm, rotary position embedding, gradient
-norm and clipping.
+norm and clipping; and of its and of VAEs' and U-Nets' blocks: attention, group
+norm of channels-last activations, dropout.
 
 This module is the thin Python binding of ``libseamblend.so`` (C ABI in
 ``include/seam_blend.h``): it turns torch tensors into pointers, sizes and the

@@ -301,11 +301,18 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
 }
 
 // ---------------------------------------------------------------------------
-// The same two gradients for 16-bit heads of up to 192: every turn multiplies the
-// next tile's scores while it turns this tile's into probabilities, an element
-// beside each product, so that one wave keeps the matrix cores and the vector
-// unit at work together.  Three buffers: the turn of tile t reads tiles t and
-// t + 1 and stores tile t + 2.
+// The same two gradients for 16-bit heads of up to 192, of whole chunks: every turn
+// multiplies the next tile's scores while it turns this tile's into probabilities,
+// an element beside each product, so that one wave keeps the matrix cores and the
+// vector unit at work together.  Three buffers: the turn of tile t reads tiles t and
+// t + 1 and stores tile t + 2.  Straight through, without a branch around products:
+// with one the compiler carries the sums from one kind of register to the other and
+// back (dk and dv 2.71 ms with the branches that spare a wave tiles it does not see,
+// 1.86 without).  10140 tokens of 12 heads of 128 bf16: dq 0.93 ms (1020 TFLOP/s; 1.27
+// with one column of rows to a wave), dk and dv 1.39 ms (910), against 4.3 ms in all
+// for the kernels above; 8192 tokens of 16 heads of 64 0.52 and 0.63 ms.  Tiles of 64
+// rows or keys, for half the barriers, lose (dq 1.12 ms: registers), as does reading
+// 12 products ahead in place of 6 (heads of 64: 1.61 ms against 1.22 in all).
 // ---------------------------------------------------------------------------
 constexpr int kProductsAhead = 6; // LDS reads this many products before their use
 

@@ -16,7 +16,10 @@ using sb::failf;
 namespace {
 
 constexpr int64_t kMaxChannels = 1 << 16;
-constexpr int64_t kMaxGroups = 1 << 24; // samples times groups: a block each
+// samples times groups: a block of 1024 threads each, beside those for the channels,
+// in a grid of fewer than 2^32 threads
+constexpr int64_t kMaxGroups = (1 << 22) - (1 << 12);
+constexpr int64_t kMaxPositions = (int64_t)1 << 30; // of a sample: a chunk's end is a 32-bit sum
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
@@ -28,8 +31,8 @@ int read_shape(const int64_t *shape, int64_t groups, int dtype, sb::ChanArgs &a)
   if (groups < 1 || C % groups != 0)
     return failf(SB_EARG, "channels (%lld) must be a multiple of groups (%lld)", (long long)C, (long long)groups);
   if (C > kMaxChannels) return failf(SB_EGEOM, "more than %lld channels", (long long)kMaxChannels);
-  if (S >= sb::kMaxExtent || N >= sb::kMaxExtent || N * groups >= kMaxGroups)
-    return failf(SB_EGEOM, "2^31 positions of a sample, or 2^24 samples times groups, or more");
+  if (S >= kMaxPositions || N >= sb::kMaxExtent || N * groups > kMaxGroups)
+    return failf(SB_EGEOM, "2^30 positions of a sample or more, or more than 2^22 - 2^12 samples times groups");
   std::memset(&a, 0, sizeof a);
   a.N = (int32_t)N;
   a.S = (int32_t)S;

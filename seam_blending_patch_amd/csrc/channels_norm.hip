@@ -3,7 +3,10 @@
 //
 // A thread keeps one vector of channels and goes along the positions: whatever the
 // group's channels, a block reads whole runs of a position's channels, and sums
-// stay in registers by channel until the block's end.  Bound by memory.
+// stay in registers by channel until the block's end.  Bound by memory: two samples
+// of 512 x 512 x 256 fp16 134 us (sums 42, merge 5, result 87 us: 6.4 and 6.2 TB/s,
+// part of both from the caches), the gradient of 256 x 256 x 512 bf16 69 us (27, 5 and
+// 37 us).  A second reading of x (and dy) is the price of groups that no block holds.
 #include <type_traits>
 
 #include "sb_channels.h"
@@ -463,7 +466,10 @@ __global__ __launch_bounds__(kChanThreads) void gradient_kernel(const ChanArgs a
 }
 
 // ---------------------------------------------------------------------------
-// groups that a block holds in registers
+// Groups that a block holds in registers: one launch, x read once.  64 samples of
+// 1024 x 320 bf16 39 us against 53 in passes over blocks, 8 of 256 x 1280 fp16 10
+// against 20 (the host's work of a call); 2 of 1024 x 320 fp16, where 16 blocks have
+// 80 KiB each to fetch, 13.2 against 15.
 // ---------------------------------------------------------------------------
 // A block's channels c0 .. c0 + CS of sample n; a thread has vector column col of
 // positions r, r + RB, ...

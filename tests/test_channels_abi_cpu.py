@@ -43,8 +43,8 @@ GN_BAD = [
     (dict(x=None), -1, b"null x"), (dict(xs=None), -1, b"strides of x"), (dict(shape=None), -1, b"null shape"),
     (dict(shape=i64(2, 6, 0)), -1, b"channels"), (dict(shape=i64(-1, 6, 64)), -1, b"samples"),
     (dict(shape=i64(2, 6, 66)), -1, b"multiple"), (dict(groups=0), -1, b"multiple"), (dict(dtype=4), -1, b"dtype"),
-    (dict(shape=i64(2, 6, 1 << 17)), -2, b"channels"), (dict(shape=i64(2, 1 << 31, 64)), -2, b"2^31"),
-    (dict(shape=i64(1 << 23, 6, 64)), -2, b"2^24"), (dict(shape=i64(1 << 62, 6, 64)), -2, b"2^24"),
+    (dict(shape=i64(2, 6, 1 << 17)), -2, b"channels"), (dict(shape=i64(2, 1 << 30, 64)), -2, b"2^30"),
+    (dict(shape=i64(1 << 20, 6, 64)), -2, b"2^22"), (dict(shape=i64(1 << 62, 6, 64)), -2, b"2^22"),
     (dict(act=2), -1, b"activation"), (dict(wdtype=2), -1, b"weights"), (dict(gamma=P(0x500001)), -1, b"aligned"),
     (dict(xs=i64(384, -64)), -2, b"strides of x"), (dict(xs=i64(1 << 40, 64)), -2, b"strides of x"),
     (dict(x=P(0x100001)), -1, b"aligned"), (dict(work=None), -1, b"workspace"), (dict(work=P(0x800004)), -1, b"16-byte"),

@@ -107,9 +107,9 @@ int check_distinct(const Heads &out) {
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// How a kernel's work is cut (causal gradients into more splits than blocks alone
-// would need, for the longest tiles are twice the mean): blocks of `waves` waves with 32 rows (keys) each,
-// the other side in splits where that alone does not fill the chip.
+// How a kernel's work is cut: blocks of `waves` waves with 32 rows (keys) each, the
+// other side in splits where that alone does not fill the chip (causal gradients
+// into more, for their longest tiles are twice the mean).
 struct Plan {
   int waves;
   int wave_rows; // of dq's pipelined kernel (0: not that one)
@@ -201,14 +201,16 @@ int check_workspace(const void *workspace, size_t bytes, int64_t need) {
   return SB_OK;
 }
 
-// launches of as many units as a grid takes
+// launches of as many units as a grid takes: fewer than 2^24 blocks, and fewer than
+// 2^32 threads (kMaxBlocksX counts 256 of them to a block)
 template <class F> hipError_t over_units(sb::AttnArgs a, const Plan &p, F launch) {
+  const int64_t grid = p.waves > sb::kAttnWaves ? sb::kMaxBlocksX / 2 : sb::kMaxBlocksX;
   a.tiles = (int32_t)p.tiles;
   a.splits = (int32_t)p.splits;
   a.span = (int32_t)p.span;
   a.div_set = sb::make_fastdiv((uint32_t)(8 * p.tiles * p.splits));
   a.div_splits = sb::make_fastdiv((uint32_t)p.splits);
-  const int64_t units = (int64_t)a.B * a.Hk, each = p.tiles * p.splits, most = std::max<int64_t>(1, sb::kMaxBlocksX / each);
+  const int64_t units = (int64_t)a.B * a.Hk, each = p.tiles * p.splits, most = std::max<int64_t>(1, grid / each);
   for (int64_t u = 0; u < units; u += most) {
     a.unit0 = (uint32_t)u;
     a.units = (uint32_t)std::min(most, units - u);
@@ -266,7 +268,8 @@ extern "C" int attention_forward(const void *q, const int64_t q_stride[3], const
   // beside the shortest (2049 tokens, 16 heads of 80 in 4 groups of two samples
   // fp32: 288 us, longest first 336).
   const int64_t units = (int64_t)a.B * a.Hk, beside = sb_cu_count() / units;
-  if (a.causal && !a.q_len && !a.k_len && p.waves == sb::kAttnWaves && p.splits == 1 && units <= 8 && p.tiles > beside && 2 * p.tiles <= 5 * beside)
+  if (a.causal && !a.q_len && !a.k_len && p.waves == sb::kAttnWaves && p.splits == 1 && units <= 8 &&
+      p.tiles > beside && 2 * p.tiles <= 5 * beside)
     a.beside = (int32_t)beside;
   if (p.splits > 1) {
     a.part = (float *)workspace;

@@ -708,22 +708,22 @@ template <int DT, int DP> void launch_dkv(const AttnArgs &a, int, int whole, hip
 }
 
 #define SB_WIDTHS(F)                                                                                                   \
-  template <int DT> hipError_t F(const AttnArgs &a, int waves, int rows, hipStream_t st) {                                     \
+  template <int DT> hipError_t F(const AttnArgs &a, int waves, int rows, hipStream_t st) {                             \
     switch (attn_padded(a.D)) {                                                                                        \
-    case 32: F<DT, 32>(a, waves, rows, st); break;                                                                           \
-    case 64: F<DT, 64>(a, waves, rows, st); break;                                                                           \
-    case 96: F<DT, 96>(a, waves, rows, st); break;                                                                           \
-    case 128: F<DT, 128>(a, waves, rows, st); break;                                                                         \
-    case 160: F<DT, 160>(a, waves, rows, st); break;                                                                         \
-    case 192: F<DT, 192>(a, waves, rows, st); break;                                                                         \
-    default: F<DT, 256>(a, waves, rows, st);                                                                                 \
+    case 32: F<DT, 32>(a, waves, rows, st); break;                                                                     \
+    case 64: F<DT, 64>(a, waves, rows, st); break;                                                                     \
+    case 96: F<DT, 96>(a, waves, rows, st); break;                                                                     \
+    case 128: F<DT, 128>(a, waves, rows, st); break;                                                                   \
+    case 160: F<DT, 160>(a, waves, rows, st); break;                                                                   \
+    case 192: F<DT, 192>(a, waves, rows, st); break;                                                                   \
+    default: F<DT, 256>(a, waves, rows, st);                                                                           \
     }                                                                                                                  \
     return hipGetLastError();                                                                                          \
   }                                                                                                                    \
-  hipError_t F(const AttnArgs &a, int dtype, int waves, int rows, hipStream_t st) {                                              \
-    if (dtype == DT_F32) return F<DT_F32>(a, waves, rows, st);                                                               \
-    if (dtype == DT_F16) return F<DT_F16>(a, waves, rows, st);                                                               \
-    return F<DT_BF16>(a, waves, rows, st);                                                                                   \
+  hipError_t F(const AttnArgs &a, int dtype, int waves, int rows, hipStream_t st) {                                    \
+    if (dtype == DT_F32) return F<DT_F32>(a, waves, rows, st);                                                         \
+    if (dtype == DT_F16) return F<DT_F16>(a, waves, rows, st);                                                         \
+    return F<DT_BF16>(a, waves, rows, st);                                                                             \
   }
 SB_WIDTHS(launch_dq)
 SB_WIDTHS(launch_dkv)

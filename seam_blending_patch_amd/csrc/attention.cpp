@@ -266,7 +266,7 @@ extern "C" int attention_forward(const void *q, const int64_t q_stride[3], const
   const hipStream_t st = (hipStream_t)stream;
   // Causal tiles that are resident all at once, two blocks to a CU: the longest
   // beside the shortest (2049 tokens, 16 heads of 80 in 4 groups of two samples
-  // fp32: 288 us, longest first 336).
+  // fp32: 269 us, longest first 315).
   const int64_t units = (int64_t)a.B * a.Hk, beside = sb_cu_count() / units;
   if (a.causal && !a.q_len && !a.k_len && p.waves == sb::kAttnWaves && p.splits == 1 && units <= 8 &&
       p.tiles > beside && 2 * p.tiles <= 5 * beside)

@@ -83,13 +83,23 @@ template <int DT, int DP, int KT> struct Softmax {
   }
   // (left to the compiler's order: with several waves to a SIMD it is as good for heads
   // of 128 and better for 64, 8192 tokens of 16 heads 318 us against 367)
-  __device__ __forceinline__ void scores(const char *lds, int kt) {
+  // (all: D reaches the last 16 elements of the padded head, else their products are
+  // left out: 2049 causal tokens of heads of 80 fp32 269 us, with them 286; 8192 tokens
+  // of heads of 48 bf16 326 and 339)
+  __device__ __forceinline__ void scores(const char *lds, int kt, bool all) {
+    constexpr int kMost = T::kFrags - 8 / T::V;
     f32x16 c[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       c[j] = f32x16{0};
 #pragma unroll
-      for (int u = 0; u < T::kFrags; ++u) c[j] = mma<DT>(T::row_fragment(lds, kt, 32 * j, u), qf[u], c[j]);
+      for (int u = 0; u < kMost; ++u) c[j] = mma<DT>(T::row_fragment(lds, kt, 32 * j, u), qf[u], c[j]);
+    }
+    if (all) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int u = kMost; u < T::kFrags; ++u) c[j] = mma<DT>(T::row_fragment(lds, kt, 32 * j, u), qf[u], c[j]);
     }
     keep(c);
   }
@@ -177,10 +187,10 @@ template <int DT, int DP, int KT> struct Softmax {
 
 // Blocks of one wave (single tokens: bound by memory, 4.3 TB/s over a cache of unlike
 // lengths, 5.0 over one of 4096 keys each) or four, which take turns at the matrix
-// cores as they come.  8192 tokens of 16 heads of 64 bf16: 320 us, 860 TFLOP/s, what
+// cores as they come.  8192 tokens of 16 heads of 64 bf16: 330 us, 830 TFLOP/s, what
 // the vector unit's work on the scores allows there; 2049 causal tokens of 16 heads
-// of 80 fp32: 288 us, 75 TFLOP/s where a library product reaches 139 (a sixth of it
-// for the padding to 96, a third for the unequal tiles).
+// of 80 fp32: 269 us, 80 TFLOP/s where a library product reaches 139 (a twelfth of it
+// for the values' padding to 96, a third for the unequal tiles).
 template <int DT, int DP, int NW>
 __global__ __launch_bounds__(64 * NW, forward_waves(DT, DP, NW)) void attention_kernel(const AttnArgs a) {
   constexpr int kThreads = 64 * NW;
@@ -195,6 +205,7 @@ __global__ __launch_bounds__(64 * NW, forward_waves(DT, DP, NW)) void attention_
   Softmax<DT, DP, KT> x;
   x.start(a, r);
   const float slack = 8.0f / a.scale2;
+  const bool all = a.D > DP - 16;
   const int64_t k_base = r.w.b * a.k.b + r.w.hk * a.k.h, v_base = r.w.b * a.v.b + r.w.hk * a.v.h;
   const auto k_at = [&](int k) { return k_base + k * a.k.t; };
   const auto v_at = [&](int k) { return v_base + k * a.v.t; };
@@ -222,7 +233,7 @@ __global__ __launch_bounds__(64 * NW, forward_waves(DT, DP, NW)) void attention_
     if (k0 < r.wend) {
       // (the wave that has products goes first, the other has a softmax to do meanwhile)
       __builtin_amdgcn_s_setprio(1);
-      x.scores(lds, row_lane + cur);
+      x.scores(lds, row_lane + cur, all);
       __builtin_amdgcn_s_setprio(0);
       if (k0 + KT > r.sure) x.hide(r.sees - k0 - 4 * r.h);
       x.soften(a.scale2, slack);
@@ -295,7 +306,7 @@ __global__ __launch_bounds__(128 * kAttnWaves) void attention_wide_kernel(const 
     __syncthreads();
     const bool second = __builtin_amdgcn_readfirstlane(threadIdx.x) >= kThreads / 2;
     if (second) lds_barrier();
-    if (r.begin < r.wend) x.scores(lds, row_lane);
+    if (r.begin < r.wend) x.scores(lds, row_lane, true);
     // byte offsets of the buffers of tiles t, t + 1 and t + 2
     int b0 = 0, b1 = 2 * T::kBytes, b2 = 4 * T::kBytes;
     for (int t = 0, k0 = r.begin; t < tiles; ++t, k0 += KT) {

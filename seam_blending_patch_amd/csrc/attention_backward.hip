@@ -5,6 +5,14 @@
 // Two kernels, one for dq (and delta) that goes along the keys, one for dk and dv
 // that goes along the rows: each result has one owner that adds it up in a fixed
 // order, at the price of forming S and dout v^T twice (7 products for 5).
+//
+// Roundings to 16 bits: P and dS where they enter a product (the matrix cores' rate in
+// 16 bits is 8 times that in fp32), and delta is formed of the rounded out (out in fp32
+// would have to be kept by the forward pass, or a product more formed here).  Errors of
+// dq and dk against 64 bits, relative, bf16, 1500 rows of heads of 128, emulated on the
+// CPU: 1.7e-3 for the results' own rounding, 2.4e-3 with that of dS, 2.4e-3 and 2.2e-3
+// with that of out in delta, 2.9e-3 and 2.7e-3 with both; measured up to 3.5e-3 over
+// 10140 tokens (fp16 an eighth of these).  fp32 rounds nothing.
 #include "attention_tile.h"
 
 namespace sb {

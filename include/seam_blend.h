@@ -419,9 +419,10 @@ size_t attention_backward_workspace_bytes(const int64_t shape[6], int dtype);
  *                none with each other or an input (checked; SB_EARG).  Zeros where a
  *                length, or causal order, leaves nothing.
  * Other arguments as attention_forward's.  P and dS are rounded to dtype for the
- * products they enter (in fp16 what is below 6e-8 vanishes: scale the loss), and
- * the row sums are those of out as it was rounded: in 16 bits dq and dk are about
- * twice as far off as their last rounding alone would leave them.  The
+ * products they enter (in fp16 what is below 6e-8 vanishes: scale the loss): in 16 bits
+ * the gradients are about 1.4 times as far off as their last rounding alone would leave
+ * them.  What out was rounded to does not matter (its row sums with dout are corrected
+ * by what dS adds up to).  The
  * heads that share a key head are added up in fp32, in a fixed order: deterministic.
  */
 int attention_backward(const void *dout, const int64_t dout_stride[3], const void *q, const int64_t q_stride[3],

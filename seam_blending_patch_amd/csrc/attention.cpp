@@ -154,7 +154,8 @@ Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward, bool causal, bool
     p.wave_rows = 32;
     return p;
   }
-  return cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, want, 512);
+  const bool paired = !forward && sb::attn_dq_paired(eb, padded);
+  return cut(units, a.rows, 32 * sb::kAttnWaves / (paired ? 2 : 1), a.Lk, sb::kAttnWaves, want, 512);
 }
 
 Plan plan_keys(const sb::AttnArgs &a, int dtype, bool causal) {
@@ -166,6 +167,13 @@ Plan plan_keys(const sb::AttnArgs &a, int dtype, bool causal) {
 
 int64_t rows_part(const sb::AttnArgs &a, const Plan &p) { // floats of the splits' rows
   return p.splits > 1 ? up(p.splits * a.B * a.Hk * a.rows * (int64_t)a.D, 4) : 0;
+}
+// (of dq in 16 bits beside its rows: their means, and two numbers of each)
+int64_t rows_part_mean(const sb::AttnArgs &a, const Plan &p, int dtype) {
+  return dtype == SB_F32 ? 0 : rows_part(a, p);
+}
+int64_t rows_part_left(const sb::AttnArgs &a, const Plan &p, int dtype) {
+  return dtype == SB_F32 || p.splits == 1 ? 0 : up(2 * p.splits * a.B * a.Hk * (int64_t)a.rows, 4);
 }
 int64_t rows_part_lse(const sb::AttnArgs &a, const Plan &p) {
   return p.splits > 1 ? up(p.splits * a.B * a.Hk * (int64_t)a.rows, 4) : 0;
@@ -188,7 +196,10 @@ int64_t backward_floats(const sb::AttnArgs &a, int dtype) {
   int64_t most = 0;
   for (const bool causal : {false, true}) {
     most = std::max(most, keys_part(a, plan_keys(a, dtype, causal)));
-    for (const bool lengths : {false, true}) most = std::max(most, rows_part(a, plan_rows(a, dtype, false, causal, lengths)));
+    for (const bool lengths : {false, true}) {
+      const Plan p = plan_rows(a, dtype, false, causal, lengths);
+      most = std::max(most, rows_part(a, p) + rows_part_mean(a, p, dtype) + rows_part_left(a, p, dtype));
+    }
   }
   return delta_floats(a) + most;
 }
@@ -326,9 +337,13 @@ extern "C" int attention_backward(const void *dout, const int64_t dout_stride[3]
   if (a.Lq > 0) {
     const Plan p = plan_rows(a, dtype, false, a.causal, a.q_len || a.k_len);
     a.part = p.splits > 1 ? part : nullptr;
+    a.part_mean = part + rows_part(a, p);
+    a.part_left = a.part_mean + rows_part_mean(a, p, dtype);
     e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, p.wave_rows, st); });
     a.splits = (int32_t)p.splits;
-    if (e == hipSuccess && p.splits > 1) e = sb_launch_attention_sum(a, &a.dq, 1, a.rows, a.group, dtype, st);
+    if (e == hipSuccess && p.splits > 1)
+      e = dtype == SB_F32 ? sb_launch_attention_sum(a, &a.dq, 1, a.rows, a.group, dtype, st)
+                          : sb_launch_attention_dq_join(a, dtype, st);
   }
   if (e == hipSuccess && a.Lk > 0) {
     const Plan p = plan_keys(a, dtype, a.causal);

@@ -420,6 +420,46 @@ template <int DT> __global__ __launch_bounds__(kSumThreads) void sum_kernel(cons
   store_four<DT>((void *)out.p, b * out.b + q * out.t + (int64_t)(hk * a.div_group.d + g) * out.h + d, n, acc);
 }
 
+// dq's splits added up the same way, less what their sums left of the row times its
+// mean key; and delta with it (its row's first thread, behind its own splits' loads).
+template <int DT> __global__ __launch_bounds__(kSumThreads) void dq_join_kernel(const AttnArgs a, const FastDiv div_quads,
+                                                                                int64_t rows) {
+  const uint32_t row = blockIdx.x * (kSumThreads / div_quads.d) + fdiv(threadIdx.x, div_quads);
+  const int d = (int)(threadIdx.x % div_quads.d) * 4, n = a.D - d;
+  if (threadIdx.x >= kSumThreads / div_quads.d * div_quads.d || row >= rows) return;
+  f32x4v acc = {0, 0, 0, 0}, mean = {0, 0, 0, 0};
+  float left = 0.0f, exact = 0.0f;
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    Vec<16> v[8], m[8];
+    float2 l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool any = s0 + j < a.splits;
+      const int64_t at = (any ? s0 + j : 0) * rows + row;
+      v[j] = load_part<DT_F32>(a.part, at * a.D + d, any ? n : 0);
+      m[j] = load_part<DT_F32>(a.part_mean, at * a.D + d, any ? n : 0);
+      l[j] = *reinterpret_cast<const float2 *>(a.part_left + 2 * at);
+      if (!any) l[j] = float2{0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] += __uint_as_float(v[j].w[i]);
+        mean[i] += __uint_as_float(m[j].w[i]);
+      }
+      left += l[j].x;
+      exact += l[j].y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(-left, mean[i], acc[i]);
+  const uint32_t unit = (uint32_t)(row / (uint32_t)a.rows), b = fdiv(unit, a.div_Hk), hk = unit - b * a.div_Hk.d;
+  const int r = (int)(row - unit * (uint32_t)a.rows);
+  store_four<DT>((void *)a.dq.p, row_at(a.dq, a, b, hk, r) + d, n, acc);
+  if (d == 0 && r < length_of(a.q_len, b, a.Lq) * a.group) a.delta[stat_at(a, b, hk, r)] += exact;
+}
+
 template <int DT, int DP> void launch(const AttnArgs &a, int waves, hipStream_t st) {
   if (waves == 1) hipLaunchKernelGGL((attention_kernel<DT, DP, 1>), dim3(a.blocks), dim3(64), 0, st, a);
   else if (waves == kAttnWaves || !attn_wide(Elem<DT>::bytes, DP))
@@ -464,6 +504,15 @@ hipError_t sb_launch_attention_join(const sb::AttnArgs &a, int dtype, hipStream_
     SB_JOIN(sb::kJoinRows);
   }
 #undef SB_JOIN
+  return hipGetLastError();
+}
+
+hipError_t sb_launch_attention_dq_join(const sb::AttnArgs &a, int dtype, hipStream_t st) {
+  const sb::FastDiv quads = sb::make_fastdiv((uint32_t)((a.D + 3) / 4));
+  const int64_t rows = (int64_t)a.B * a.Hk * a.rows, each = sb::kSumThreads / quads.d;
+  const dim3 grid((unsigned)((rows + each - 1) / each)), block(sb::kSumThreads);
+  if (dtype == sb::DT_F16) hipLaunchKernelGGL((sb::dq_join_kernel<sb::DT_F16>), grid, block, 0, st, a, quads, rows);
+  else hipLaunchKernelGGL((sb::dq_join_kernel<sb::DT_BF16>), grid, block, 0, st, a, quads, rows);
   return hipGetLastError();
 }
 

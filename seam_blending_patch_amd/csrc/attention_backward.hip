@@ -4,57 +4,122 @@
 //   dS = P (dout v^T - delta), dq = scale dS k, dk = scale dS^T q, dv = P^T dout.
 // Two kernels, one for dq (and delta) that goes along the keys, one for dk and dv
 // that goes along the rows: each result has one owner that adds it up in a fixed
-// order, at the price of forming S and dout v^T twice (7 products for 5).
+// order, at the price of forming S and dout v^T twice (7 products for 5, in 16 bits 8:
+// Left below).
 //
 // Roundings to 16 bits: P and dS where they enter a product (the matrix cores' rate in
-// 16 bits is 8 times that in fp32), and delta is formed of the rounded out (out in fp32
-// would have to be kept by the forward pass, or a product more formed here).  Errors of
-// dq and dk against 64 bits, relative, bf16, 1500 rows of heads of 128, emulated on the
-// CPU: 1.7e-3 for the results' own rounding, 2.4e-3 with that of dS, 2.4e-3 and 2.2e-3
-// with that of out in delta, 2.9e-3 and 2.7e-3 with both; measured up to 3.5e-3 over
-// 10140 tokens (fp16 an eighth of these).  fp32 rounds nothing.
+// 16 bits is 8 times that in fp32).  That of out, which delta is formed of, is taken out
+// again.  Errors of dq and dk against 64 bits, relative, 10140 tokens of heads of 128
+// bf16: 2.2e-3 and 2.4e-3, 1.7e-3 for the results' own rounding alone (3.5e-3 with out's
+// rounding left in); fp16 an eighth.  fp32 rounds nothing.
 #include "attention_tile.h"
 
 namespace sb {
 namespace {
 
+// What a row of dq still needs when its keys are done, in 16 bits (fp32: out's rounding
+// is one of fp32, nothing is left).  delta is formed of an `out` that was rounded, and
+// each dS was: with r = the sum of the row's dS, which is zero but for these,
+//   dq = scale (sum dS k - r m),  m = sum P k,
+// takes both out along m, and delta + the sum of dS before its rounding is the exact
+// delta that dk's kernel needs.  The price is a product more, of the fragments that dS
+// takes, and as many registers for m as for dq: 10140 tokens of 12 heads of 128 bf16 dq
+// 1.38 ms, 0.93 without (when two columns of rows to a wave had room); 8192 of 16 heads of
+// 64 0.64 and 0.54; a pass of its own for delta would form two products again.
+template <int DT> constexpr bool kMeanOf = DT != DT_F32;
+template <int DT> struct Left {
+  float rounded, exact;
+  __device__ __forceinline__ void add(float ds) { exact += ds; }
+  __device__ __forceinline__ void add(uint32_t packed) { rounded = pair_sum<DT>(packed, rounded); }
+};
+
+// A row's results: dq (columns from 32 db0 on), or the split's share of it with what
+// is left, and delta.
+template <int DT, int NB, int NM>
+__device__ __forceinline__ void store_dq(const AttnArgs &a, const Work &w, int row, int h, int db0, bool live, float delta,
+                                         Left<DT> left, f32x16 (&dq)[NB], const f32x16 (&mean)[NM]) {
+  if constexpr (kMeanOf<DT>) {
+    left.rounded = half_sum(left.rounded);
+    left.exact = half_sum(left.exact);
+  }
+  if (row >= a.rows) return;
+  const float by = live ? a.scale : 0.0f;
+  const bool first = h == 0 && db0 == 0;
+  if (a.part) {
+    const int64_t at = ((int64_t)w.split * a.B * a.Hk + w.unit) * a.rows + row;
+#pragma unroll
+    for (int db = 0; db < NB; ++db)
+      store_column<DT_F32>(a.part, at * a.D, db0 + db, h, a.D, live ? dq[db] : f32x16{0}, by);
+    if constexpr (kMeanOf<DT>) {
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+        store_column<DT_F32>(a.part_mean, at * a.D, db0 + db, h, a.D, live ? mean[db] : f32x16{0}, by);
+      if (first) {
+        float *const to = a.part_left + 2 * at;
+        to[0] = live ? left.rounded : 0.0f;
+        to[1] = live ? left.exact : 0.0f;
+      }
+    }
+    if (live && first && w.split == 0) a.delta[stat_at(a, w.b, w.hk, row)] = delta;
+  } else {
+    const int64_t at = row_at(a.dq, a, w.b, w.hk, row);
+#pragma unroll
+    for (int db = 0; db < NB; ++db) {
+      if constexpr (kMeanOf<DT>) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[db][i] = __builtin_fmaf(-left.rounded, mean[db][i], dq[db][i]);
+      }
+      store_column<DT>((void *)a.dq.p, at, db0 + db, h, a.D, live ? dq[db] : f32x16{0}, by);
+    }
+    if (live && first) a.delta[stat_at(a, w.b, w.hk, row)] = kMeanOf<DT> ? delta + left.exact : delta;
+  }
+}
+
 // dq.  As forward: a lane has a row; S^T = K Q^T, (dout v^T)^T = V dOut^T, and
-// dS^T feeds dQ^T += K^T dS^T.
-template <int DT, int DP, int NW>
+// dS^T feeds dQ^T += K^T dS^T.  PAIR: a head is too long for one wave's registers; two
+// waves have half of its elements of the same rows each, and add up their halves of
+// the scores, of dout v^T and of delta through LDS.
+template <int DT, int DP, int NW, bool PAIR>
 __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
-  constexpr int kThreads = 64 * NW, KT = 32;
+  constexpr int kThreads = 64 * NW, KT = 32, W = PAIR ? 2 : 1, ROWS = 32 * NW / W;
   using T = Tile<DT, DP, KT>;
   using St = Stage<DT, DP, KT, kThreads>;
-  constexpr bool kAhead = St::N <= 8 && T::kFrags * 4 <= 64; // the next tile is requested while this one is used
-  constexpr int kBufs = kAhead ? 2 : 1, NB = DP / 32, PW = DT == DT_F32 ? 16 : 8;
+  constexpr int NF = T::kFrags / W, NB = DP / 32 / W, PW = DT == DT_F32 ? 16 : 8;
+  constexpr bool kAhead = St::N <= 8 && NF * 4 <= 64; // the next tile is requested while this one is used
+  constexpr int kBufs = kAhead ? 2 : 1;
+  constexpr bool kMean = kMeanOf<DT>;
   __shared__ alignas(1024) char lds[kBufs * 2 * T::kBytes]; // of each buffer keys, then values
+  __shared__ float halves[PAIR ? NW : 1][PAIR ? 32 : 1][64];
 
   const Work w = work_of<true>(a);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, n = lane & 31;
+  const int part = PAIR ? wave & 1 : 0;
   const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
   const int off = klen - qlen, live_rows = qlen * a.group;
-  const int r0 = w.tile * 32 * NW, wr0 = r0 + wave * 32, row = wr0 + n;
+  const int r0 = w.tile * ROWS, wr0 = r0 + wave / W * 32, row = wr0 + n;
   const bool live = row < live_rows;
   const auto seen = [&](int r) {
     return a.causal ? min(max((int)fdiv((uint32_t)r, a.div_group) + off + 1, 0), klen) : klen;
   };
   const int sees = live ? seen(row) : klen;
   const int sure = seen(min(wr0, max(live_rows - 1, 0)));
-  const int last = min(r0 + 32 * NW, live_rows) - 1, wlast = min(wr0 + 32, live_rows) - 1;
+  const int last = min(r0 + ROWS, live_rows) - 1, wlast = min(wr0 + 32, live_rows) - 1;
   const int begin = w.split * a.span;
   const int end = last < r0 ? 0 : min(seen(last), begin + a.span);
   const int wend = wlast < wr0 ? 0 : min(seen(wlast), end);
 
-  u32x4 qf[T::kFrags], gf[T::kFrags];
+  u32x4 qf[NF], gf[NF];
   float delta = 0.0f, lse2 = kInf; // (a row that sees no key, or is none: its probabilities are exp2(-inf))
+  Left<DT> left = {};
   {
     const int64_t at = live ? row_at(a.q, a, w.b, w.hk, row) : 0, to = live ? row_at(a.out, a, w.b, w.hk, row) : 0,
                   gt = live ? row_at(a.dout, a, w.b, w.hk, row) : 0;
 #pragma unroll
-    for (int u = 0; u < T::kFrags; ++u) {
-      qf[u] = load_chunk<DT>(a.q.p, at, 2 * u + h, a.D, live);
-      gf[u] = load_chunk<DT>(a.dout.p, gt, 2 * u + h, a.D, live);
-      const u32x4 of = load_chunk<DT>(a.out.p, to, 2 * u + h, a.D, live);
+    for (int u = 0; u < NF; ++u) {
+      const int c = 2 * (u + part * NF) + h;
+      qf[u] = load_chunk<DT>(a.q.p, at, c, a.D, live);
+      gf[u] = load_chunk<DT>(a.dout.p, gt, c, a.D, live);
+      const u32x4 of = load_chunk<DT>(a.out.p, to, c, a.D, live);
       float f[T::V], g[T::V];
       unpack<DT, 16>(Vec<16>{of[0], of[1], of[2], of[3]}, f);
       unpack<DT, 16>(Vec<16>{gf[u][0], gf[u][1], gf[u][2], gf[u][3]}, g);
@@ -62,16 +127,23 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
       for (int i = 0; i < T::V; ++i) delta = __builtin_fmaf(f[i], g[i], delta);
     }
     delta = half_sum(delta);
+    if constexpr (PAIR) {
+      halves[wave][0][lane] = delta;
+      __syncthreads();
+      delta += halves[wave ^ 1][0][lane];
+      __syncthreads();
+    }
     if (live) {
       const int64_t st = stat_at(a, w.b, w.hk, row);
       const float lse = a.lse[st];
       if (lse != -kInf) lse2 = lse * kLog2e;
-      if (w.split == 0 && h == 0) a.delta[st] = delta;
     }
   }
-  f32x16 dq[NB];
+  f32x16 dq[NB], mean[kMean ? NB : 1];
 #pragma unroll
   for (int db = 0; db < NB; ++db) dq[db] = f32x16{0};
+#pragma unroll
+  for (int db = 0; db < (kMean ? NB : 1); ++db) mean[db] = f32x16{0};
 
   const int64_t k_base = w.b * a.k.b + w.hk * a.k.h, v_base = w.b * a.v.b + w.hk * a.v.h;
   const auto k_at = [&](int r) { return k_base + r * a.k.t; };
@@ -98,25 +170,54 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
       __syncthreads();
     }
     const int kt = row_lane + cur, vt = kt + T::kBytes, kc = col_lane + cur;
-    if (k0 < wend) {
+    if (PAIR || k0 < wend) {
       f32x16 s = {0}, dp = {0};
 #pragma unroll
-      for (int u = 0; u < T::kFrags; ++u) {
-        s = mma<DT>(T::row_fragment(lds, kt, 0, u), qf[u], s);
-        dp = mma<DT>(T::row_fragment(lds, vt, 0, u), gf[u], dp);
+      for (int u = 0; u < NF; ++u) {
+        s = mma<DT>(T::row_fragment(lds, kt, 0, u + part * NF), qf[u], s);
+        dp = mma<DT>(T::row_fragment(lds, vt, 0, u + part * NF), gf[u], dp);
       }
-      float ds[16];
+      if constexpr (PAIR) { // (the barrier before the next tile keeps these until they are read)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
+        for (int i = 0; i < 16; ++i) {
+          halves[wave][i][lane] = s[i];
+          halves[wave][16 + i][lane] = dp[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[i] += halves[wave ^ 1][i][lane];
+          dp[i] += halves[wave ^ 1][16 + i][lane];
+        }
+      }
+      float p[16], ds[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.scale2, -lse2));
+        ds[i] = p[i] * (dp[i] - delta);
+      }
       if (k0 + KT > sure) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ds[i] = k0 + 8 * (i >> 2) + 4 * h + (i & 3) < sees ? ds[i] : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+          const bool sees_it = k0 + 8 * (i >> 2) + 4 * h + (i & 3) < sees;
+          p[i] = sees_it ? p[i] : 0.0f;
+          ds[i] = sees_it ? ds[i] : 0.0f;
+        }
       }
-      uint32_t p[PW];
-      pack_operand<DT>(ds, p);
+      uint32_t pp[PW], pd[PW];
+      pack_operand<DT>(ds, pd);
+      if constexpr (kMean) {
+        pack_operand<DT>(p, pp);
 #pragma unroll
-      for (int db = 0; db < NB; ++db) dq[db] = T::column_product(lds, kc, 0, db, p, dq[db]);
+        for (int i = 0; i < 16; ++i) left.add(ds[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) left.add(pd[i]);
+      }
+#pragma unroll
+      for (int db = 0; db < NB; ++db) {
+        dq[db] = T::column_product(lds, kc, 0, db + part * NB, pd, dq[db]);
+        if constexpr (kMean) mean[db] = T::column_product(lds, kc, 0, db + part * NB, pp, mean[db]);
+      }
     }
     if constexpr (kAhead) {
       cur ^= 2 * T::kBytes;
@@ -128,19 +229,7 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
     }
   }
 
-  if (row >= a.rows) return;
-  const float by = live ? a.scale : 0.0f;
-  if (a.part) {
-    const int64_t at = ((int64_t)w.split * a.B * a.Hk + w.unit) * a.rows + row;
-#pragma unroll
-    for (int db = 0; db < NB; ++db)
-      store_column<DT_F32>(a.part, at * a.D, db, h, a.D, live ? dq[db] : f32x16{0}, by);
-  } else {
-    const int64_t at = row_at(a.dq, a, w.b, w.hk, row);
-#pragma unroll
-    for (int db = 0; db < NB; ++db)
-      store_column<DT>((void *)a.dq.p, at, db, h, a.D, live ? dq[db] : f32x16{0}, by);
-  }
+  store_dq<DT, NB>(a, w, row, h, part * NB, live, delta, left, dq, mean);
 }
 
 // dk and dv.  A lane has a key: S = Q K^T and dOut V^T put the rows into its
@@ -316,11 +405,10 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
 // t + 1 and stores tile t + 2.  Straight through, without a branch around products:
 // with one the compiler carries the sums from one kind of register to the other and
 // back (dk and dv 2.71 ms with the branches that spare a wave tiles it does not see,
-// 1.86 without).  10140 tokens of 12 heads of 128 bf16: dq 0.93 ms (1020 TFLOP/s; 1.27
-// with one column of rows to a wave), dk and dv 1.39 ms (910), against 4.3 ms in all
-// for the kernels above; 8192 tokens of 16 heads of 64 0.52 and 0.63 ms.  Tiles of 64
-// rows or keys, for half the barriers, lose (dq 1.12 ms: registers), as does reading
-// 12 products ahead in place of 6 (heads of 64: 1.61 ms against 1.22 in all).
+// 1.86 without).  10140 tokens of 12 heads of 128 bf16: dq 1.38 ms (910 TFLOP/s on its four
+// products), dk and dv 1.41 ms (900); 8192 tokens of 16 heads of 64 0.64 and 0.63 ms.
+// Reading 12 products ahead in place of 6 loses (heads of 64 1.61 ms against 1.22 in all,
+// with three products for dq).
 // ---------------------------------------------------------------------------
 constexpr int kProductsAhead = 6; // LDS reads this many products before their use
 
@@ -330,6 +418,12 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
+
+// Waits for all that was requested, in every lane: threads that store no chunk would
+// leave it open to the compiler whether they still wait for theirs, and it would wait
+// again between the next requests (dq of 10140 tokens of 12 heads of 128 bf16: 1.43 ms, 1.77
+// without this).
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); } // (vmcnt 0, no other counter)
 
 // dq: a wave has R columns of 32 rows.
 template <int DT, int DP, int NW, int R>
@@ -381,14 +475,14 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
       const int64_t st = stat_at(a, w.b, w.hk, row);
       const float lse = a.lse[st];
       if (lse != -kInf) lse2[c] = lse * kLog2e;
-      if (w.split == 0 && h == 0) a.delta[st] = delta[c];
     }
   }
-  f32x16 dq[R][NB];
+  f32x16 dq[R][NB], mean[R][NB];
+  Left<DT> left[R] = {};
 #pragma unroll
   for (int c = 0; c < R; ++c)
 #pragma unroll
-    for (int db = 0; db < NB; ++db) dq[c][db] = f32x16{0};
+    for (int db = 0; db < NB; ++db) dq[c][db] = mean[c][db] = f32x16{0};
 
   const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
   const int tiles = end > begin ? (end - begin + KT - 1) / KT : 0;
@@ -429,6 +523,7 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
     int b0 = 0, b1 = 2 * T::kBytes, b2 = 4 * T::kBytes;
     for (int t = 0, k0 = begin; t < tiles; ++t, k0 += KT) {
       if (t + 2 < tiles) {
+        arrived();
         sk.store(lds + b2);
         sv.store(lds + b2 + T::kBytes);
         if (t + 3 < tiles) {
@@ -437,11 +532,11 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
         }
       }
       {
-        float ds[R][16];
+        float p[R][16], ds[R][16];
 #pragma unroll
         for (int c = 0; c < R; ++c) s1[c] = dp1[c] = f32x16{0};
         // (behind the last tile: scores of what the buffer holds, not used)
-        uint32_t p[R][8];
+        uint32_t pp[R][8], pd[R][8];
         in_order<2 * NF + 2 * NB, kProductsAhead>(
             [&](int i) {
               const int j = i - 2 * NF;
@@ -452,22 +547,44 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
 #pragma unroll
               for (int c = 0; c < R; ++c) {
                 if (j >= 0) {
-                  const uint32_t *q = p[c] + 4 * (j / NB);
+                  const uint32_t *q = pd[c] + 4 * (j / NB), *m = pp[c] + 4 * (j / NB);
                   dq[c][j % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, dq[c][j % NB]);
+                  mean[c][j % NB] = mma<DT>(f, u32x4{m[0], m[1], m[2], m[3]}, mean[c][j % NB]);
+                  // (beside the products: the sums, and the second half's packing)
+#pragma unroll
+                  for (int e = j * 8 / NB; e < (j + 1) * 8 / NB; ++e) left[c].add(ds[c][e]);
+                  if (j == NB - 1) {
+#pragma unroll
+                    for (int e = 4; e < 8; ++e) {
+                      pp[c][e] = pack_pair<DT>(p[c] + 2 * e);
+                      pd[c][e] = pack_pair<DT>(ds[c] + 2 * e);
+                    }
+                  }
+#pragma unroll
+                  for (int e = j * 4 / NB; e < (j + 1) * 4 / NB; ++e) left[c].add(pd[c][e]);
                   continue;
                 }
                 if (i & 1) dp1[c] = mma<DT>(f, gf[c][i >> 1], dp1[c]);
                 else s1[c] = mma<DT>(f, qf[c][i >> 1], s1[c]);
 #pragma unroll
-                for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e)
-                  ds[c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e], a.scale2, -lse2[c])) * (dp[c][e] - delta[c]);
+                for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e) {
+                  p[c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e], a.scale2, -lse2[c]));
+                  ds[c][e] = p[c][e] * (dp[c][e] - delta[c]);
+                }
                 if (j == -1) {
                   if (k0 + KT > sure) {
-                    const int left = sees[c] - k0 - 4 * h;
+                    const int keys = sees[c] - k0 - 4 * h;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) ds[c][x] = 8 * (x >> 2) + (x & 3) < left ? ds[c][x] : 0.0f;
+                    for (int x = 0; x < 16; ++x) {
+                      p[c][x] = 8 * (x >> 2) + (x & 3) < keys ? p[c][x] : 0.0f;
+                      ds[c][x] = 8 * (x >> 2) + (x & 3) < keys ? ds[c][x] : 0.0f;
+                    }
                   }
-                  pack_operand<DT>(ds[c], p[c]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    pp[c][e] = pack_pair<DT>(p[c] + 2 * e);
+                    pd[c][e] = pack_pair<DT>(ds[c] + 2 * e);
+                  }
                 }
               }
             });
@@ -488,20 +605,7 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
 #pragma unroll
   for (int c = 0; c < R; ++c) {
     const int row = wr0 + 32 * c + n;
-    if (row >= a.rows) continue;
-    const bool live = row < live_rows;
-    const float by = live ? a.scale : 0.0f;
-    if (a.part) {
-      const int64_t at = ((int64_t)w.split * a.B * a.Hk + w.unit) * a.rows + row;
-#pragma unroll
-      for (int db = 0; db < NB; ++db)
-        store_column<DT_F32>(a.part, at * a.D, db, h, a.D, live ? dq[c][db] : f32x16{0}, by);
-    } else {
-      const int64_t at = row_at(a.dq, a, w.b, w.hk, row);
-#pragma unroll
-      for (int db = 0; db < NB; ++db)
-        store_column<DT>((void *)a.dq.p, at, db, h, a.D, live ? dq[c][db] : f32x16{0}, by);
-    }
+    store_dq<DT, NB>(a, w, row, h, 0, row < live_rows, delta[c], left[c], dq[c], mean[c]);
   }
 }
 
@@ -701,8 +805,10 @@ template <int DT, int DP> void launch_dq(const AttnArgs &a, int waves, int wave_
       return;
     }
   }
-  if (waves == 1) hipLaunchKernelGGL((dq_kernel<DT, DP, 1>), grid, dim3(64), 0, st, a);
-  else hipLaunchKernelGGL((dq_kernel<DT, DP, kAttnWaves>), grid, block, 0, st, a);
+  constexpr bool kPair = attn_dq_paired(Elem<DT>::bytes, DP);
+  constexpr int kFew = kPair ? 2 : 1; // waves of a block of 32 rows
+  if (waves == 1) hipLaunchKernelGGL((dq_kernel<DT, DP, kFew, kPair>), grid, dim3(64 * kFew), 0, st, a);
+  else hipLaunchKernelGGL((dq_kernel<DT, DP, kAttnWaves, kPair>), grid, block, 0, st, a);
 }
 template <int DT, int DP> void launch_dkv(const AttnArgs &a, int, int whole, hipStream_t st) {
   const dim3 grid(a.blocks), block(64 * kAttnWaves);

@@ -150,6 +150,17 @@ template <int DT> __device__ __forceinline__ void pack_operand(const float *s, u
   }
 }
 
+template <int DT> __device__ __forceinline__ uint32_t pack_pair(const float *s) { return narrow2<DT>(f32x2{s[0], s[1]}); }
+
+// c + the two values of a packed pair
+template <int DT> __device__ __forceinline__ float pair_sum(uint32_t w, float c) {
+  if constexpr (DT == DT_F16)
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), __builtin_bit_cast(f16x2, 0x3C003C00u), c, false);
+  else
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, 0x3F803F80u), c,
+                                           false);
+}
+
 // One chunk of a row of D elements at p, zeros past its end and for no row.
 template <int DT> __device__ __forceinline__ u32x4 load_chunk(const void *p, int64_t row, int c, int D, bool any) {
   const int e = c * kVec<DT>;

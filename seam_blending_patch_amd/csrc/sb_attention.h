@@ -21,6 +21,7 @@ struct AttnArgs {
   float *lse;             // [B, heads of q, Lq] natural logarithms (nullptr: not wanted, forward)
   float *delta;           // [B, heads of q, Lq] row sums of dout * out (backward)
   float *part, *part_lse; // partial results of the splits, [splits][units][rows or keys][D] (part_lse: no D)
+  float *part_mean, *part_left; // of dq's rows in 16 bits: [splits][units][rows][D] and [splits][units][rows][2]
   const int32_t *q_len, *k_len; // of each sample, or nullptr
   int32_t B, Lq, Lk, Hk, group, D;
   int32_t rows;           // Lq * group
@@ -53,11 +54,15 @@ __host__ __device__ constexpr bool attn_pipelined(int elem_bytes, int padded) {
 }
 
 // columns of 32 rows of a wave of those for dq, at most (their registers)
-__host__ __device__ constexpr int attn_columns(int padded) { return padded <= 128 ? 2 : 1; }
+__host__ __device__ constexpr int attn_columns(int padded) { return padded <= 64 ? 2 : 1; }
 
 // keys of a block of the key gradients: 32 a wave, or a pair of waves where a
 // head's two halves go to two of them
 __host__ __device__ constexpr bool attn_paired(int elem_bytes, int padded) { return padded * elem_bytes > (elem_bytes == 2 ? 384 : 640); }
+
+// dq's kernel that takes any head: two waves to a row (16 bits, whose rows have a second
+// sum; one wave spills: 4096 tokens of 8 heads of 256 bf16, gradient 2.71 ms, 1.32 so)
+__host__ __device__ constexpr bool attn_dq_paired(int elem_bytes, int padded) { return elem_bytes == 2 && padded >= 192; }
 
 } // namespace sb
 
@@ -68,6 +73,8 @@ hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, i
 hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, int whole, hipStream_t st);
 // joins the splits of the forward pass
 hipError_t sb_launch_attention_join(const sb::AttnArgs &a, int dtype, hipStream_t st);
+// dq of 16 bits from its splits, and delta with what they leave
+hipError_t sb_launch_attention_dq_join(const sb::AttnArgs &a, int dtype, hipStream_t st);
 // adds up a.splits splits of n (1 or 2) gradients of the same shape: partial
 // results [n][splits][units][len][D] to out[k], rows r of a unit at position
 // r / group of head hk * group + r % group

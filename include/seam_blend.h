@@ -419,11 +419,13 @@ size_t attention_backward_workspace_bytes(const int64_t shape[6], int dtype);
  *                none with each other or an input (checked; SB_EARG).  Zeros where a
  *                length, or causal order, leaves nothing.
  * Other arguments as attention_forward's.  P and dS are rounded to dtype for the
- * products they enter (in fp16 what is below 6e-8 vanishes: scale the loss): in 16 bits
- * the gradients are about 1.4 times as far off as their last rounding alone would leave
- * them.  What out was rounded to does not matter (its row sums with dout are corrected
- * by what dS adds up to).  The
- * heads that share a key head are added up in fp32, in a fixed order: deterministic.
+ * products they enter: in 16 bits the gradients are about 1.4 times as far off as
+ * their last rounding alone would leave them.  What out was rounded to does not matter
+ * (its row sums with dout are corrected by what dS adds up to).  In fp16 both are
+ * lifted by powers of two that go by dout's norm (dq: its row's, dk: the largest of its
+ * rows), so that its scale does not matter while the results are in fp16's range and
+ * values have norms up to 2000.  The heads that share a key head are added up in fp32,
+ * in a fixed order: deterministic.
  */
 int attention_backward(const void *dout, const int64_t dout_stride[3], const void *q, const int64_t q_stride[3],
                        const void *k, const int64_t k_stride[3], const void *v, const int64_t v_stride[3],

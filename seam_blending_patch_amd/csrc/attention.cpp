@@ -182,6 +182,9 @@ int64_t keys_part(const sb::AttnArgs &a, const Plan &p) {
   return p.splits > 1 ? up(2 * p.splits * a.B * a.Hk * (int64_t)a.Lk * a.D, 4) : 0;
 }
 int64_t delta_floats(const sb::AttnArgs &a) { return up((int64_t)a.B * a.Hk * a.rows, 4); }
+int64_t peak_floats(const sb::AttnArgs &a, int dtype) {
+  return dtype == SB_F16 ? up((int64_t)a.B * a.Hk * ((a.rows + 31) / 32), 4) : 0;
+}
 
 // (the workspace's size goes by the shape alone: the largest need)
 int64_t forward_floats(const sb::AttnArgs &a, int dtype) {
@@ -201,7 +204,7 @@ int64_t backward_floats(const sb::AttnArgs &a, int dtype) {
       most = std::max(most, rows_part(a, p) + rows_part_mean(a, p, dtype) + rows_part_left(a, p, dtype));
     }
   }
-  return delta_floats(a) + most;
+  return delta_floats(a) + peak_floats(a, dtype) + most;
 }
 
 int check_workspace(const void *workspace, size_t bytes, int64_t need) {
@@ -331,7 +334,8 @@ extern "C" int attention_backward(const void *dout, const int64_t dout_stride[3]
   a.causal = causal != 0;
   a.lse = const_cast<float *>(lse); // only read
   a.delta = (float *)workspace;
-  float *const part = a.delta + delta_floats(a);
+  a.peak = a.delta + delta_floats(a);
+  float *const part = a.peak + peak_floats(a, dtype);
   const hipStream_t st = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (a.Lq > 0) {

@@ -17,6 +17,63 @@
 namespace sb {
 namespace {
 
+// fp16 reaches from 6e-8 (6e-5 at full precision) to 65504 only, so what is packed into
+// it is lifted by powers of two that the results are divided by again: P by 2^14, and dS
+// by 2^4 over the norm of its row's dout (dk's kernel: the largest of its rows), rounded
+// up to a power of two, less where out's norm passes 2^8.  |dS| <= P |dout| (|v| + |out|),
+// so nothing passes fp16's range while values have norms up to 2000, however dout is
+// scaled; and dS keeps full precision down to 4e-6 of dout's norm.  (dout of 1e-3 over
+// 4096 keys of heads of 128, emulated: dq's error 2.8e-4, 9e-4 without.)  The loops have as
+// many instructions with it: lifts are part of the log sums, and of a multiply-add in place
+// of a subtraction (1537, 769 and 0 causal tokens 110 -> 112 us).
+template <int DT> constexpr bool kLifts = DT == DT_F16;
+template <int DT> constexpr int kLiftP = kLifts<DT> ? 14 : 0;
+constexpr int kLiftS = 4;
+struct Lift {
+  float by, undo; // of dp - delta beside P's, of dS
+  // the square of dout's norm, larger where out's norm is large
+  static __device__ __forceinline__ float size(float dout_square, float out_square) {
+    return dout_square * fmaxf(1.0f, out_square * 0x1p-16f);
+  }
+  // the power of two, at most 33 in size, that the norm is rounded up to (0 for infinity and NaN)
+  static __device__ __forceinline__ int power(float square) { return (__builtin_amdgcn_frexp_expf(square) + 1) >> 1; }
+  template <int DT> static __device__ __forceinline__ Lift of(int power) {
+    if constexpr (!kLifts<DT>) return Lift{1.0f, 1.0f};
+    return Lift{__int_as_float((127 + kLiftS - kLiftP<DT> - power) << 23), __int_as_float((127 + power - kLiftS) << 23)};
+  }
+};
+// P (dp - delta): of P as lifted, and delta times `by`
+template <int DT> __device__ __forceinline__ float gradient_of(float p, float dp, float delta, float by) {
+  if constexpr (kLifts<DT>) return p * __builtin_fmaf(dp, by, -delta);
+  else return p * (dp - delta);
+}
+// the largest size of the 32 rows of a wave's column, for dk's kernel
+__device__ __forceinline__ void store_peak(const AttnArgs &a, const Work &w, int row0, int lane, float square) {
+#pragma unroll
+  for (int k = 16; k; k >>= 1) square = fmaxf(square, __shfl_xor(square, k));
+  if (lane == 0 && w.split == 0 && row0 < a.rows) a.peak[(int64_t)w.unit * ((a.rows + 31) / 32) + row0 / 32] = square;
+}
+// and the power of that of rows begin (a multiple of 32) to end - 1 (none: 0), for a block
+__device__ __forceinline__ int read_peak(const AttnArgs &a, const Work &w, int begin, int end, float *lds) {
+  const float *const peak = a.peak + (int64_t)w.unit * ((a.rows + 31) / 32);
+  const int blocks = (end + 31) / 32;
+  float most = 0.0f;
+  for (int i0 = begin / 32 + (int)threadIdx.x; i0 < blocks; i0 += 4 * 64 * kAttnWaves) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = peak[min(i0 + j * 64 * kAttnWaves, blocks - 1)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) most = fmaxf(most, v[j]);
+  }
+#pragma unroll
+  for (int k = 32; k; k >>= 1) most = fmaxf(most, __shfl_xor(most, k));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = most;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAttnWaves; ++i) most = fmaxf(most, lds[i]);
+  return __builtin_amdgcn_readfirstlane(Lift::power(most)); // (the same in every lane)
+}
+
 // What a row of dq still needs when its keys are done, in 16 bits (fp32: out's rounding
 // is one of fp32, nothing is left).  delta is formed of an `out` that was rounded, and
 // each dS was: with r = the sum of the row's dS, which is zero but for these,
@@ -37,13 +94,14 @@ template <int DT> struct Left {
 // is left, and delta.
 template <int DT, int NB, int NM>
 __device__ __forceinline__ void store_dq(const AttnArgs &a, const Work &w, int row, int h, int db0, bool live, float delta,
-                                         Left<DT> left, f32x16 (&dq)[NB], const f32x16 (&mean)[NM]) {
+                                         float undo, Left<DT> left, f32x16 (&dq)[NB], const f32x16 (&mean)[NM]) {
+  constexpr float kUnlift = 1.0f / (1 << kLiftP<DT>);
   if constexpr (kMeanOf<DT>) {
     left.rounded = half_sum(left.rounded);
-    left.exact = half_sum(left.exact);
+    left.exact = half_sum(left.exact) * undo;
   }
   if (row >= a.rows) return;
-  const float by = live ? a.scale : 0.0f;
+  const float by = live ? a.scale * undo : 0.0f;
   const bool first = h == 0 && db0 == 0;
   if (a.part) {
     const int64_t at = ((int64_t)w.split * a.B * a.Hk + w.unit) * a.rows + row;
@@ -53,16 +111,17 @@ __device__ __forceinline__ void store_dq(const AttnArgs &a, const Work &w, int r
     if constexpr (kMeanOf<DT>) {
 #pragma unroll
       for (int db = 0; db < NB; ++db)
-        store_column<DT_F32>(a.part_mean, at * a.D, db0 + db, h, a.D, live ? mean[db] : f32x16{0}, by);
+        store_column<DT_F32>(a.part_mean, at * a.D, db0 + db, h, a.D, live ? mean[db] : f32x16{0}, a.scale * kUnlift);
       if (first) {
         float *const to = a.part_left + 2 * at;
-        to[0] = live ? left.rounded : 0.0f;
+        to[0] = live ? left.rounded * undo : 0.0f;
         to[1] = live ? left.exact : 0.0f;
       }
     }
     if (live && first && w.split == 0) a.delta[stat_at(a, w.b, w.hk, row)] = delta;
   } else {
     const int64_t at = row_at(a.dq, a, w.b, w.hk, row);
+    left.rounded *= kUnlift;
 #pragma unroll
     for (int db = 0; db < NB; ++db) {
       if constexpr (kMeanOf<DT>) {
@@ -109,7 +168,7 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
   const int wend = wlast < wr0 ? 0 : min(seen(wlast), end);
 
   u32x4 qf[NF], gf[NF];
-  float delta = 0.0f, lse2 = kInf; // (a row that sees no key, or is none: its probabilities are exp2(-inf))
+  float delta = 0.0f, square = 0.0f, out_square = 0.0f, lse2 = kInf; // (a row that sees no key, or is none: its probabilities are exp2(-inf))
   Left<DT> left = {};
   {
     const int64_t at = live ? row_at(a.q, a, w.b, w.hk, row) : 0, to = live ? row_at(a.out, a, w.b, w.hk, row) : 0,
@@ -124,21 +183,41 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
       unpack<DT, 16>(Vec<16>{of[0], of[1], of[2], of[3]}, f);
       unpack<DT, 16>(Vec<16>{gf[u][0], gf[u][1], gf[u][2], gf[u][3]}, g);
 #pragma unroll
-      for (int i = 0; i < T::V; ++i) delta = __builtin_fmaf(f[i], g[i], delta);
+      for (int i = 0; i < T::V; ++i) {
+        delta = __builtin_fmaf(f[i], g[i], delta);
+        if constexpr (kLifts<DT>) {
+          square = __builtin_fmaf(g[i], g[i], square);
+          out_square = __builtin_fmaf(f[i], f[i], out_square);
+        }
+      }
     }
     delta = half_sum(delta);
+    if constexpr (kLifts<DT>) {
+      square = half_sum(square);
+      out_square = half_sum(out_square);
+    }
     if constexpr (PAIR) {
       halves[wave][0][lane] = delta;
+      halves[wave][1][lane] = square;
+      halves[wave][2][lane] = out_square;
       __syncthreads();
       delta += halves[wave ^ 1][0][lane];
+      square += halves[wave ^ 1][1][lane];
+      out_square += halves[wave ^ 1][2][lane];
       __syncthreads();
+    }
+    if constexpr (kLifts<DT>) {
+      square = Lift::size(square, out_square);
+      if (part == 0) store_peak(a, w, wr0, lane, square);
     }
     if (live) {
       const int64_t st = stat_at(a, w.b, w.hk, row);
       const float lse = a.lse[st];
-      if (lse != -kInf) lse2 = lse * kLog2e;
+      if (lse != -kInf) lse2 = lse * kLog2e - kLiftP<DT>;
     }
   }
+  const Lift lift = Lift::of<DT>(Lift::power(square));
+  const float lifted = delta * lift.by;
   f32x16 dq[NB], mean[kMean ? NB : 1];
 #pragma unroll
   for (int db = 0; db < NB; ++db) dq[db] = f32x16{0};
@@ -194,7 +273,7 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], a.scale2, -lse2));
-        ds[i] = p[i] * (dp[i] - delta);
+        ds[i] = gradient_of<DT>(p[i], dp[i], lifted, lift.by);
       }
       if (k0 + KT > sure) {
 #pragma unroll
@@ -229,7 +308,7 @@ __global__ __launch_bounds__(64 * NW) void dq_kernel(const AttnArgs a) {
     }
   }
 
-  store_dq<DT, NB>(a, w, row, h, part * NB, live, delta, left, dq, mean);
+  store_dq<DT, NB>(a, w, row, h, part * NB, live, delta, lift.undo, left, dq, mean);
 }
 
 // dk and dv.  A lane has a key: S = Q K^T and dOut V^T put the rows into its
@@ -248,6 +327,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
   __shared__ alignas(1024) char lds[kBufs * 2 * T::kBytes]; // of each buffer q, then dout
   __shared__ alignas(16) float stats[kBufs][2][RT]; // log sums (base 2) and deltas
   __shared__ float halves[PAIR ? kAttnWaves : 1][PAIR ? 32 : 1][64];
+  __shared__ float peaks[kAttnWaves];
 
   const Work w = work_of<false>(a);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, n = lane & 31;
@@ -277,6 +357,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
   const auto g_at = [&](int r) { return row_at(a.dout, a, w.b, w.hk, r); };
   const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
   St sq, sg;
+  Lift lift = Lift::of<DT>(0);
+  if constexpr (kLifts<DT>) lift = Lift::of<DT>(read_peak(a, w, begin, end, peaks));
   float stat[2];
   const auto load_stats = [&](int r) { // of row r + thread
     stat[0] = kInf;                    // (no row: no probability)
@@ -285,8 +367,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
     if (threadIdx.x < RT && at < live_rows) {
       const int64_t st = stat_at(a, w.b, w.hk, at);
       const float lse = a.lse[st];
-      if (lse != -kInf) stat[0] = lse * kLog2e;
-      stat[1] = a.delta[st];
+      if (lse != -kInf) stat[0] = lse * kLog2e - kLiftP<DT>;
+      stat[1] = a.delta[st] * lift.by;
     }
   };
   const auto store_stats = [&](int buf) {
@@ -349,7 +431,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           p[4 * j + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * j + i], a.scale2, -l4[i]));
-          ds[4 * j + i] = p[4 * j + i] * (dp[4 * j + i] - d4[i]);
+          ds[4 * j + i] = gradient_of<DT>(p[4 * j + i], dp[4 * j + i], d4[i], lift.by);
         }
       }
       if (r0 < wsure) { // causal: some row of the tile does not see some key of the wave
@@ -381,7 +463,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
   }
 
   if (key >= a.Lk) return;
-  const float by = live ? a.scale : 0.0f;
+  const float by = live ? a.scale * lift.undo : 0.0f;
+  constexpr float kUnlift = 1.0f / (1 << kLiftP<DT>);
   const int64_t units = (int64_t)a.B * a.Hk, at = ((int64_t)w.split * units + w.unit) * a.Lk + key;
 #pragma unroll
   for (int db = 0; db < NB; ++db) {
@@ -389,10 +472,10 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
     const int d = db + part * NB;
     if (a.part) {
       store_column<DT_F32>(a.part, at * a.D, d, h, a.D, k, by);
-      store_column<DT_F32>(a.part, ((int64_t)a.splits * units * a.Lk + at) * a.D, d, h, a.D, v, 1.0f);
+      store_column<DT_F32>(a.part, ((int64_t)a.splits * units * a.Lk + at) * a.D, d, h, a.D, v, kUnlift);
     } else {
       store_column<DT>((void *)a.dk.p, w.b * a.dk.b + w.hk * a.dk.h + key * a.dk.t, d, h, a.D, k, by);
-      store_column<DT>((void *)a.dv.p, w.b * a.dv.b + w.hk * a.dv.h + key * a.dv.t, d, h, a.D, v, 1.0f);
+      store_column<DT>((void *)a.dv.p, w.b * a.dv.b + w.hk * a.dv.h + key * a.dv.t, d, h, a.D, v, kUnlift);
     }
   }
 }
@@ -448,7 +531,8 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
   const int end = last < r0 ? 0 : min(seen(last), begin + a.span);
 
   u32x4 qf[R][NF], gf[R][NF];
-  float delta[R], lse2[R];
+  float delta[R], lse2[R], lifted[R];
+  Lift lift[R];
   int sees[R];
 #pragma unroll
   for (int c = 0; c < R; ++c) {
@@ -457,7 +541,7 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
     sees[c] = live ? seen(row) : klen;
     const int64_t at = live ? row_at(a.q, a, w.b, w.hk, row) : 0, to = live ? row_at(a.out, a, w.b, w.hk, row) : 0,
                   gt = live ? row_at(a.dout, a, w.b, w.hk, row) : 0;
-    float d = 0.0f;
+    float d = 0.0f, square = 0.0f, out_square = 0.0f;
 #pragma unroll
     for (int u = 0; u < NF; ++u) {
       qf[c][u] = load_chunk<DT>(a.q.p, at, 2 * u + h, a.D, live);
@@ -467,14 +551,26 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
       unpack<DT, 16>(Vec<16>{of[0], of[1], of[2], of[3]}, f);
       unpack<DT, 16>(Vec<16>{gf[c][u][0], gf[c][u][1], gf[c][u][2], gf[c][u][3]}, g);
 #pragma unroll
-      for (int i = 0; i < T::V; ++i) d = __builtin_fmaf(f[i], g[i], d);
+      for (int i = 0; i < T::V; ++i) {
+        d = __builtin_fmaf(f[i], g[i], d);
+        if constexpr (kLifts<DT>) {
+          square = __builtin_fmaf(g[i], g[i], square);
+          out_square = __builtin_fmaf(f[i], f[i], out_square);
+        }
+      }
     }
     delta[c] = half_sum(d);
+    if constexpr (kLifts<DT>) {
+      square = Lift::size(half_sum(square), half_sum(out_square));
+      store_peak(a, w, wr0 + 32 * c, lane, square);
+    }
+    lift[c] = Lift::of<DT>(Lift::power(square));
+    lifted[c] = delta[c] * lift[c].by;
     lse2[c] = kInf; // (a row that sees no key, or is none: its probabilities are exp2(-inf))
     if (live) {
       const int64_t st = stat_at(a, w.b, w.hk, row);
       const float lse = a.lse[st];
-      if (lse != -kInf) lse2[c] = lse * kLog2e;
+      if (lse != -kInf) lse2[c] = lse * kLog2e - kLiftP<DT>;
     }
   }
   f32x16 dq[R][NB], mean[R][NB];
@@ -569,7 +665,7 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
 #pragma unroll
                 for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e) {
                   p[c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e], a.scale2, -lse2[c]));
-                  ds[c][e] = p[c][e] * (dp[c][e] - delta[c]);
+                  ds[c][e] = gradient_of<DT>(p[c][e], dp[c][e], lifted[c], lift[c].by);
                 }
                 if (j == -1) {
                   if (k0 + KT > sure) {
@@ -605,7 +701,7 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
 #pragma unroll
   for (int c = 0; c < R; ++c) {
     const int row = wr0 + 32 * c + n;
-    store_dq<DT, NB>(a, w, row, h, 0, row < live_rows, delta[c], left[c], dq[c], mean[c]);
+    store_dq<DT, NB>(a, w, row, h, 0, row < live_rows, delta[c], lift[c].undo, left[c], dq[c], mean[c]);
   }
 }
 
@@ -617,6 +713,7 @@ template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv
   constexpr int NF = T::kFrags, NB = DP / 32;
   __shared__ alignas(1024) char lds[3 * 2 * T::kBytes]; // of each buffer q, then dout
   __shared__ alignas(16) float stats[3][2][RT];         // log sums (base 2) and deltas
+  __shared__ float peaks[kAttnWaves];
 
   const Work w = work_of<false>(a);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, n = lane & 31;
@@ -640,6 +737,8 @@ template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv
 #pragma unroll
   for (int db = 0; db < NB; ++db) dk[db] = dv[db] = f32x16{0};
 
+  Lift lift = Lift::of<DT>(0);
+  if constexpr (kLifts<DT>) lift = Lift::of<DT>(read_peak(a, w, begin, end, peaks));
   u32x4 sq[S::N], sg[S::N];
   float stat[2];
   const bool any = S::chunk() * T::V < a.D && !(S::kIdle && S::row(0) >= RT);
@@ -683,8 +782,8 @@ template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv
     }
     if (threadIdx.x < RT) {
       // (no row, or one without keys: no probability)
-      stats[buffer][0][threadIdx.x] = r + (int)threadIdx.x >= live_rows || stat[0] == -kInf ? kInf : stat[0] * kLog2e;
-      stats[buffer][1][threadIdx.x] = stat[1];
+      stats[buffer][0][threadIdx.x] = r + (int)threadIdx.x >= live_rows || stat[0] == -kInf ? kInf : stat[0] * kLog2e - kLiftP<DT>;
+      stats[buffer][1][threadIdx.x] = stat[1] * lift.by;
     }
   };
   const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
@@ -747,7 +846,7 @@ template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv
 #pragma unroll
               for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e) {
                 p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.scale2, -lse2[e >> 2][e & 3]));
-                ds[e] = p[e] * (dp[e] - delta[e >> 2][e & 3]);
+                ds[e] = gradient_of<DT>(p[e], dp[e], delta[e >> 2][e & 3], lift.by);
               }
               if (j == -1) {
                 if (r0 < wsure) { // causal: some row of the tile does not see some key of the wave
@@ -774,17 +873,18 @@ template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv
   }
 
   if (key >= a.Lk) return;
-  const float by = live ? a.scale : 0.0f;
+  const float by = live ? a.scale * lift.undo : 0.0f;
+  constexpr float kUnlift = 1.0f / (1 << kLiftP<DT>);
   const int64_t units = (int64_t)a.B * a.Hk, at = ((int64_t)w.split * units + w.unit) * a.Lk + key;
 #pragma unroll
   for (int db = 0; db < NB; ++db) {
     const f32x16 k = live ? dk[db] : f32x16{0}, v = live ? dv[db] : f32x16{0};
     if (a.part) {
       store_column<DT_F32>(a.part, at * a.D, db, h, a.D, k, by);
-      store_column<DT_F32>(a.part, ((int64_t)a.splits * units * a.Lk + at) * a.D, db, h, a.D, v, 1.0f);
+      store_column<DT_F32>(a.part, ((int64_t)a.splits * units * a.Lk + at) * a.D, db, h, a.D, v, kUnlift);
     } else {
       store_column<DT>((void *)a.dk.p, w.b * a.dk.b + w.hk * a.dk.h + key * a.dk.t, db, h, a.D, k, by);
-      store_column<DT>((void *)a.dv.p, w.b * a.dv.b + w.hk * a.dv.h + key * a.dv.t, db, h, a.D, v, 1.0f);
+      store_column<DT>((void *)a.dv.p, w.b * a.dv.b + w.hk * a.dv.h + key * a.dv.t, db, h, a.D, v, kUnlift);
     }
   }
 }

@@ -20,6 +20,7 @@ struct AttnArgs {
   AttnHeads q, k, v, out, dout, dq, dk, dv; // out and the gradients are written (out only forward)
   float *lse;             // [B, heads of q, Lq] natural logarithms (nullptr: not wanted, forward)
   float *delta;           // [B, heads of q, Lq] row sums of dout * out (backward)
+  float *peak;            // [units][32 rows] fp16: the largest size of their dS (backward)
   float *part, *part_lse; // partial results of the splits, [splits][units][rows or keys][D] (part_lse: no D)
   float *part_mean, *part_left; // of dq's rows in 16 bits: [splits][units][rows][D] and [splits][units][rows][2]
   const int32_t *q_len, *k_len; // of each sample, or nullptr

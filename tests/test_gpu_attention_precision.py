@@ -23,15 +23,17 @@ def sb():
     return m
 
 
-def backward(dout, q, k, v, out, scale, causal, q_len=None, k_len=None):
-    """((dq, dk), tolerances).  With delta' the row sums of dout and the rounded out,
+def backward(dout, q, k, v, out, scale, causal, q_len=None, k_len=None, tiny=None):
+    """((dq, dk), tolerances); tiny: what P, dS of dq and dS of dk may lose below the
+    normal numbers (arrays of [B, heads, Lq, 1]), by default fp16's.  With delta' the row sums of dout and the rounded out,
     dS' = P (dp - delta') is off by E = |delta - delta'| times P, which its own sum takes
     out again:
       dq = sum dS' k - r m, r = sum dS' (rounded), m = sum P k (P rounded);
       dk = sum P (dp - delta' - sum dS') q.
     So E itself is nowhere an error, but dS' and P are rounded (h of each), and r and m
     take those roundings along."""
-    dt, h, tiny = q.dtype, ref.HALF[q.dtype], ref.TINY[q.dtype]
+    dt, h = q.dtype, ref.HALF[q.dtype]
+    tinies = [np.full((q.shape[0], q.shape[2], q.shape[1], 1), ref.TINY[dt])] * 3 if tiny is None else tiny
     ql, kl = ref.lengths(q_len, k_len, q, k)
     group, d = q.shape[2] // k.shape[2], q.shape[3]
     dq, dk = np.zeros(q.shape), np.zeros(k.shape)
@@ -40,6 +42,7 @@ def backward(dout, q, k, v, out, scale, causal, q_len=None, k_len=None):
     for b, (nq, nk) in enumerate(zip(ql, kl)):
         for x in range(q.shape[2] if nq and nk else 0):
             y = x // group
+            tiny_p, tiny_q, tiny_k = (t[b, x, :nq] for t in tinies)
             qq, kk, vv, gg, oo = q[b, :nq, x], k[b, :nk, y], v[b, :nk, y], g[b, :nq, x], out[b, :nq, x]
             p, ls, off, seen = ref.probabilities(qq, kk, scale, causal, dt)
             off = off + 4 * U * np.abs(np.where(np.isfinite(ls), ls, 0.0))[:, None]
@@ -51,15 +54,15 @@ def backward(dout, q, k, v, out, scale, causal, q_len=None, k_len=None):
             most = np.abs(ds) + p * e  # |dS'|
             own = (d + 8) * U * size + 4 * U * (np.abs(dp) + np.abs(near))  # of dp - delta', before the rounding
             err = off * most + p * own
-            rounded = err + (h + 2 * U) * (most + err) + tiny * seen + (nk + 8) * U * most
-            e_p = (off + h + (nk + 8) * U) * p + tiny * seen
+            rounded = err + (h + 2 * U) * (most + err) + tiny_q * seen + (nk + 8) * U * most
+            e_p = (off + h + (nk + 8) * U) * p + tiny_p * seen
             m = p @ np.abs(kk)
             dq[b, :nq, x] = scale * ds @ kk
             tq[b, :nq, x] = scale * (rounded @ np.abs(kk) + rounded.sum(1, keepdims=True) * (m + e_p @ np.abs(kk))
                                      + e * (e_p @ np.abs(kk)) + 4 * U * e * m)
             e_sum = (err + (nk + 8) * U * most).sum(1, keepdims=True) + 2 * U * np.abs(delta)
             err = off * np.abs(ds) + p * (own + e_sum)
-            err = err + (h + 2 * U) * (np.abs(ds) + err) + tiny * seen
+            err = err + (h + 2 * U) * (np.abs(ds) + err) + tiny_k * seen
             rows = nq * group
             dk[b, :nk, y] += scale * ds.T @ qq
             tk[b, :nk, y] += scale * ((err + (rows + 8) * U * np.abs(ds)).T @ np.abs(qq))

@@ -153,15 +153,18 @@ template <int DT, int DP, int KT> struct Softmax {
       for (int db = 0; db < NB; ++db) o[db] = o[db] * by;
     }
     const float base = m == -kInf ? 0.0f : -m * scale2;
+    // (a tile's own sum first: small weights behind a large one would be lost one by one)
+    float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], scale2, base));
-        l += s[j][i];
+        sum += s[j][i];
       }
       pack_operand<DT>(s[j], p[j]);
     }
+    l += sum;
   }
   template <int NW> __device__ __forceinline__ void finish(const AttnArgs &a, const Rows<NW> &r) {
     if (r.row >= a.rows) return;

@@ -1,0 +1,44 @@
+"""attention where most of the keys have weights far below the largest one."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+KEYS, GAP = 30000, 17.5
+
+
+@pytest.fixture(scope="module")
+def sb():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import seam_blending_patch_amd as m
+    return m
+
+
+def sink(queries, d, at, dtype):
+    """one key with a value of 0 and a weight of nearly 1, 29999 others of 2.5e-8 each with
+    values of 1; and what these weigh in all, 7.5e-4.  Queries alike: every row says the
+    same; few rows take splits, 140000 the blocks of eight waves."""
+    q = torch.zeros(1, queries, 1, d, dtype=dtype)
+    k, v = torch.zeros(1, KEYS, 1, d, dtype=dtype), torch.ones(1, KEYS, 1, d, dtype=dtype)
+    q[..., 0], k[0, at, 0, 0], v[0, at] = 1.0, GAP, 0.0
+    rest = (KEYS - 1) * torch.exp(torch.tensor(-GAP, dtype=torch.float64))
+    return q.cuda(), k.cuda(), v.cuda(), rest.item()
+
+
+PLACES = [(n, d, at) for n in (1, 40, 300) for d in (64, 128, 160, 256) for at in (0, 11111, 29999)] \
+    + [(140000, d, 11111) for d in (64, 128, 160)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("queries,d,at", [p for p in PLACES if p[1] in (64, 128)], ids=str)
+def test_the_log_sum(sb, queries, d, at, dtype):
+    """a tile's weights (16 or 32 of a lane) are added up before they are added to the
+    rest: at most KEYS / 32 + 32 roundings of the whole in fp32, and a few of the score's
+    and the logarithm's"""
+    q, k, v, rest = sink(queries, d, at, dtype)
+    _, lse = sb.attention(q, k, v, scale=1.0, return_lse=True)
+    want = GAP + torch.log1p(torch.tensor(rest, dtype=torch.float64)).item()
+    assert (lse.double() - want).abs().max().item() <= (KEYS / 32 + 32) * 2.0 ** -24 + 8 * 2.0 ** -24 * GAP

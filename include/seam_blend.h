@@ -395,8 +395,9 @@ int grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *n
  *                bytes, 16-byte aligned; not looked at where that is 0.  Contents
  *                need not be initialised.
  * A query that sees no key has a row of zeros and lse -inf.  Scores, softmax
- * statistics and sums are fp32; probabilities (times a power of two) are rounded to
- * dtype for the product with v, and out once.  Any element alignment is taken;
+ * statistics and sums are fp32; probabilities (times a power of two, in fp16 one that
+ * keeps those down to 2^-32 of the largest) are rounded to dtype for the product with
+ * v, and out once.  Any element alignment is taken;
  * 16-byte aligned rows are fastest.  Deterministic.
  */
 int attention_forward(const void *q, const int64_t q_stride[3], const void *k, const int64_t k_stride[3],

@@ -50,6 +50,10 @@ template <int NW> struct Rows {
 template <int DT, int DP, int KT> struct Softmax {
   using T = Tile<DT, DP, KT>;
   static constexpr int NS = KT / 32, NB = DP / 32, PW = DT == DT_F32 ? 16 : 8;
+  // fp16: P and its sum are held times 2^7, up to 2^15, so that keys of 2^-32 of the
+  // largest weight still count (one key of weight 1 and 30000 of 3e-8, whose values are
+  // all the result, are lost without)
+  static constexpr int kLift = DT == DT_F16 ? 7 : 0;
   u32x4 qf[T::kFrags];
   f32x16 o[NB];
   float m, l; // m: of the scores before scaling; l: of this lane's half of the keys
@@ -143,8 +147,8 @@ template <int DT, int DP, int KT> struct Softmax {
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
     mx = half_max(mx);
     // The running maximum only has to keep exp2 in range: it moves when some row's
-    // has grown by 2^8 or more (P is then at most 2^8, which 16 bits hold as exactly
-    // as 1), which spares most tiles the turn over O.
+    // has grown by 2^8 or more (P is at most 2^8 in between, which 16 bits hold as
+    // exactly as 1), which spares most tiles the turn over O.
     if (__any(mx > m + slack)) {
       const float up = fmaxf(m, mx), by = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f((m - up) * scale2);
       m = up;
@@ -152,7 +156,7 @@ template <int DT, int DP, int KT> struct Softmax {
 #pragma unroll
       for (int db = 0; db < NB; ++db) o[db] = o[db] * by;
     }
-    const float base = m == -kInf ? 0.0f : -m * scale2;
+    const float base = m == -kInf ? 0.0f : kLift ? __builtin_fmaf(-m, scale2, (float)kLift) : -m * scale2;
     // (a tile's own sum first: small weights behind a large one would be lost one by one)
     float sum = 0.0f;
 #pragma unroll
@@ -171,7 +175,7 @@ template <int DT, int DP, int KT> struct Softmax {
     l = half_sum(l);
     const bool some = r.live && !(l == 0.0f); // (a NaN goes on)
     const float by = some ? 1.0f / l : 0.0f;
-    const float lse = some ? m * a.scale + logf(l) : -kInf;
+    const float lse = some ? m * a.scale + logf(l * (1.0f / (1 << kLift))) : -kInf;
     if (a.part_lse) {
       const int64_t at = ((int64_t)r.w.split * a.B * a.Hk + r.w.unit) * a.rows + r.row;
       if (r.h == 0) a.part_lse[at] = lse;

@@ -461,9 +461,12 @@ size_t group_norm_workspace_bytes(const int64_t shape[3], int64_t groups, int dt
  *   workspace    caller-owned device scratch, 16-byte aligned, contents need not be
  *                initialised.
  * Any element alignment is taken; 16-byte aligned positions are fastest.
- * Statistics are fp32 about each group's first value and merged by Chan's formula
- * (the merge over blocks in 64 bits), so a mean that is large against the spread
- * costs no accuracy; one rounding to dtype.  Deterministic.  No positions: no-op.
+ * Statistics are fp32, one rounding to dtype.  A group that a block holds in registers
+ * is summed up about its mean; others by batches of 8 positions about their first
+ * value, means kept as two floats, merged by Chan's formula (over blocks in 64 bits).
+ * Either way the first of m's two numbers is m in fp32, and neither a mean that is
+ * large against the spread nor a value far out costs accuracy.  Deterministic.  No
+ * positions: no-op.
  */
 int group_norm_forward(const void *x, const int64_t x_stride[2], const int64_t shape[3], int64_t groups, float eps,
                        const void *gamma, const void *beta, int activation, int dtype, int weight_dtype, void *out,
@@ -479,7 +482,8 @@ int group_norm_forward(const void *x, const int64_t x_stride[2], const int64_t s
  *   dx           may be dy or x themselves, else shares no element with them.
  *   dgamma, dbeta  device pointers to [C] of weight_dtype, or NULL where not wanted;
  *                written, not added to (zeros without positions).
- * Sums are fp32 by block and 64-bit over blocks, in a fixed order.
+ * Sums are fp32 by block and 64-bit over blocks, in a fixed order (groups that a block
+ * holds: their means in fp32, and of one sample dgamma and dbeta too).
  */
 int group_norm_backward(const void *dy, const int64_t dy_stride[2], const void *x, const int64_t x_stride[2],
                         const int64_t shape[3], int64_t groups, const float *stats, const void *gamma,

@@ -117,8 +117,9 @@ int check_types(int activation, int dtype, int wdtype, const void *const *weight
   return SB_OK;
 }
 
-// floats: partials by chunk and channel, then the groups' statistics (or means)
-int64_t part_floats(const sb::ChanArgs &a) { return up(2 * (int64_t)a.N * a.chunks * a.C, 4); }
+// floats: partials by chunk and channel (three forward, two backward), then the groups'
+// statistics (or means)
+int64_t part_floats(const sb::ChanArgs &a) { return up(3 * (int64_t)a.N * a.chunks * a.C, 4); }
 int64_t workspace_bytes(const sb::ChanArgs &a) {
   return (part_floats(a) + up(3 * (int64_t)a.N * a.G, 4)) * (int64_t)sizeof(float);
 }

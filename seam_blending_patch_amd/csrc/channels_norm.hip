@@ -4,9 +4,11 @@
 // A thread keeps one vector of channels and goes along the positions: whatever the
 // group's channels, a block reads whole runs of a position's channels, and sums
 // stay in registers by channel until the block's end.  Bound by memory: two samples
-// of 512 x 512 x 256 fp16 134 us (sums 42, merge 5, result 87 us: 6.4 and 6.2 TB/s,
-// part of both from the caches), the gradient of 256 x 256 x 512 bf16 69 us (27, 5 and
-// 37 us).  A second reading of x (and dy) is the price of groups that no block holds.
+// of 512 x 512 x 256 fp16 136 to 146 us (kernels: sums 44, merge 6, result 92 us: 6.1 and
+// 5.8 TB/s, part of both from the caches).  The gradient of 256 x 256 x 512 bf16 69 to 81 us
+// (36, 7 and 37 us, 3.7 and 5.4 TB/s: its sums are bound by two blocks to a CU and their
+// vector work as much as by memory).  A second reading of x (and dy) is the price of groups
+// that no block holds.
 #include <type_traits>
 
 #include "sb_channels.h"
@@ -41,29 +43,31 @@ template <int DT> __device__ __forceinline__ float value_at(const void *p, int64
   return widen<DT>(((const typename El<DT>::bits *)p)[e]);
 }
 
-// the first part of a group's mean: its first value.  Sums are taken of what is
-// left, so a mean that is large against the spread costs no accuracy.
-template <int DT> __device__ __forceinline__ float group_shift(const ChanArgs &a, int n, int g) {
-  return value_at<DT>(a.x, n * a.sx.n + (int64_t)g * a.Cg);
+// A mean as the unevaluated sum of two floats, so that one that is large against the
+// spread costs no accuracy: moved on by d, and made up again so that the first is the
+// mean in fp32.
+__device__ __forceinline__ void move_mean(float &hi, float &lo, float d) {
+  lo += d;
+  const float s = hi + lo, back = s - hi;
+  lo = (hi - (s - back)) + (lo - back); // (what the sum's rounding left out, whichever is larger)
+  hi = s;
 }
 
 // Statistics of a block's chunk by channel: batches of a thread's positions,
-// each by two passes over its registers, merged (Chan, Golub & LeVeque); then the
-// block's threads by a tree.
+// each by two passes over its registers about its first value, merged (Chan, Golub &
+// LeVeque); then the block's threads by a tree.  A value far out costs digits of its
+// own batch alone, 8 positions of a channel.
 template <int DT, Cover C>
 __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
   constexpr int V = kVec<DT>, R = kChanBatch;
-  __shared__ float lds[2][kChanThreads * V];
+  __shared__ float lds[3][kChanThreads * V];
   const Place p = place_of(a);
   const int e = p.col * V, len = p.s1 - p.s0;
-  float K[V], mean[V], m2[V];
+  float hi[V], lo[V], m2[V];
   int count = 0;
 #pragma unroll
-  for (int k = 0; k < V; ++k) mean[k] = m2[k] = 0.0f;
+  for (int k = 0; k < V; ++k) hi[k] = lo[k] = m2[k] = 0.0f;
   if (p.on) {
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      K[k] = group_shift<DT>(a, p.n, (int)fdiv((uint32_t)min(e + k, a.C - 1), a.div_Cg));
     const int turns = turns_of(len, p.r, a.RB);
     int64_t at = p.n * a.sx.n + (int64_t)(p.s0 + p.r) * a.sx.s;
     const int64_t step = a.RB * a.sx.s;
@@ -72,7 +76,7 @@ __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
 #pragma unroll
       for (int j = 0; j < R; ++j)
         if (decltype(full)::value || j < m) v[j] = request_row<DT, C>(a.x, at + j * step, e, a.C);
-      float s[V];
+      float K[V], s[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) s[k] = 0.0f;
 #pragma unroll
@@ -82,7 +86,10 @@ __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
           float f[V];
           unpack<DT, 16>(v[j], f);
 #pragma unroll
-          for (int k = 0; k < V; ++k) s[k] += f[k] - K[k];
+          for (int k = 0; k < V; ++k) {
+            if (j == 0) K[k] = f[k];
+            else s[k] += f[k] - K[k];
+          }
         }
       const float rm = 1.0f / (float)m;
       float q[V];
@@ -102,12 +109,21 @@ __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
             q[k] = __builtin_fmaf(d, d, q[k]);
           }
         }
-      const float w = (float)m / (float)(count + m), wc = w * (float)count;
+      if (count == 0) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float d = s[k] - mean[k];
-        mean[k] = __builtin_fmaf(d, w, mean[k]);
-        m2[k] += __builtin_fmaf(d * d, wc, q[k]);
+        for (int k = 0; k < V; ++k) {
+          hi[k] = K[k];
+          move_mean(hi[k], lo[k], s[k]);
+          m2[k] = q[k];
+        }
+      } else {
+        const float w = (float)m / (float)(count + m), wc = w * (float)count;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float d = (K[k] - hi[k]) + (s[k] - lo[k]);
+          move_mean(hi[k], lo[k], d * w);
+          m2[k] += __builtin_fmaf(d * d, wc, q[k]);
+        }
       }
       count += m;
       at += R * step;
@@ -124,8 +140,9 @@ __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
     if (p.on && p.r >= s && p.r < 2 * s) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        lds[0][k * kChanThreads + threadIdx.x] = mean[k];
-        lds[1][k * kChanThreads + threadIdx.x] = m2[k];
+        lds[0][k * kChanThreads + threadIdx.x] = hi[k];
+        lds[1][k * kChanThreads + threadIdx.x] = lo[k];
+        lds[2][k * kChanThreads + threadIdx.x] = m2[k];
       }
     }
     __syncthreads();
@@ -138,21 +155,22 @@ __global__ __launch_bounds__(kChanThreads) void stats_kernel(const ChanArgs a) {
         const int from = threadIdx.x + s * a.CV;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-          const float d = lds[0][k * kChanThreads + from] - mean[k];
-          mean[k] = __builtin_fmaf(d, w, mean[k]);
-          m2[k] += __builtin_fmaf(d * d, wc, lds[1][k * kChanThreads + from]);
+          const float d = (lds[0][k * kChanThreads + from] - hi[k]) + (lds[1][k * kChanThreads + from] - lo[k]);
+          move_mean(hi[k], lo[k], d * w);
+          m2[k] += __builtin_fmaf(d * d, wc, lds[2][k * kChanThreads + from]);
         }
         count += theirs;
       }
     }
   }
   if (p.on && p.r == 0) {
-    float *to = a.part + ((int64_t)p.n * a.chunks + p.chunk) * 2 * a.C + e;
+    float *to = a.part + ((int64_t)p.n * a.chunks + p.chunk) * 3 * a.C + e;
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (C != CUT || e + k < a.C) {
-        to[k] = mean[k];
-        to[a.C + k] = m2[k];
+        to[k] = hi[k];
+        to[a.C + k] = lo[k];
+        to[2 * a.C + k] = m2[k];
       }
   }
 }
@@ -176,50 +194,52 @@ __device__ __forceinline__ void block_sums(double &u, double &v, double (*lds)[2
   }
 }
 
-// Calls f(chunk, channel of the group, first, second) with a group's partials, 8 of
-// a thread on their way at a time.
-template <class F> __device__ __forceinline__ void over_partials(const ChanArgs &a, int n, int g, F f) {
-  const float *part = a.part + (int64_t)n * a.chunks * 2 * a.C + g * a.Cg;
+// Calls f(chunk, channel of the group, partials) with a group's partials (W of a chunk
+// and channel), 8 of a thread on their way at a time.
+template <int W, class F> __device__ __forceinline__ void over_partials(const ChanArgs &a, int n, int g, F f) {
+  const float *part = a.part + (int64_t)n * a.chunks * W * a.C + g * a.Cg;
   const int items = a.chunks * a.Cg;
   for (int i0 = threadIdx.x; i0 < items; i0 += 8 * kMergeThreads) {
-    float u[8], v[8];
+    float v[8][W];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = min(i0 + j * kMergeThreads, items - 1), chunk = (int)fdiv((uint32_t)i, a.div_Cg);
-      const float *at = part + (int64_t)chunk * 2 * a.C + (i - chunk * a.Cg);
-      u[j] = at[0];
-      v[j] = at[a.C];
+      const float *at = part + (int64_t)chunk * W * a.C + (i - chunk * a.Cg);
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[j][w] = at[w * a.C];
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = i0 + j * kMergeThreads;
       if (i < items) {
         const int chunk = (int)fdiv((uint32_t)i, a.div_Cg);
-        f(chunk, i - chunk * a.Cg, u[j], v[j]);
+        f(chunk, i - chunk * a.Cg, v[j]);
       }
     }
   }
 }
 
 // A group's chunks and channels merged: a block to a group.  In 64 bits the merge of
-// many sets may be taken by sums of squares: the means are of what is left of the
-// group's first value.
+// many sets may be taken by sums of squares, of what the group's first value leaves of
+// the means: that is either near them or, far out of n values, a deviation of its
+// distance over sqrt(n) by itself (n up to 2^30 leaves 2^-23 of the variance).
 template <int DT> __global__ __launch_bounds__(kMergeThreads) void merge_kernel(const ChanArgs a) {
   __shared__ double lds[kMergeThreads / 64][2];
   const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G;
   const double total = (double)a.S * a.Cg;
+  const double first = value_at<DT>(a.x, n * a.sx.n + (int64_t)g * a.Cg);
   double s = 0.0, t = 0.0;
-  over_partials(a, n, g, [&](int chunk, int, float mean, float m2) {
-    const double count = min(a.S, (chunk + 1) * a.chunk) - chunk * a.chunk, m = mean;
+  over_partials<3>(a, n, g, [&](int chunk, int, const float (&v)[3]) {
+    const double count = min(a.S, (chunk + 1) * a.chunk) - chunk * a.chunk, m = ((double)v[0] - first) + (double)v[1];
     s += count * m;
-    t += (double)m2 + count * m * m;
+    t += (double)v[2] + count * m * m;
   });
   block_sums(s, t, lds);
   if (threadIdx.x == 0) {
-    const double mean = s / total, var = fmax(t / total - mean * mean, 0.0);
+    const double rest = s / total, var = fmax(t / total - rest * rest, 0.0), mean = first + rest;
     float *to = a.stats + ((int64_t)n * a.G + g) * 3;
-    to[0] = group_shift<DT>(a, n, g);
-    to[1] = (float)mean;
+    to[0] = (float)mean;
+    to[1] = (float)(mean - (double)to[0]);
     to[2] = (float)(1.0 / sqrt(var + (double)a.eps));
   }
 }
@@ -377,10 +397,10 @@ template <int WT> __global__ __launch_bounds__(kMergeThreads) void gather_kernel
   if ((int)blockIdx.x < a.N * a.G) {
     const int n = blockIdx.x / a.G, g = blockIdx.x - n * a.G;
     double s = 0.0, t = 0.0;
-    over_partials(a, n, g, [&](int, int c, float sg, float sh) {
+    over_partials<2>(a, n, g, [&](int, int c, const float (&v)[2]) {
       const double gamma = a.gamma ? (double)value_at<WT>(a.gamma, g * a.Cg + c) : 1.0;
-      s += gamma * (double)sg;
-      t += gamma * (double)sh;
+      s += gamma * (double)v[0];
+      t += gamma * (double)v[1];
     });
     block_sums(s, t, lds);
     if (threadIdx.x == 0) {

@@ -40,8 +40,8 @@ struct ChanArgs {
   int32_t sg, CS;        // groups held by one block, channels of those (whole vectors); 0: the passes over blocks
   FastDiv div_CVs;       // vectors of those channels
   float *stats;          // [N][G][3]: the mean in two parts, 1 / sigma
-  float *part;           // forward [N][chunks][2][C]: means less the first part, sums of squares about them;
-                         // backward: sums of g and of g h
+  float *part;           // forward [N][chunks][3][C]: means in two parts, sums of squares about them;
+                         // backward [N][chunks][2][C]: sums of g and of g h
   float *coef;           // [N][G][2] backward: the means of gamma g and of gamma g h
   FastDiv div_CV, div_Cg, div_slabs, div_chunks;
   uint32_t block0;       // of this launch

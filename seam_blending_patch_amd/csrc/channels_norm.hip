@@ -236,7 +236,7 @@ template <int DT> __global__ __launch_bounds__(kMergeThreads) void merge_kernel(
   });
   block_sums(s, t, lds);
   if (threadIdx.x == 0) {
-    const double rest = s / total, var = fmax(t / total - rest * rest, 0.0), mean = first + rest;
+    const double rest = s / total, off = t / total - rest * rest, var = off < 0.0 ? 0.0 : off, mean = first + rest; // (NaN stays)
     float *to = a.stats + ((int64_t)n * a.G + g) * 3;
     to[0] = (float)mean;
     to[1] = (float)(mean - (double)to[0]);
@@ -588,8 +588,8 @@ template <int DT, int WT, bool SILU> __global__ __launch_bounds__(kHeldThreads) 
   }
   group_sums<2, V, kHeldThreads>(a.sg, group, d2, lds, sums[1]);
   if ((int)threadIdx.x < a.sg) { // this thread's group is its own number
-    const float e1 = sums[1][0][threadIdx.x] * inv, var = fmaxf(sums[1][1][threadIdx.x] * inv - e1 * e1, 0.0f);
-    const float r = 1.0f / sqrtf(var + a.eps);
+    const float e1 = sums[1][0][threadIdx.x] * inv, off = sums[1][1][threadIdx.x] * inv - e1 * e1;
+    const float r = 1.0f / sqrtf((off < 0.0f ? 0.0f : off) + a.eps); // (NaN stays)
     sums[2][0][threadIdx.x] = e1;
     sums[2][1][threadIdx.x] = r;
     float *to = a.stats + ((int64_t)p.n * a.G + (int)fdiv((uint32_t)p.c0, a.div_Cg) + threadIdx.x) * 3;

@@ -278,12 +278,18 @@ extern "C" int attention_forward(const void *q, const int64_t q_stride[3], const
   a.lse = lse;
   const Plan p = plan_rows(a, dtype, true, a.causal, a.q_len || a.k_len);
   const hipStream_t st = (hipStream_t)stream;
-  // Causal tiles that are resident all at once, two blocks to a CU: the longest
-  // beside the shortest (2049 tokens, 16 heads of 80 in 4 groups of two samples
-  // fp32: 269 us, longest first 315).
+  // Causal tiles of which a CU holds two or more and a unit has one to two and a half
+  // for each of its share of the CUs: the longest beside the shortest, and what is over,
+  // the shortest of all, last.  16 heads in 4 groups of two samples fp32, against longest
+  // first: 1280, 2080 and 2560 tokens of heads of 80 163, 274 and 393 us (172, 320 and
+  // 412), of 32 58, 94 and 138 (63, 121 and 164), of 128 198, 328 and 490 (219, 415 and
+  // 534); 16-bit heads of 40 to 192 the same either way.  Where a CU holds one tile, the
+  // second ones do come second: heads of 160 fp32 285, 607 and 857 (285, 504 and 808), of
+  // 256 bf16 84, 181 and 244 (84, 155 and 236).
   const int64_t units = (int64_t)a.B * a.Hk, beside = sb_cu_count() / units;
   if (a.causal && !a.q_len && !a.k_len && p.waves == sb::kAttnWaves && p.splits == 1 && units <= 8 &&
-      p.tiles > beside && 2 * p.tiles <= 5 * beside)
+      p.tiles > beside && 2 * p.tiles <= 5 * beside &&
+      sb::attn_forward_waves(sb::elem_bytes(dtype), sb::attn_padded(a.D), p.waves) > 1)
     a.beside = (int32_t)beside;
   if (p.splits > 1) {
     a.part = (float *)workspace;

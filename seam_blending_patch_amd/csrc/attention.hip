@@ -5,15 +5,6 @@
 namespace sb {
 namespace {
 
-// Waves of a SIMD that the registers are shared out for: two that take turns at
-// the matrix cores and at the softmax are worth more than any register (128 wide,
-// 20280 rows and keys of 12 heads bf16: 5.94 ms for one, 2.96 for two); longer
-// heads would spill.
-constexpr int forward_waves(int dt, int dp, int nw) {
-  if (dt == DT_F32) return dp <= 32 ? 3 : dp <= 96 || (dp == 128 && nw > 1) ? 2 : 1;
-  return dp <= 64 ? 3 : dp <= 160 || (dp == 192 && nw > 1) ? 2 : 1;
-}
-
 // What a block of NW waves has to do, and a wave and a lane of it: a wave has 32
 // rows (query, head of the group), a lane one of them.
 template <int NW> struct Rows {
@@ -199,7 +190,7 @@ template <int DT, int DP, int KT> struct Softmax {
 // of 80 fp32: 269 us, 80 TFLOP/s where a library product reaches 139 (a twelfth of it
 // for the values' padding to 96, a third for the unequal tiles).
 template <int DT, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, forward_waves(DT, DP, NW)) void attention_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, attn_forward_waves(Elem<DT>::bytes, DP, NW)) void attention_kernel(const AttnArgs a) {
   constexpr int kThreads = 64 * NW;
   constexpr int KT = NW > 1 && Tile<DT, DP, 32>::SC <= 16 ? 64 : 32; // keys of a tile
   using T = Tile<DT, DP, KT>;

@@ -289,8 +289,8 @@ template <bool LAST_FIRST> __device__ __forceinline__ Work work_of(const AttnArg
   k.unit = a.unit0 + first + (in - rest * of);
   k.tile = (int)fdiv(rest, a.div_splits);
   k.split = (int)rest - k.tile * (int)a.div_splits.d;
-  if (a.beside && k.tile >= a.beside) { // the second blocks of the CUs get longer as the first get shorter
-    const int over = max(a.tiles - 2 * a.beside, 0); // (the shortest tiles of all, for whoever is done first)
+  if (a.beside && k.tile >= a.beside) { // the second tiles of the CUs get longer as the first get shorter
+    const int over = max(a.tiles - 2 * a.beside, 0); // (the shortest of all, for whoever is done first)
     k.tile = k.tile < 2 * a.beside ? a.tiles - 1 - over - (k.tile - a.beside) : a.tiles - over + (k.tile - 2 * a.beside);
   }
   if (LAST_FIRST) k.tile = a.tiles - 1 - k.tile;

@@ -32,7 +32,7 @@ struct AttnArgs {
   FastDiv div_group, div_set, div_splits, div_Hk; // (set: the blocks of 8 units)
   uint32_t unit0, units;  // of this launch
   uint32_t blocks;
-  int32_t beside;         // tiles of a unit after which the next share their CUs (0: longest first throughout)
+  int32_t beside;         // tiles of a unit after which the next are put beside them (0: longest first throughout)
   float scale, scale2;    // of the scores, and that times log2(e)
 };
 
@@ -41,6 +41,15 @@ constexpr int64_t kAttnWidth = 256; // longest head
 
 inline int attn_padded(int64_t d) { // head lengths that kernels are built for
   return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : d <= 128 ? 128 : d <= 160 ? 160 : d <= 192 ? 192 : 256;
+}
+
+// Waves of a SIMD that forward's registers are shared out for (blocks of a CU, of
+// kAttnWaves): two that take turns at the matrix cores and at the softmax are worth
+// more than any register (128 wide, 20280 rows and keys of 12 heads bf16: 5.94 ms for
+// one, 2.96 for two); longer heads would spill.
+__host__ __device__ constexpr int attn_forward_waves(int elem_bytes, int padded, int waves) {
+  if (elem_bytes == 4) return padded <= 32 ? 3 : padded <= 96 || (padded == 128 && waves > 1) ? 2 : 1;
+  return padded <= 64 ? 3 : padded <= 160 || (padded == 192 && waves > 1) ? 2 : 1;
 }
 
 // heads for which forward has blocks of twice as many waves too

@@ -47,7 +47,10 @@ template <int DT, int DP, int KT> struct Softmax {
   static constexpr int kLift = DT == DT_F16 ? 7 : 0;
   u32x4 qf[T::kFrags];
   f32x16 o[NB];
-  float m, l; // m: of the scores before scaling; l: of this lane's half of the keys
+  // P = exp2(s scale2 - c): c is near the row's largest exponent so far, less kLift, and is
+  // exactly what the sums were formed with, so that moving them on to another c leaves
+  // none of its rounding in the weights.  l: of this lane's half of the keys.
+  float c, l;
   float s[NS][16];
   uint32_t p[NS][PW];
 
@@ -57,7 +60,7 @@ template <int DT, int DP, int KT> struct Softmax {
     for (int u = 0; u < T::kFrags; ++u) qf[u] = load_chunk<DT>(a.q.p, at, 2 * u + r.h, a.D, r.live);
 #pragma unroll
     for (int db = 0; db < NB; ++db) o[db] = f32x16{0};
-    m = -kInf;
+    c = -kInf;
     l = 0.0f;
   }
   // Steps of the products: first those of P with the values (kMix of them), then
@@ -130,24 +133,26 @@ template <int DT, int DP, int KT> struct Softmax {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[j][i] = 32 * j + 8 * (i >> 2) + (i & 3) < left ? s[j][i] : -kInf;
   }
-  __device__ __forceinline__ void soften(float scale2, float slack) {
+  __device__ __forceinline__ void soften(float scale2) {
     float mx = s[0][0];
 #pragma unroll
     for (int j = 0; j < NS; ++j)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[j][i]);
-    mx = half_max(mx);
-    // The running maximum only has to keep exp2 in range: it moves when some row's
-    // has grown by 2^8 or more (P is at most 2^8 in between, which 16 bits hold as
-    // exactly as 1), which spares most tiles the turn over O.
-    if (__any(mx > m + slack)) {
-      const float up = fmaxf(m, mx), by = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f((m - up) * scale2);
-      m = up;
+    mx = half_max(mx) * scale2 - kLift;
+    // c only has to keep exp2 in range: it moves when some row's largest has grown by
+    // 2^8 or more (P is at most 2^8 in between, which 16 bits hold as exactly as 1), which
+    // spares most tiles the turn over O.  (fp16, exponents so large that their own
+    // rounding counts in powers of two: that is what 2^8 are left to.)
+    const float slack = kLift && !(fabsf(c) < 0x1p20f) ? 0.0f : 8.0f;
+    if (__any(mx > c + slack)) {
+      const float up = fmaxf(c, mx), by = c == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c - up);
+      c = up;
       l *= by;
 #pragma unroll
       for (int db = 0; db < NB; ++db) o[db] = o[db] * by;
     }
-    const float base = m == -kInf ? 0.0f : kLift ? __builtin_fmaf(-m, scale2, (float)kLift) : -m * scale2;
+    const float base = c == -kInf ? 0.0f : -c;
     // (a tile's own sum first: small weights behind a large one would be lost one by one)
     float sum = 0.0f;
 #pragma unroll
@@ -166,7 +171,7 @@ template <int DT, int DP, int KT> struct Softmax {
     l = half_sum(l);
     const bool some = r.live && !(l == 0.0f); // (a NaN goes on)
     const float by = some ? 1.0f / l : 0.0f;
-    const float lse = some ? m * a.scale + logf(l * (1.0f / (1 << kLift))) : -kInf;
+    const float lse = some ? __builtin_fmaf(c, kLn2, logf(l)) : -kInf;
     if (a.part_lse) {
       const int64_t at = ((int64_t)r.w.split * a.B * a.Hk + r.w.unit) * a.rows + r.row;
       if (r.h == 0) a.part_lse[at] = lse;
@@ -202,7 +207,6 @@ __global__ __launch_bounds__(64 * NW, attn_forward_waves(Elem<DT>::bytes, DP, NW
   const Rows<NW> r(a);
   Softmax<DT, DP, KT> x;
   x.start(a, r);
-  const float slack = 8.0f / a.scale2;
   const bool all = a.D > DP - 16;
   const int64_t k_base = r.w.b * a.k.b + r.w.hk * a.k.h, v_base = r.w.b * a.v.b + r.w.hk * a.v.h;
   const auto k_at = [&](int k) { return k_base + k * a.k.t; };
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(64 * NW, attn_forward_waves(Elem<DT>::bytes, DP, NW
       x.scores(lds, row_lane + cur, all);
       __builtin_amdgcn_s_setprio(0);
       if (k0 + KT > r.sure) x.hide(r.sees - k0 - 4 * r.h);
-      x.soften(a.scale2, slack);
+      x.soften(a.scale2);
       __builtin_amdgcn_s_setprio(1);
       x.mix(lds, col_lane + cur + T::kBytes);
       __builtin_amdgcn_s_setprio(0);
@@ -282,7 +286,6 @@ __global__ __launch_bounds__(128 * kAttnWaves) void attention_wide_kernel(const 
   const Rows<NW> r(a);
   Softmax<DT, DP, KT> x;
   x.start(a, r);
-  const float slack = 8.0f / a.scale2;
   const int64_t k_base = r.w.b * a.k.b + r.w.hk * a.k.h, v_base = r.w.b * a.v.b + r.w.hk * a.v.h;
   const int row_lane = T::row_place(r.lane), col_lane = T::column_place(r.lane);
   const int tiles = r.end > r.begin ? (r.end - r.begin + KT - 1) / KT : 0;
@@ -311,7 +314,7 @@ __global__ __launch_bounds__(128 * kAttnWaves) void attention_wide_kernel(const 
       lds_barrier();
       if (k0 < r.wend) {
         if (k0 + KT > r.sure) x.hide(r.sees - k0 - 4 * r.h);
-        x.soften(a.scale2, slack);
+        x.soften(a.scale2);
       }
       if (t + 2 < tiles) {
         sk.store(lds + b2);

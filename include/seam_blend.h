@@ -481,7 +481,8 @@ int group_norm_forward(const void *x, const int64_t x_stride[2], const int64_t s
  *   stats        what the forward call wrote; gamma, beta as there.
  *   dx           may be dy or x themselves, else shares no element with them.
  *   dgamma, dbeta  device pointers to [C] of weight_dtype, or NULL where not wanted;
- *                written, not added to (zeros without positions).
+ *                written, not added to (zeros without positions); share no memory with
+ *                each other, gamma or beta (checked; SB_EARG).
  * Sums are fp32 by block and 64-bit over blocks, in a fixed order (groups that a block
  * holds: their means in fp32, and of one sample dgamma and dbeta too).
  */

@@ -257,7 +257,8 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int, stats: t
     """Gradient of group_norm: (dx, dgamma, dbeta), from the forward call's input
     and its stats.  weight_grads: whether dgamma and dbeta (of the weights' dtype;
     float32 without any) are formed; by default where a weight or one of them is
-    given, None in their place otherwise.  They are written, not added to.
+    given, None in their place otherwise.  They are written, not added to,
+    and share no memory with each other or a weight.
     ``dx`` may be ``dy`` or ``x``.  ``workspace``: optional uint8 GPU tensor of
     group_norm_workspace_bytes(x, groups) bytes.  The results carry no autograd
     history."""

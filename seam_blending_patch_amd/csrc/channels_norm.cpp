@@ -117,6 +117,18 @@ int check_types(int activation, int dtype, int wdtype, const void *const *weight
   return SB_OK;
 }
 
+// gradients of the weights are written while others are still read: none may share memory
+int check_weights_apart(const void *const *weights, int wdtype, int64_t C) {
+  static const char *const names[4] = {"gamma", "beta", "dgamma", "dbeta"};
+  const uintptr_t bytes = (uintptr_t)C * sb::elem_bytes(wdtype);
+  for (int x = 2; x < 4; ++x)
+    for (int y = 0; y < x; ++y) {
+      const uintptr_t a = (uintptr_t)weights[x], b = (uintptr_t)weights[y];
+      if (a && b && a < b + bytes && b < a + bytes) return failf(SB_EARG, "%s overlaps %s", names[x], names[y]);
+    }
+  return SB_OK;
+}
+
 // floats: partials by chunk and channel (three forward, two backward), then the groups'
 // statistics (or means)
 int64_t part_floats(const sb::ChanArgs &a) { return up(3 * (int64_t)a.N * a.chunks * a.C, 4); }
@@ -180,7 +192,8 @@ extern "C" int group_norm_backward(const void *dy, const int64_t dy_stride[2], c
   sb::ChanArgs a;
   int rc;
   const void *weights[4] = {gamma, beta, dgamma, dbeta};
-  if ((rc = read_shape(shape, groups, dtype, a)) || (rc = check_types(activation, dtype, weight_dtype, weights, 4)))
+  if ((rc = read_shape(shape, groups, dtype, a)) || (rc = check_types(activation, dtype, weight_dtype, weights, 4)) ||
+      (rc = check_weights_apart(weights, weight_dtype, a.C)))
     return rc;
   if (a.N == 0 || a.S == 0) {
     a.N = a.S = a.chunks = 0; // the weights' gradients are zeros

@@ -80,7 +80,7 @@ template <int DT, int DP, int KT> struct Softmax {
     o[i % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, o[i % NB]);
   }
   // (left to the compiler's order: with several waves to a SIMD it is as good for heads
-  // of 128 and better for 64, 8192 tokens of 16 heads 318 us against 367)
+  // of 128 and better for 64, 8192 tokens of 16 heads 320 us against 367)
   // (all: D reaches the last 16 elements of the padded head, else their products are
   // left out: 2049 causal tokens of heads of 80 fp32 269 us, with them 286; 8192 tokens
   // of heads of 48 bf16 326 and 339)
@@ -190,7 +190,7 @@ template <int DT, int DP, int KT> struct Softmax {
 
 // Blocks of one wave (single tokens: bound by memory, 4.3 TB/s over a cache of unlike
 // lengths, 5.0 over one of 4096 keys each) or four, which take turns at the matrix
-// cores as they come.  8192 tokens of 16 heads of 64 bf16: 330 us, 830 TFLOP/s, what
+// cores as they come.  8192 tokens of 16 heads of 64 bf16: 320 us, 860 TFLOP/s, what
 // the vector unit's work on the scores allows there; 2049 causal tokens of 16 heads
 // of 80 fp32: 269 us, 80 TFLOP/s where a library product reaches 139 (a twelfth of it
 // for the values' padding to 96, a third for the unequal tiles).
@@ -253,13 +253,6 @@ __global__ __launch_bounds__(64 * NW, attn_forward_waves(Elem<DT>::bytes, DP, NW
     }
   }
   x.finish(a, r);
-}
-
-// A barrier for LDS alone: what is on its way from memory stays on its way.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Many rows: blocks of 8 waves in two sets, one wave of each to a SIMD, half a

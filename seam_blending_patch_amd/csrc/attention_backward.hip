@@ -495,13 +495,6 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
 // ---------------------------------------------------------------------------
 constexpr int kProductsAhead = 6; // LDS reads this many products before their use
 
-// A barrier for LDS alone: what is on its way from memory stays on its way.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // Waits for all that was requested, in every lane: threads that store no chunk would
 // leave it open to the compiler whether they still wait for theirs, and it would wait
 // again between the next requests (dq of 10140 tokens of 12 heads of 128 bf16: 1.43 ms, 1.77
@@ -910,7 +903,7 @@ template <int DT, int DP> void launch_dq(const AttnArgs &a, int waves, int wave_
   if (waves == 1) hipLaunchKernelGGL((dq_kernel<DT, DP, kFew, kPair>), grid, dim3(64 * kFew), 0, st, a);
   else hipLaunchKernelGGL((dq_kernel<DT, DP, kAttnWaves, kPair>), grid, block, 0, st, a);
 }
-template <int DT, int DP> void launch_dkv(const AttnArgs &a, int, int whole, hipStream_t st) {
+template <int DT, int DP> void launch_dkv(const AttnArgs &a, int whole, hipStream_t st) {
   const dim3 grid(a.blocks), block(64 * kAttnWaves);
   if constexpr (attn_pipelined(Elem<DT>::bytes, DP)) {
     if (whole) {
@@ -921,34 +914,32 @@ template <int DT, int DP> void launch_dkv(const AttnArgs &a, int, int whole, hip
   hipLaunchKernelGGL((dkv_kernel<DT, DP, attn_paired(Elem<DT>::bytes, DP)>), grid, block, 0, st, a);
 }
 
-#define SB_WIDTHS(F)                                                                                                   \
-  template <int DT> hipError_t F(const AttnArgs &a, int waves, int rows, hipStream_t st) {                             \
-    switch (attn_padded(a.D)) {                                                                                        \
-    case 32: F<DT, 32>(a, waves, rows, st); break;                                                                     \
-    case 64: F<DT, 64>(a, waves, rows, st); break;                                                                     \
-    case 96: F<DT, 96>(a, waves, rows, st); break;                                                                     \
-    case 128: F<DT, 128>(a, waves, rows, st); break;                                                                   \
-    case 160: F<DT, 160>(a, waves, rows, st); break;                                                                   \
-    case 192: F<DT, 192>(a, waves, rows, st); break;                                                                   \
-    default: F<DT, 256>(a, waves, rows, st);                                                                           \
-    }                                                                                                                  \
-    return hipGetLastError();                                                                                          \
-  }                                                                                                                    \
-  hipError_t F(const AttnArgs &a, int dtype, int waves, int rows, hipStream_t st) {                                    \
-    if (dtype == DT_F32) return F<DT_F32>(a, waves, rows, st);                                                         \
-    if (dtype == DT_F16) return F<DT_F16>(a, waves, rows, st);                                                         \
-    return F<DT_BF16>(a, waves, rows, st);                                                                             \
+// f(type, padded length) with both as constants
+template <int DT, class F> void of_width(int padded, F f) {
+  constexpr std::integral_constant<int, DT> dt{};
+  switch (padded) {
+  case 32: f(dt, std::integral_constant<int, 32>{}); break;
+  case 64: f(dt, std::integral_constant<int, 64>{}); break;
+  case 96: f(dt, std::integral_constant<int, 96>{}); break;
+  case 128: f(dt, std::integral_constant<int, 128>{}); break;
+  case 160: f(dt, std::integral_constant<int, 160>{}); break;
+  case 192: f(dt, std::integral_constant<int, 192>{}); break;
+  default: f(dt, std::integral_constant<int, 256>{});
   }
-SB_WIDTHS(launch_dq)
-SB_WIDTHS(launch_dkv)
-#undef SB_WIDTHS
+}
+template <class F> hipError_t of_kind(int dtype, int D, F f) {
+  if (dtype == DT_F32) of_width<DT_F32>(attn_padded(D), f);
+  else if (dtype == DT_F16) of_width<DT_F16>(attn_padded(D), f);
+  else of_width<DT_BF16>(attn_padded(D), f);
+  return hipGetLastError();
+}
 
 } // namespace
 } // namespace sb
 
 hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int wave_rows, hipStream_t st) {
-  return sb::launch_dq(a, dtype, waves, wave_rows, st);
+  return sb::of_kind(dtype, a.D, [&](auto dt, auto dp) { sb::launch_dq<dt(), dp()>(a, waves, wave_rows, st); });
 }
 hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, int whole, hipStream_t st) {
-  return sb::launch_dkv(a, dtype, sb::kAttnWaves, whole, st);
+  return sb::of_kind(dtype, a.D, [&](auto dt, auto dp) { sb::launch_dkv<dt(), dp()>(a, whole, st); });
 }

@@ -14,6 +14,7 @@
 //    operand's fragment takes those rows of its tile.
 #pragma once
 
+#include <type_traits>
 #include <utility>
 
 #include "sb_attention.h"
@@ -138,8 +139,9 @@ template <int N, int AHEAD, class Read, class Use> __device__ __forceinline__ vo
 }
 
 // 16 result registers as the operand of the next product.  16-bit: rounded to
-// nearest, so that a product of probabilities (at most 1) or of their gradients
-// with 16-bit values adds half a step of each to a sum whose terms have as much.
+// nearest, so that a product of probabilities (times a power of two) or of their
+// gradients with 16-bit values adds half a step of each to a sum whose terms have as
+// much.
 template <int DT> __device__ __forceinline__ void pack_operand(const float *s, uint32_t *p) {
   if constexpr (DT == DT_F32) {
 #pragma unroll
@@ -251,6 +253,13 @@ template <int DT, int DP, int ROWS, int THREADS> struct RowStage {
     }
   }
 };
+// A barrier for LDS alone: what is on its way from memory stays on its way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // zeros in `bytes` of LDS where heads are shorter than what the kernel is built for
 template <int THREADS> __device__ __forceinline__ void clear_tiles(char *lds, int bytes, bool shorter) {
   if (shorter) {

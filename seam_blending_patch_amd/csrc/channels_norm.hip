@@ -250,7 +250,7 @@ __device__ __forceinline__ float logistic(float z) {
 }
 
 // What a thread keeps of its channels: h = ((x - K) - m) r, z = h gamma + beta.
-template <int DT, int WT, Cover C> struct Channels {
+template <int DT, int WT> struct Channels {
   static constexpr int V = kVec<DT>;
   float K[V], m[V], r[V], gamma[V], beta[V];
   __device__ __forceinline__ void load(const ChanArgs &a, int n, int e) {
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kChanThreads) void apply_kernel(const ChanArgs a) {
   const Place p = place_of(a);
   if (!p.on) return;
   const int e = p.col * V;
-  Channels<DT, WT, C> ch;
+  Channels<DT, WT> ch;
   ch.load(a, p.n, e);
   const int turns = turns_of(p.s1 - p.s0, p.r, a.RB);
   int64_t in = p.n * a.sx.n + (int64_t)(p.s0 + p.r) * a.sx.s, to = p.n * a.sout.n + (int64_t)(p.s0 + p.r) * a.sout.s;
@@ -301,8 +301,8 @@ __global__ __launch_bounds__(kChanThreads) void apply_kernel(const ChanArgs a) {
 }
 
 // g = dy act'(z), h: of one vector
-template <int DT, int WT, Cover C, bool SILU>
-__device__ __forceinline__ void gradient_of(const Channels<DT, WT, C> &ch, const Vec<16> &x, const Vec<16> &dy,
+template <int DT, int WT, bool SILU>
+__device__ __forceinline__ void gradient_of(const Channels<DT, WT> &ch, const Vec<16> &x, const Vec<16> &dy,
                                             float *g, float *h) {
   constexpr int V = kVec<DT>;
   unpack<DT, 16>(x, h);
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(kChanThreads) void sums_kernel(const ChanArgs a) {
 #pragma unroll
   for (int k = 0; k < V; ++k) sg[k] = sh[k] = 0.0f;
   if (p.on) {
-    Channels<DT, WT, C> ch;
+    Channels<DT, WT> ch;
     ch.load(a, p.n, e);
     const int turns = turns_of(p.s1 - p.s0, p.r, a.RB);
     int64_t ix = p.n * a.sx.n + (int64_t)(p.s0 + p.r) * a.sx.s, iy = p.n * a.sdy.n + (int64_t)(p.s0 + p.r) * a.sdy.s;
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(kChanThreads) void sums_kernel(const ChanArgs a) {
           settle_row<DT, C>(v[j], e, a.C);
           settle_row<DT, C>(w[j], e, a.C);
           float g[V], h[V];
-          gradient_of<DT, WT, C, SILU>(ch, v[j], w[j], g, h);
+          gradient_of<DT, WT, SILU>(ch, v[j], w[j], g, h);
 #pragma unroll
           for (int k = 0; k < V; ++k) {
             sg[k] += g[k];
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(kChanThreads) void gradient_kernel(const ChanArgs a
   const Place p = place_of(a);
   if (!p.on) return;
   const int e = p.col * V;
-  Channels<DT, WT, C> ch;
+  Channels<DT, WT> ch;
   ch.load(a, p.n, e);
   float mg[V], mh[V];
 #pragma unroll
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kChanThreads) void gradient_kernel(const ChanArgs a
         settle_row<DT, C>(v[j], e, a.C);
         settle_row<DT, C>(w[j], e, a.C);
         float g[V], h[V];
-        gradient_of<DT, WT, C, SILU>(ch, v[j], w[j], g, h);
+        gradient_of<DT, WT, SILU>(ch, v[j], w[j], g, h);
 #pragma unroll
         for (int k = 0; k < V; ++k)
           g[k] = ch.r[k] * (__builtin_fmaf(g[k], ch.gamma[k], -mg[k]) - h[k] * mh[k]);
@@ -633,7 +633,7 @@ __global__ __launch_bounds__(kHeldBackThreads) void held_gradient_kernel(const C
     v[j] = load_part<DT>(a.x, p.n * a.sx.n + at * a.sx.s + e, V);
     w[j] = load_part<DT>(a.dy, p.n * a.sdy.n + at * a.sdy.s + e, V);
   }
-  Channels<DT, WT, WHOLE> ch;
+  Channels<DT, WT> ch;
   ch.load(a, p.n, e);
   int group[V];
 #pragma unroll
@@ -646,7 +646,7 @@ __global__ __launch_bounds__(kHeldBackThreads) void held_gradient_kernel(const C
   for (int j = 0; j < NV; ++j) {
     if (j >= turns) continue;
     float g[V], h[V];
-    gradient_of<DT, WT, WHOLE, SILU>(ch, v[j], w[j], g, h);
+    gradient_of<DT, WT, SILU>(ch, v[j], w[j], g, h);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       by[0][k] += g[k];
@@ -676,7 +676,7 @@ __global__ __launch_bounds__(kHeldBackThreads) void held_gradient_kernel(const C
   for (int j = 0; j < NV; ++j) {
     if (j >= turns) continue;
     float g[V], h[V];
-    gradient_of<DT, WT, WHOLE, SILU>(ch, v[j], w[j], g, h);
+    gradient_of<DT, WT, SILU>(ch, v[j], w[j], g, h);
 #pragma unroll
     for (int k = 0; k < V; ++k) g[k] = ch.r[k] * (__builtin_fmaf(g[k], ch.gamma[k], -mg[k]) - h[k] * mh[k]);
     store_part<DT>(a.out, to + (int64_t)j * p.RB * a.sout.s, V, pack<DT, 16>(g));

@@ -112,14 +112,12 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // into more, for their longest tiles are twice the mean).
 struct Plan {
   int waves;
-  int wave_rows; // of dq's pipelined kernel (0: not that one)
   int64_t tiles, splits, span;
 };
 
 Plan cut(int64_t units, int64_t own, int64_t per_block, int64_t along, int waves, int64_t want, int64_t least) {
   Plan p;
   p.waves = waves;
-  p.wave_rows = 0;
   p.tiles = (own + per_block - 1) / per_block;
   const int64_t blocks = std::max<int64_t>(1, units * p.tiles);
   const int64_t most = std::min<int64_t>(kMaxSplits, (along + least - 1) / least);
@@ -137,24 +135,13 @@ Plan plan_rows(const sb::AttnArgs &a, int dtype, bool forward, bool causal, bool
   const bool whole = whole_chunks(a, dtype);
   // Single tokens: a wave to a block, as many splits as keep the memory busy; twice
   // as many where lengths leave some of them empty (8 tokens over 16384, 14044, ... 0
-  // keys, 32 heads of 128 in 8 groups bf16 61.9 us with 16 waves a CU, 69.0 with 8;
+  // keys, 32 heads of 128 in 8 groups bf16, the same inputs again, 61.9 us with 16 waves
+  // a CU, 69.0 with 8 (72 with 16 where inputs change and none is in the caches);
   // 32 over 4096 keys each 118 and 108).
   if (a.rows <= 32) return cut(units, a.rows, 32, a.Lk, 1, (lengths ? 16 : 8) * cus, 128);
   if (forward && whole && sb::attn_wide(eb, padded) && units * ((a.rows + 32 * wide - 1) / (32 * wide)) >= 2 * cus)
     return cut(units, a.rows, 32 * wide, a.Lk, wide, 1, a.Lk + 1);
-  Plan p;
-  if (!forward && whole && sb::attn_pipelined(eb, padded)) {
-    const int64_t rows = 64 * sb::kAttnWaves;
-    if (sb::attn_columns(padded) > 1 && 2 * units * ((a.rows + rows - 1) / rows) >= 3 * cus) {
-      p = cut(units, a.rows, rows, a.Lk, sb::kAttnWaves, 1, a.Lk + 1);
-      p.wave_rows = 64;
-      return p;
-    }
-    p = cut(units, a.rows, 32 * sb::kAttnWaves, a.Lk, sb::kAttnWaves, want, 512);
-    p.wave_rows = 32;
-    return p;
-  }
-  const bool paired = !forward && sb::attn_dq_paired(eb, padded);
+  const bool paired = !forward && !(whole && sb::attn_pipelined(eb, padded)) && sb::attn_dq_paired(eb, padded);
   return cut(units, a.rows, 32 * sb::kAttnWaves / (paired ? 2 : 1), a.Lk, sb::kAttnWaves, want, 512);
 }
 
@@ -349,7 +336,7 @@ extern "C" int attention_backward(const void *dout, const int64_t dout_stride[3]
     a.part = p.splits > 1 ? part : nullptr;
     a.part_mean = part + rows_part(a, p);
     a.part_left = a.part_mean + rows_part_mean(a, p, dtype);
-    e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, p.wave_rows, st); });
+    e = over_units(a, p, [&](const sb::AttnArgs &b) { return sb_launch_attention_dq(b, dtype, p.waves, whole_chunks(a, dtype), st); });
     a.splits = (int32_t)p.splits;
     if (e == hipSuccess && p.splits > 1)
       e = dtype == SB_F32 ? sb_launch_attention_sum(a, &a.dq, 1, a.rows, a.group, dtype, st)

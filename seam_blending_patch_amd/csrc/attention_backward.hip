@@ -81,8 +81,8 @@ __device__ __forceinline__ int read_peak(const AttnArgs &a, const Work &w, int b
 // takes both out along m, and delta + the sum of dS before its rounding is the exact
 // delta that dk's kernel needs.  The price is a product more, of the fragments that dS
 // takes, and as many registers for m as for dq: 10140 tokens of 12 heads of 128 bf16 dq
-// 1.38 ms, 0.93 without (when two columns of rows to a wave had room); 8192 of 16 heads of
-// 64 0.64 and 0.54; a pass of its own for delta would form two products again.
+// 1.38 ms, 0.93 without (when two columns of 32 rows to a wave had room); 8192 of 16 heads of
+// 64 0.61 and 0.54; a pass of its own for delta would form two products again.
 template <int DT> constexpr bool kMeanOf = DT != DT_F32;
 template <int DT> struct Left {
   float rounded, exact;
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void dkv_kernel(const AttnArgs a) 
 // with one the compiler carries the sums from one kind of register to the other and
 // back (dk and dv 2.71 ms with the branches that spare a wave tiles it does not see,
 // 1.86 without).  10140 tokens of 12 heads of 128 bf16: dq 1.38 ms (910 TFLOP/s on its four
-// products), dk and dv 1.41 ms (900); 8192 tokens of 16 heads of 64 0.64 and 0.63 ms.
+// products), dk and dv 1.41 ms (900); 8192 tokens of 16 heads of 64 0.61 and 0.62 ms.
 // Reading 12 products ahead in place of 6 loses (heads of 64 1.61 ms against 1.22 in all,
 // with three products for dq).
 // ---------------------------------------------------------------------------
@@ -501,10 +501,10 @@ constexpr int kProductsAhead = 6; // LDS reads this many products before their u
 // without this).
 __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); } // (vmcnt 0, no other counter)
 
-// dq: a wave has R columns of 32 rows.
-template <int DT, int DP, int NW, int R>
-__global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a) {
-  constexpr int kThreads = 64 * NW, KT = 32, ROWS = 32 * R;
+// dq: a wave has 32 rows.  (Two columns of them to a wave, where there are registers for
+// that: 8192 tokens of 16 heads of 64 bf16 1229 us in all, so 1208.)
+template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dq_pipelined_kernel(const AttnArgs a) {
+  constexpr int kThreads = 64 * kAttnWaves, KT = 32;
   using T = Tile<DT, DP, KT>;
   using St = RowStage<DT, DP, KT, kThreads>;
   constexpr int NB = DP / 32, NF = T::kFrags;
@@ -514,64 +514,55 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, n = lane & 31;
   const int klen = length_of(a.k_len, w.b, a.Lk), qlen = length_of(a.q_len, w.b, a.Lq);
   const int off = klen - qlen, live_rows = qlen * a.group;
-  const int r0 = w.tile * ROWS * NW, wr0 = r0 + wave * ROWS;
+  const int r0 = w.tile * 32 * kAttnWaves, wr0 = r0 + wave * 32, row = wr0 + n;
+  const bool live = row < live_rows;
   const auto seen = [&](int r) {
     return a.causal ? min(max((int)fdiv((uint32_t)r, a.div_group) + off + 1, 0), klen) : klen;
   };
+  const int sees = live ? seen(row) : klen;
   const int sure = seen(min(wr0, max(live_rows - 1, 0)));
-  const int last = min(r0 + ROWS * NW, live_rows) - 1;
+  const int last = min(r0 + 32 * kAttnWaves, live_rows) - 1;
   const int begin = w.split * a.span;
   const int end = last < r0 ? 0 : min(seen(last), begin + a.span);
 
-  u32x4 qf[R][NF], gf[R][NF];
-  float delta[R], lse2[R], lifted[R];
-  Lift lift[R];
-  int sees[R];
-#pragma unroll
-  for (int c = 0; c < R; ++c) {
-    const int row = wr0 + 32 * c + n;
-    const bool live = row < live_rows;
-    sees[c] = live ? seen(row) : klen;
+  u32x4 qf[NF], gf[NF];
+  float delta = 0.0f, square = 0.0f, out_square = 0.0f, lse2 = kInf; // (lse2: as in dq_kernel)
+  {
     const int64_t at = live ? row_at(a.q, a, w.b, w.hk, row) : 0, to = live ? row_at(a.out, a, w.b, w.hk, row) : 0,
                   gt = live ? row_at(a.dout, a, w.b, w.hk, row) : 0;
-    float d = 0.0f, square = 0.0f, out_square = 0.0f;
 #pragma unroll
     for (int u = 0; u < NF; ++u) {
-      qf[c][u] = load_chunk<DT>(a.q.p, at, 2 * u + h, a.D, live);
-      gf[c][u] = load_chunk<DT>(a.dout.p, gt, 2 * u + h, a.D, live);
+      qf[u] = load_chunk<DT>(a.q.p, at, 2 * u + h, a.D, live);
+      gf[u] = load_chunk<DT>(a.dout.p, gt, 2 * u + h, a.D, live);
       const u32x4 of = load_chunk<DT>(a.out.p, to, 2 * u + h, a.D, live);
       float f[T::V], g[T::V];
       unpack<DT, 16>(Vec<16>{of[0], of[1], of[2], of[3]}, f);
-      unpack<DT, 16>(Vec<16>{gf[c][u][0], gf[c][u][1], gf[c][u][2], gf[c][u][3]}, g);
+      unpack<DT, 16>(Vec<16>{gf[u][0], gf[u][1], gf[u][2], gf[u][3]}, g);
 #pragma unroll
       for (int i = 0; i < T::V; ++i) {
-        d = __builtin_fmaf(f[i], g[i], d);
+        delta = __builtin_fmaf(f[i], g[i], delta);
         if constexpr (kLifts<DT>) {
           square = __builtin_fmaf(g[i], g[i], square);
           out_square = __builtin_fmaf(f[i], f[i], out_square);
         }
       }
     }
-    delta[c] = half_sum(d);
+    delta = half_sum(delta);
     if constexpr (kLifts<DT>) {
       square = Lift::size(half_sum(square), half_sum(out_square));
-      store_peak(a, w, wr0 + 32 * c, lane, square);
+      store_peak(a, w, wr0, lane, square);
     }
-    lift[c] = Lift::of<DT>(Lift::power(square));
-    lifted[c] = delta[c] * lift[c].by;
-    lse2[c] = kInf; // (a row that sees no key, or is none: its probabilities are exp2(-inf))
     if (live) {
-      const int64_t st = stat_at(a, w.b, w.hk, row);
-      const float lse = a.lse[st];
-      if (lse != -kInf) lse2[c] = lse * kLog2e - kLiftP<DT>;
+      const float lse = a.lse[stat_at(a, w.b, w.hk, row)];
+      if (lse != -kInf) lse2 = lse * kLog2e - kLiftP<DT>;
     }
   }
-  f32x16 dq[R][NB], mean[R][NB];
-  Left<DT> left[R] = {};
+  const Lift lift = Lift::of<DT>(Lift::power(square));
+  const float lifted = delta * lift.by;
+  f32x16 dq[NB], mean[NB];
+  Left<DT> left = {};
 #pragma unroll
-  for (int c = 0; c < R; ++c)
-#pragma unroll
-    for (int db = 0; db < NB; ++db) dq[c][db] = mean[c][db] = f32x16{0};
+  for (int db = 0; db < NB; ++db) dq[db] = mean[db] = f32x16{0};
 
   const int row_lane = T::row_place(lane), col_lane = T::column_place(lane);
   const int tiles = end > begin ? (end - begin + KT - 1) / KT : 0;
@@ -595,19 +586,14 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
       sv.load(begin + 2 * KT, klen);
     }
     __syncthreads();
-    f32x16 s[R], dp[R], s1[R], dp1[R];
-    // steps: for each fragment u the keys' and the values', times R columns
+    f32x16 s = {0}, dp = {0}, s1, dp1;
+    // steps: for each fragment u the keys' and the values'
     const auto read = [&](int buffer, int i) {
       return T::row_fragment(lds, row_lane + buffer + (i & 1) * T::kBytes, 0, i >> 1);
     };
-#pragma unroll
-    for (int c = 0; c < R; ++c) s[c] = dp[c] = f32x16{0};
     in_order<2 * NF, kProductsAhead>([&](int i) { return read(0, i); }, [&](int i, u32x4 f) {
-#pragma unroll
-      for (int c = 0; c < R; ++c) {
-        if (i & 1) dp[c] = mma<DT>(f, gf[c][i >> 1], dp[c]);
-        else s[c] = mma<DT>(f, qf[c][i >> 1], s[c]);
-      }
+      if (i & 1) dp = mma<DT>(f, gf[i >> 1], dp);
+      else s = mma<DT>(f, qf[i >> 1], s);
     });
     int b0 = 0, b1 = 2 * T::kBytes, b2 = 4 * T::kBytes;
     for (int t = 0, k0 = begin; t < tiles; ++t, k0 += KT) {
@@ -621,11 +607,10 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
         }
       }
       {
-        float p[R][16], ds[R][16];
-#pragma unroll
-        for (int c = 0; c < R; ++c) s1[c] = dp1[c] = f32x16{0};
+        float p[16], ds[16];
+        s1 = dp1 = f32x16{0};
         // (behind the last tile: scores of what the buffer holds, not used)
-        uint32_t pp[R][8], pd[R][8];
+        uint32_t pp[8], pd[8];
         in_order<2 * NF + 2 * NB, kProductsAhead>(
             [&](int i) {
               const int j = i - 2 * NF;
@@ -633,55 +618,49 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
             },
             [&](int i, u32x4 f) {
               const int j = i - 2 * NF;
+              if (j >= 0) {
+                const uint32_t *q = pd + 4 * (j / NB), *m = pp + 4 * (j / NB);
+                dq[j % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, dq[j % NB]);
+                mean[j % NB] = mma<DT>(f, u32x4{m[0], m[1], m[2], m[3]}, mean[j % NB]);
+                // (beside the products: the sums, and the second half's packing)
 #pragma unroll
-              for (int c = 0; c < R; ++c) {
-                if (j >= 0) {
-                  const uint32_t *q = pd[c] + 4 * (j / NB), *m = pp[c] + 4 * (j / NB);
-                  dq[c][j % NB] = mma<DT>(f, u32x4{q[0], q[1], q[2], q[3]}, dq[c][j % NB]);
-                  mean[c][j % NB] = mma<DT>(f, u32x4{m[0], m[1], m[2], m[3]}, mean[c][j % NB]);
-                  // (beside the products: the sums, and the second half's packing)
+                for (int e = j * 8 / NB; e < (j + 1) * 8 / NB; ++e) left.add(ds[e]);
+                if (j == NB - 1) {
 #pragma unroll
-                  for (int e = j * 8 / NB; e < (j + 1) * 8 / NB; ++e) left[c].add(ds[c][e]);
-                  if (j == NB - 1) {
-#pragma unroll
-                    for (int e = 4; e < 8; ++e) {
-                      pp[c][e] = pack_pair<DT>(p[c] + 2 * e);
-                      pd[c][e] = pack_pair<DT>(ds[c] + 2 * e);
-                    }
+                  for (int e = 4; e < 8; ++e) {
+                    pp[e] = pack_pair<DT>(p + 2 * e);
+                    pd[e] = pack_pair<DT>(ds + 2 * e);
                   }
-#pragma unroll
-                  for (int e = j * 4 / NB; e < (j + 1) * 4 / NB; ++e) left[c].add(pd[c][e]);
-                  continue;
                 }
-                if (i & 1) dp1[c] = mma<DT>(f, gf[c][i >> 1], dp1[c]);
-                else s1[c] = mma<DT>(f, qf[c][i >> 1], s1[c]);
 #pragma unroll
-                for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e) {
-                  p[c][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[c][e], a.scale2, -lse2[c]));
-                  ds[c][e] = gradient_of<DT>(p[c][e], dp[c][e], lifted[c], lift[c].by);
+                for (int e = j * 4 / NB; e < (j + 1) * 4 / NB; ++e) left.add(pd[e]);
+                return;
+              }
+              if (i & 1) dp1 = mma<DT>(f, gf[i >> 1], dp1);
+              else s1 = mma<DT>(f, qf[i >> 1], s1);
+#pragma unroll
+              for (int e = i * 16 / (2 * NF); e < (i + 1) * 16 / (2 * NF); ++e) {
+                p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.scale2, -lse2));
+                ds[e] = gradient_of<DT>(p[e], dp[e], lifted, lift.by);
+              }
+              if (j == -1) {
+                if (k0 + KT > sure) {
+                  const int keys = sees - k0 - 4 * h;
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) {
+                    p[x] = 8 * (x >> 2) + (x & 3) < keys ? p[x] : 0.0f;
+                    ds[x] = 8 * (x >> 2) + (x & 3) < keys ? ds[x] : 0.0f;
+                  }
                 }
-                if (j == -1) {
-                  if (k0 + KT > sure) {
-                    const int keys = sees[c] - k0 - 4 * h;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                      p[c][x] = 8 * (x >> 2) + (x & 3) < keys ? p[c][x] : 0.0f;
-                      ds[c][x] = 8 * (x >> 2) + (x & 3) < keys ? ds[c][x] : 0.0f;
-                    }
-                  }
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    pp[c][e] = pack_pair<DT>(p[c] + 2 * e);
-                    pd[c][e] = pack_pair<DT>(ds[c] + 2 * e);
-                  }
+                for (int e = 0; e < 4; ++e) {
+                  pp[e] = pack_pair<DT>(p + 2 * e);
+                  pd[e] = pack_pair<DT>(ds + 2 * e);
                 }
               }
             });
-#pragma unroll
-        for (int c = 0; c < R; ++c) {
-          s[c] = s1[c];
-          dp[c] = dp1[c];
-        }
+        s = s1;
+        dp = dp1;
       }
       lds_barrier();
       const int b = b0;
@@ -691,11 +670,7 @@ __global__ __launch_bounds__(64 * NW) void dq_pipelined_kernel(const AttnArgs a)
     }
   }
 
-#pragma unroll
-  for (int c = 0; c < R; ++c) {
-    const int row = wr0 + 32 * c + n;
-    store_dq<DT, NB>(a, w, row, h, 0, row < live_rows, delta[c], lift[c].undo, left[c], dq[c], mean[c]);
-  }
+  store_dq<DT, NB>(a, w, row, h, 0, live, delta, lift.undo, left, dq, mean);
 }
 
 // dk and dv: a wave has 32 keys.
@@ -882,19 +857,12 @@ template <int DT, int DP> __global__ __launch_bounds__(64 * kAttnWaves) void dkv
   }
 }
 
-// wave_rows: 32 or 64 (where attn_columns allows it) rows of a wave, for whole
-// chunks; 0: the kernels that take any head
-template <int DT, int DP> void launch_dq(const AttnArgs &a, int waves, int wave_rows, hipStream_t st) {
+// whole: heads of whole 16-byte chunks, which some kernels want
+template <int DT, int DP> void launch_dq(const AttnArgs &a, int waves, int whole, hipStream_t st) {
   const dim3 grid(a.blocks), block(64 * kAttnWaves);
   if constexpr (attn_pipelined(Elem<DT>::bytes, DP)) {
-    if constexpr (attn_columns(DP) > 1) {
-      if (wave_rows == 64) {
-        hipLaunchKernelGGL((dq_pipelined_kernel<DT, DP, kAttnWaves, 2>), grid, block, 0, st, a);
-        return;
-      }
-    }
-    if (wave_rows) {
-      hipLaunchKernelGGL((dq_pipelined_kernel<DT, DP, kAttnWaves, 1>), grid, block, 0, st, a);
+    if (whole && waves > 1) {
+      hipLaunchKernelGGL((dq_pipelined_kernel<DT, DP>), grid, block, 0, st, a);
       return;
     }
   }
@@ -937,8 +905,8 @@ template <class F> hipError_t of_kind(int dtype, int D, F f) {
 } // namespace
 } // namespace sb
 
-hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int wave_rows, hipStream_t st) {
-  return sb::of_kind(dtype, a.D, [&](auto dt, auto dp) { sb::launch_dq<dt(), dp()>(a, waves, wave_rows, st); });
+hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int whole, hipStream_t st) {
+  return sb::of_kind(dtype, a.D, [&](auto dt, auto dp) { sb::launch_dq<dt(), dp()>(a, waves, whole, st); });
 }
 hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, int whole, hipStream_t st) {
   return sb::of_kind(dtype, a.D, [&](auto dt, auto dp) { sb::launch_dkv<dt(), dp()>(a, whole, st); });

@@ -63,9 +63,6 @@ __host__ __device__ constexpr bool attn_pipelined(int elem_bytes, int padded) {
   return elem_bytes == 2 && padded <= 192;
 }
 
-// columns of 32 rows of a wave of those for dq, at most (their registers)
-__host__ __device__ constexpr int attn_columns(int padded) { return padded <= 64 ? 2 : 1; }
-
 // keys of a block of the key gradients: 32 a wave, or a pair of waves where a
 // head's two halves go to two of them
 __host__ __device__ constexpr bool attn_paired(int elem_bytes, int padded) { return padded * elem_bytes > (elem_bytes == 2 ? 384 : 640); }
@@ -77,9 +74,9 @@ __host__ __device__ constexpr bool attn_dq_paired(int elem_bytes, int padded) { 
 } // namespace sb
 
 // waves: 1, kAttnWaves or (forward, attn_wide) twice that, each with 32 rows of a
-// tile; wave_rows, whole: as launch_dq and launch_dkv say
+// tile; whole: heads of whole 16-byte chunks
 hipError_t sb_launch_attention(const sb::AttnArgs &a, int dtype, int waves, hipStream_t st);
-hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int wave_rows, hipStream_t st);
+hipError_t sb_launch_attention_dq(const sb::AttnArgs &a, int dtype, int waves, int whole, hipStream_t st);
 hipError_t sb_launch_attention_dkv(const sb::AttnArgs &a, int dtype, int whole, hipStream_t st);
 // joins the splits of the forward pass
 hipError_t sb_launch_attention_join(const sb::AttnArgs &a, int dtype, hipStream_t st);

@@ -189,7 +189,7 @@ template <int DT, int DP, int KT> struct Softmax {
 };
 
 // Blocks of one wave (single tokens: bound by memory, 4.3 TB/s over a cache of unlike
-// lengths, 5.0 over one of 4096 keys each) or four, which take turns at the matrix
+// lengths in the caches, 5.0 over one of 4096 keys each) or four, which take turns at the matrix
 // cores as they come.  8192 tokens of 16 heads of 64 bf16: 320 us, 860 TFLOP/s, what
 // the vector unit's work on the scores allows there; 2049 causal tokens of 16 heads
 // of 80 fp32: 269 us, 80 TFLOP/s where a library product reaches 139 (a twelfth of it
@@ -263,11 +263,12 @@ __global__ __launch_bounds__(64 * NW, attn_forward_waves(Elem<DT>::bytes, DP, NW
 // in the next it softens them, in the one after that it multiplies its values.
 // Keys t + 2 and values t + 1 are stored while tile t is softened, in one of three
 // buffers: its last reader was done two phases before, its first comes two after.
-// 20280 tokens of 12 heads of 128 bf16: 2.6 ms, 970 TFLOP/s (2.8 ms in blocks of four
+// 20280 tokens of 12 heads of 128 bf16: 2.65 ms, 940 TFLOP/s (2.8 ms in blocks of four
 // waves; a library product reaches 1220).  The bound is LDS: a phase's fragments are
 // 64 KiB by rows and 64 KiB by columns for four waves, at 115 and 82 bytes a clock
 // 1370 clocks beside 1024 of products; without the softmax the rest takes 2.1 ms.
-// Heads of 64 have half the products to a softmax and gain nothing (431 us against 320).
+// Heads of 64 have half the products to a softmax and gain nothing (8192 tokens of 16
+// 431 us against 320).
 template <int DT, int DP>
 __global__ __launch_bounds__(128 * kAttnWaves) void attention_wide_kernel(const AttnArgs a) {
   constexpr int NW = 2 * kAttnWaves, kThreads = 64 * NW;

@@ -4,11 +4,10 @@
 // A thread keeps one vector of channels and goes along the positions: whatever the
 // group's channels, a block reads whole runs of a position's channels, and sums
 // stay in registers by channel until the block's end.  Bound by memory: two samples
-// of 512 x 512 x 256 fp16 136 to 146 us (kernels: sums 44, merge 6, result 92 us: 6.1 and
-// 5.8 TB/s, part of both from the caches).  The gradient of 256 x 256 x 512 bf16 69 to 81 us
-// (36, 7 and 37 us, 3.7 and 5.4 TB/s: its sums are bound by two blocks to a CU and their
-// vector work as much as by memory).  A second reading of x (and dy) is the price of groups
-// that no block holds.
+// of 512 x 512 x 256 fp16 145 us a call (kernels under the profiler: sums 53, merge 6, result
+// 100 us: 5.1 and 5.4 TB/s).  The gradient of 256 x 256 x 512 bf16 81 us (37, 7 and 39 us,
+// 3.6 and 5.2 TB/s: two blocks to a CU do not hide the sums' vector work).  A second
+// reading of x (and dy) is the price of groups that no block holds.
 #include <type_traits>
 
 #include "sb_channels.h"

@@ -47,8 +47,10 @@ template <int DT> __device__ __forceinline__ float gradient_of(float p, float dp
   if constexpr (kLifts<DT>) return p * __builtin_fmaf(dp, by, -delta);
   else return p * (dp - delta);
 }
-// the largest size of the 32 rows of a wave's column, for dk's kernel
+// the largest size of a wave's 32 rows, for dk's kernel (an infinite one would say nothing
+// of the others, and leaves nothing to lift in what it reaches)
 __device__ __forceinline__ void store_peak(const AttnArgs &a, const Work &w, int row0, int lane, float square) {
+  square = square < kInf ? square : 0.0f;
 #pragma unroll
   for (int k = 16; k; k >>= 1) square = fmaxf(square, __shfl_xor(square, k));
   if (lane == 0 && w.split == 0 && row0 < a.rows) a.peak[(int64_t)w.unit * ((a.rows + 31) / 32) + row0 / 32] = square;

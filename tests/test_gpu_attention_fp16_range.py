@@ -105,3 +105,42 @@ def test_small_probabilities(sb, d):
     tol = ((off + 4 * U * np.abs(ls)[:, None] + 2.0 ** -11 + 8 * U) * p + 2.0 ** -39).T @ np.abs(f64(g)[0, :, 0])
     dv = sb.attention_backward(*(t.cuda() for t in (g, q, k, v, out, lse)))[2]
     assert_near(dv[0, :, 0], want, tol, "dv")
+
+
+@pytest.mark.parametrize("d", [64, 161, 256])
+def test_a_row_of_infinities_and_large_ones(sb, d):
+    """causal order: keys behind an infinite row's last one have the gradients of the other
+    rows, whose dS passes 65504"""
+    q, k, v, g = draw(6, 1, 60, 60, 1, 1, d, q=0.01, k=0.01, v=8.0, g=2e3)
+    g[0, 3] = float("inf")
+    (out, lse), _ = ref.forward(q, k, v, d ** -0.5, True)
+    out, lse = torch.from_numpy(out).half(), torch.from_numpy(lse).float()
+    got = sb.attention_backward(*(t.cuda() for t in (g, q, k, v, out, lse)), causal=True)
+    clean = g.clone()
+    clean[0, 3] = 0.0
+    (dq, dk), (tq, tk) = backward(clean, q, k, v, out, d ** -0.5, True, tiny=lifts(clean, out, 1))
+    rows = [i for i in range(60) if i != 3]
+    assert not torch.isfinite(got[0][0, 3]).any() and not torch.isfinite(got[1][0, :4]).all()
+    assert_near(got[0][:, rows], dq[:, rows], tq[:, rows], "dq")
+    assert_near(got[1][:, 4:], dk[:, 4:], tk[:, 4:], "dk")
+
+
+@pytest.mark.parametrize("size", [(3, 2, 1500, 4, 2, 64), (1, 200, 150, 4, 2, 128), (1, 900, 30, 2, 2, 33)], ids=str)
+def test_a_captured_gradient_follows_the_scale(sb, size):
+    """the powers of two are formed when the kernels run: a graph replayed on gradients of
+    another scale gives what a call does"""
+    scale = size[-1] ** -0.5
+    q, k, v, g = (t.cuda() for t in draw(7, *size))
+    out, lse = sb.attention(q, k, v, return_lse=True)
+    back = sb.AttentionBackward(g, q, k, v, out, lse)
+    back()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        back()
+    for turn, by in enumerate((1.0, 1e-5, 1e3, 1e-2)):
+        g.copy_(draw(8 + turn, *size, g=by)[3])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(back.out, sb.attention_backward(g, q, k, v, out, lse, scale=scale)):
+            assert torch.equal(a, b)
